@@ -13,6 +13,10 @@ _LAZY = {
     "pipeline": ("pipeline", None),
     "RecalibratedExpertBackward": ("pipeline", "RecalibratedExpertBackward"),
     "dtype_code": ("pipeline", "dtype_code"),
+    "layer": ("layer", None),
+    "Router": ("layer", "Router"),
+    "AddRMSNorm": ("layer", "AddRMSNorm"),
+    "AdamW": ("layer", "AdamW"),
 }
 
 

@@ -1,0 +1,334 @@
+"""What stands around the expert passes in a training step, on one GPU.
+
+``Router``      logits -> experts, weights, counts, balance loss and z-loss; and back
+``AddRMSNorm``  residual addition, RMS norm, 8-bit rows with scales; and back
+``AdamW``       one optimizer step over many tensors, moments in 32 bits or in 8
+
+Each owns its output buffers and workspace (allocated once through PyTorch,
+reused every call: a call overwrites what the one before it returned) and
+issues the C-ABI calls of liblrm on the stream it is given, else on torch's
+current one. Inputs are checked for type, shape, layout and device on the host;
+a mismatch raises ValueError before anything is launched. A buffer that another
+stream wrote or will read is the caller's to order, as for every call here.
+"""
+
+from __future__ import annotations
+
+import torch
+
+from . import lrm
+from .pipeline import _TORCH_DTYPE, dtype_code
+
+
+def _need(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device):
+    """A contiguous device tensor of this shape and type."""
+    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous() \
+            or t.device != device:
+        raise ValueError(f"{name}: a contiguous {dtype} tensor {shape} on {device} is needed, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t
+
+
+def _need_rows(t, name: str, cols: int, dtype: torch.dtype, device: torch.device,
+               rows: int) -> int:
+    """A device matrix whose rows are contiguous; returns its row stride."""
+    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols \
+            or (cols > 1 and t.stride(1) != 1) or t.device != device:
+        raise ValueError(f"{name}: a {dtype} tensor ({rows}, {cols}) with contiguous rows on "
+                         f"{device} is needed, got {t.dtype} {tuple(t.shape)} strides "
+                         f"{t.stride()} on {t.device}")
+    stride = t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    if stride < cols:
+        raise ValueError(f"{name}: rows overlap (stride {stride} for {cols} columns)")
+    return stride
+
+
+def _device(device) -> torch.device:
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError(f"a CUDA device is needed, got {dev}")
+    return torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
+
+
+class Router:
+    """Top-K router of T tokens over E experts.
+
+    After ``route``: ``topk_idx`` [T, K] int32 and ``alpha`` [T, K] float32 (what
+    ``RecalibratedExpertBackward`` takes); with statistics also ``counts`` [E]
+    int32, ``prob_sum`` [E] and ``loss`` [2] = (balance loss, z-loss). After
+    ``backward``: ``dlogits`` [T, E] in the logits' type. See lrm_route and
+    lrm_route_bwd in include/lrm.h for the definitions.
+    """
+
+    def __init__(self, T: int, E: int, K: int, dtype: str = "f32", renorm: bool = False,
+                 balance_coef: float = 0.01, z_coef: float = 0.0,
+                 device: str | torch.device = "cuda"):
+        self.T, self.E, self.K = T, E, K
+        self.tdtype = _TORCH_DTYPE[dtype_code(dtype)]
+        self.desc = lrm.lrm_router(T, E, K, dtype_code(dtype), E, int(renorm), balance_coef,
+                                   z_coef)
+        self.ws_bytes = lrm.lrm_router_workspace_bytes(self.desc)
+        if self.ws_bytes == 0:
+            raise ValueError(f"unsupported router shape T={T} E={E} K={K}: 1 <= K <= min(E, 32), "
+                             "E <= 1024 and T*K < 2^31 are needed")
+        self.device = dev = _device(device)
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+        self.ws = empty(self.ws_bytes, dtype=torch.uint8)
+        self.topk_idx, self.alpha = empty(T, K, dtype=torch.int32), empty(T, K)
+        self.counts, self.prob_sum = empty(E, dtype=torch.int32), empty(E)
+        self.loss = empty(2)
+        self._dlogits = None
+        lrm.lrm_clear_device_error(self.ws, self.ws_bytes)
+
+    @property
+    def dlogits(self) -> torch.Tensor:
+        if self._dlogits is None:  # a router that only serves has no gradient
+            self._dlogits = torch.empty(self.T, self.E, dtype=self.tdtype, device=self.device)
+        return self._dlogits
+
+    def _inputs(self, logits, mask):
+        self.desc.stride = _need_rows(logits, "logits", self.E, self.tdtype, self.device, self.T)
+        if mask is not None:
+            if mask.dtype is torch.bool:
+                mask = mask.view(torch.uint8)
+            _need(mask, "mask", (self.T,), torch.uint8, self.device)
+        return mask
+
+    def route(self, logits, mask=None, stats: bool = True, stream=None):
+        """Routes the tokens of ``logits`` [T, E] (rows may be strided). ``mask`` [T]
+        bool or uint8: tokens that are 0 there get weight 0 and count nowhere.
+        ``stats=False`` skips counts and losses (serving)."""
+        mask = self._inputs(logits, mask)
+        if stats:
+            lrm.lrm_route(self.desc, logits, mask, self.topk_idx, self.alpha, self.counts,
+                          self.prob_sum, self.loss, self.ws, self.ws_bytes, stream)
+        else:
+            lrm.lrm_route(self.desc, logits, mask, self.topk_idx, self.alpha, None, None, None,
+                          self.ws, self.ws_bytes, stream)
+
+    def backward(self, logits, dalpha=None, mask=None, dloss=None, stream=None):
+        """The logits' gradient, from the choices and counts of the last ``route``
+        (with statistics) on the same logits and mask. ``dalpha`` [T, K] float32
+        (``RecalibratedExpertBackward.gate_grad``), ``dloss`` [2] float32: what the
+        two losses weigh in the total (1 each by default)."""
+        mask = self._inputs(logits, mask)
+        if dalpha is not None:
+            _need(dalpha, "dalpha", (self.T, self.K), torch.float32, self.device)
+        if dloss is not None:
+            _need(dloss, "dloss", (2,), torch.float32, self.device)
+        lrm.lrm_route_bwd(self.desc, logits, mask, self.topk_idx, self.counts, dalpha, dloss,
+                          self.dlogits, self.ws, self.ws_bytes, stream)
+
+    def device_error(self, stream=None) -> int:
+        return lrm.lrm_get_device_error(self.ws, self.ws_bytes, stream)
+
+
+class AddRMSNorm:
+    """RMS norm of T rows of D columns, the residual's addition in front.
+
+    After ``forward``: ``h`` [T, D] (the sum, with a residual), ``y`` [T, D],
+    ``rstd`` [T] float32; with ``q_cols`` given also ``q`` [T, D] float8_e4m3fn
+    and ``q_scale`` [T, ceil(D / q_cols)] float32, y ~ q * scale (q_cols = 0: one
+    scale a row). ``store_y`` (default: without 8-bit rows only) says whether y
+    is written too. After ``backward``: ``dx`` [T, D] in ``grad_dtype``, the
+    gradient of x and of the residual alike, and ``dw`` [D] float32.
+    """
+
+    def __init__(self, T: int, D: int, dtype: str = "bf16", eps: float = 1e-6,
+                 q_cols: int | None = None, store_y: bool | None = None,
+                 grad_dtype: str = "f32", device: str | torch.device = "cuda"):
+        self.T, self.D = T, D
+        self.tdtype = _TORCH_DTYPE[dtype_code(dtype)]
+        self.gdtype = _TORCH_DTYPE[dtype_code(grad_dtype)]
+        self.desc = lrm.lrm_norm(T, D, dtype_code(dtype), dtype_code(grad_dtype), q_cols or 0,
+                                 eps, D, D)
+        self.ws_bytes = lrm.lrm_norm_workspace_bytes(self.desc)
+        if self.ws_bytes == 0:
+            raise ValueError(f"unsupported norm T={T} D={D} q_cols={q_cols} eps={eps}: D a "
+                             "multiple of 8 up to 16384, q_cols one of 0, 32, 64, 128, 256 and "
+                             "eps >= 0 are needed")
+        self.device = dev = _device(device)
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+        self.rstd = empty(T)
+        store_y = q_cols is None if store_y is None else store_y
+        if q_cols is None and not store_y:
+            raise ValueError("store_y=False leaves no output without q_cols")
+        self.y = empty(T, D, dtype=self.tdtype) if store_y else None
+        self.q = self.q_scale = None
+        if q_cols is not None:
+            self.q = empty(T, D, dtype=torch.float8_e4m3fn)
+            self.q_scale = empty(T, -(-D // q_cols) if q_cols else 1)
+        self._h = self._dx = self._dw = self._ws = None
+
+    @property
+    def h(self) -> torch.Tensor:
+        if self._h is None:
+            self._h = torch.empty(self.T, self.D, dtype=self.tdtype, device=self.device)
+        return self._h
+
+    def _backward_buffers(self):
+        """Gradients and workspace, allocated on the first backward call only."""
+        if self._dx is None:
+            dev = self.device
+            self._dx = torch.empty(self.T, self.D, dtype=self.gdtype, device=dev)
+            self._dw = torch.empty(self.D, dtype=torch.float32, device=dev)
+            self._ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+
+    @property
+    def dx(self) -> torch.Tensor:
+        self._backward_buffers()
+        return self._dx
+
+    @property
+    def dw(self) -> torch.Tensor:
+        self._backward_buffers()
+        return self._dw
+
+    def forward(self, x, w, residual=None, stream=None):
+        """x, residual [T, D] (rows may be strided by a multiple of 8 elements), w [D]."""
+        dt, dev = self.tdtype, self.device
+        self.desc.x_stride = _need_rows(x, "x", self.D, dt, dev, self.T)
+        h = None
+        if residual is not None:
+            self.desc.res_stride = _need_rows(residual, "residual", self.D, dt, dev, self.T)
+            h = self.h
+        _need(w, "w", (self.D,), dt, dev)
+        lrm.lrm_add_rmsnorm(self.desc, x, residual, w, h, self.y, self.q, self.q_scale, self.rstd,
+                            stream)
+
+    def backward(self, dy, w, dh=None, h=None, stream=None):
+        """dy [T, D]: the cotangent of y; dh: of the stored sum (the residual
+        stream), or None. ``h``: the normed rows, self.h by default (pass x where
+        there was no residual). Uses ``rstd`` of the last forward."""
+        dt, gt, dev, shape = self.tdtype, self.gdtype, self.device, (self.T, self.D)
+        h = self.h if h is None else _need(h, "h", shape, dt, dev)
+        _need(dy, "dy", shape, gt, dev)
+        if dh is not None:
+            _need(dh, "dh", shape, gt, dev)
+        _need(w, "w", (self.D,), dt, dev)
+        self._backward_buffers()
+        lrm.lrm_add_rmsnorm_bwd(self.desc, dy, dh, h, w, self.rstd, self._dx, self._dw, self._ws,
+                                self.ws_bytes, stream)
+
+
+_STATE = {"f32": lrm.LRM_STATE_F32, "f8": lrm.LRM_STATE_F8}
+_STATE_BLOCK = 256
+_CODE = {torch.float32: lrm.LRM_F32, torch.bfloat16: lrm.LRM_BF16}
+
+
+class AdamW:
+    """AdamW over a list of tensors, all of them in one call of liblrm.
+
+    ``params`` and ``grads``: contiguous float32 or bfloat16 device tensors, read
+    and updated in place (the framework's dw_gate, dw_up, dw_down are such
+    gradients). ``weight_decay``: one number, or one a tensor. ``state``: "f32",
+    or "f8" for 8-bit moments (e4m3 codes of m and of sqrt(v), one float32 scale
+    for 256 values each). ``master=True`` keeps float32 copies beside bfloat16
+    parameters.
+
+    The state lives in flat buffers over all tensors, each tensor beginning on a
+    whole block of 256: ``m``, ``v`` (float32, or float8_e4m3fn with v holding the
+    root), ``m_scale``, ``v_scale``, ``master`` (or None); tensor i holds
+    [starts[i], starts[i] + numel).
+    """
+
+    def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.01, state: str = "f32", master: bool = False):
+        self.params, self.grads = list(params), list(grads)
+        if len(self.params) != len(self.grads) or not self.params:
+            raise ValueError(f"{len(self.params)} parameters and {len(self.grads)} gradients")
+        if state not in _STATE:
+            raise ValueError(f"state: 'f32' or 'f8', got {state!r}")
+        if not (0 <= betas[0] < 1 and 0 <= betas[1] < 1 and eps >= 0):
+            raise ValueError(f"betas in [0, 1) and eps >= 0 are needed, got {betas}, {eps}")
+        n = len(self.params)
+        decay = list(weight_decay) if isinstance(weight_decay, (list, tuple)) else \
+            [weight_decay] * n
+        if len(decay) != n:
+            raise ValueError(f"{len(decay)} weight decays for {n} tensors")
+        self.device = dev = _device(self.params[0].device)
+        self.lr, self.t, self.state = lr, 0, state
+        self.starts, total = [], 0
+        for i, p in enumerate(self.params):
+            if p.dtype not in _CODE:
+                raise ValueError(f"params[{i}]: float32 or bfloat16 is needed, got {p.dtype}")
+            _need(p, f"params[{i}]", tuple(p.shape), p.dtype, dev)
+            self.starts.append(total)
+            total += -(-p.numel() // _STATE_BLOCK) * _STATE_BLOCK
+        blocks = total // _STATE_BLOCK
+        f8 = state == "f8"
+        st = torch.float8_e4m3fn if f8 else torch.float32
+        self.m = torch.zeros(total, dtype=torch.uint8 if f8 else st, device=dev).view(st)
+        self.v = torch.zeros(total, dtype=torch.uint8 if f8 else st, device=dev).view(st)
+        self.m_scale = torch.zeros(blocks, device=dev) if f8 else None
+        self.v_scale = torch.zeros(blocks, device=dev) if f8 else None
+        master = master and any(p.dtype is torch.bfloat16 for p in self.params)
+        self.master = torch.zeros(total, device=dev) if master else None
+        if master:
+            for p, a in zip(self.params, self.starts):
+                self.master[a:a + p.numel()].copy_(p.reshape(-1))
+        self._hyper = lrm.lrm_adamw(lr, betas[0], betas[1], eps, 1, None)
+        self._table = (lrm.lrm_adamw_tensor * n)()
+        for i, (p, a) in enumerate(zip(self.params, self.starts)):
+            s = self._table[i]
+            s.param, s.n, s.param_dtype = p.data_ptr(), p.numel(), _CODE[p.dtype]
+            s.master = self.master.data_ptr() + 4 * a \
+                if master and p.dtype is torch.bfloat16 else None
+            s.m = self.m.data_ptr() + a * self.m.element_size()
+            s.v = self.v.data_ptr() + a * self.v.element_size()
+            if f8:
+                s.m_scale = self.m_scale.data_ptr() + 4 * (a // _STATE_BLOCK)
+                s.v_scale = self.v_scale.data_ptr() + 4 * (a // _STATE_BLOCK)
+            s.state, s.weight_decay = _STATE[state], decay[i]
+        self.set_grads(self.grads)
+
+    def set_grads(self, grads):
+        """Other gradient tensors for the same parameters."""
+        grads = list(grads)
+        if len(grads) != len(self.params):
+            raise ValueError(f"{len(self.params)} parameters and {len(grads)} gradients")
+        for i, (p, g) in enumerate(zip(self.params, grads)):
+            if g.dtype not in _CODE:
+                raise ValueError(f"grads[{i}]: float32 or bfloat16 is needed, got {g.dtype}")
+            _need(g, f"grads[{i}]", tuple(p.shape), g.dtype, self.device)
+            self._table[i].grad, self._table[i].grad_dtype = g.data_ptr(), _CODE[g.dtype]
+        self.grads = grads
+
+    def step(self, lr: float | None = None, grad_scale=None, stream=None):
+        """One update. ``lr`` for this step only; ``grad_scale``: a float32 device
+        scalar that every gradient is multiplied by (clipping, loss scaling)."""
+        if grad_scale is not None:
+            if grad_scale.numel() != 1:
+                raise ValueError("grad_scale: one float32 value is needed")
+            _need(grad_scale, "grad_scale", tuple(grad_scale.shape), torch.float32, self.device)
+        h = self._hyper
+        h.lr = self.lr if lr is None else lr
+        h.step = self.t + 1
+        h.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
+        lrm.lrm_adamw_step(h, self._table, len(self._table), stream)
+        self.t += 1
+
+    def state_dict(self) -> dict:
+        """The state's own buffers (clone them to keep a copy)."""
+        return {"step": self.t, "master": self.master, "m": self.m, "v": self.v,
+                "m_scale": self.m_scale, "v_scale": self.v_scale}
+
+    def load_state_dict(self, state: dict):
+        """Copies a state of the same layout in; on torch's current stream. The
+        parameters are left as they are."""
+        for name in ("master", "m", "v", "m_scale", "v_scale"):
+            mine, other = getattr(self, name), state.get(name)
+            if (mine is None) != (other is None):
+                raise ValueError(f"{name}: the two states are of different kinds")
+            if mine is not None:
+                if other.shape != mine.shape or other.dtype is not mine.dtype:
+                    raise ValueError(f"{name}: {mine.dtype} {tuple(mine.shape)} is needed, got "
+                                     f"{other.dtype} {tuple(other.shape)}")
+                mine.copy_(other)
+        self.t = int(state["step"])

@@ -29,12 +29,15 @@ EXPORTS = (
     "lrm_dispatch_permute_noalloc", "lrm_selftest_wait_timeout", "lrm_score_variant",
     "lrm_gather_tokens", "lrm_expert_fc1_fwd", "lrm_expert_fc2_fwd", "lrm_combine",
     "lrm_expert_fwd_grouped", "lrm_expert_fc1_recompute", "lrm_expert_bwd_gathered",
-    "lrm_select_rate",
+    "lrm_select_rate", "lrm_router_workspace_bytes", "lrm_route", "lrm_route_bwd",
+    "lrm_gate_grad", "lrm_norm_workspace_bytes", "lrm_add_rmsnorm", "lrm_add_rmsnorm_bwd",
+    "lrm_adamw_step",
 )
 LRM_BWD_FC2_DGRAD, LRM_BWD_FC2_WGRAD, LRM_BWD_FC1_WGRAD = 1, 2, 4
 LRM_BWD_FC1_DGRAD, LRM_BWD_SCATTER_DX, LRM_BWD_ALL = 8, 16, 31
 LRM_METRIC_LRM, LRM_METRIC_GRAD_SQ, LRM_METRIC_GRAD_ABS, LRM_METRIC_RANDOM = range(4)
 LRM_NOALLOC_MAX_CHUNK_ENTRIES = 65536
+LRM_STATE_F32, LRM_STATE_F8 = 0, 1
 
 
 class LrmError(RuntimeError):
@@ -48,6 +51,35 @@ class lrm_shape(ctypes.Structure):
                 ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
+class lrm_router(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("stride", ctypes.c_int64),
+                ("renorm", ctypes.c_int32), ("balance_coef", ctypes.c_float),
+                ("z_coef", ctypes.c_float)]
+
+
+class lrm_norm(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("q_cols", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64),
+                ("res_stride", ctypes.c_int64)]
+
+
+class lrm_adamw_tensor(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("master", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("n", ctypes.c_int64), ("param_dtype", ctypes.c_int32),
+                ("grad_dtype", ctypes.c_int32), ("state", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("weight_decay", ctypes.c_double)]
+
+
+class lrm_adamw(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("step", ctypes.c_int64),
+                ("grad_scale", ctypes.c_void_p)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -56,6 +88,8 @@ def _load():
     lib = ctypes.CDLL(_LIB_PATH)
     vp, sz, i32, i64 = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int32, ctypes.c_int64
     sp = ctypes.POINTER(lrm_shape)
+    rp, np_ = ctypes.POINTER(lrm_router), ctypes.POINTER(lrm_norm)
+    ap, tp = ctypes.POINTER(lrm_adamw), ctypes.POINTER(lrm_adamw_tensor)
     sig = {
         "lrm_workspace_bytes": (sz, [sp]),
         "lrm_clear_device_error": (i32, [vp, sz, vp]),
@@ -84,6 +118,14 @@ def _load():
         "lrm_expert_fc1_recompute": (i32, [sp, vp, vp, vp, vp, vp, vp, sz, vp]),
         "lrm_expert_bwd_gathered": (i32, [sp, i32] + [vp] * 18 + [vp, sz, vp]),
         "lrm_select_rate": (i32, [sp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, sz, vp]),
+        "lrm_router_workspace_bytes": (sz, [rp]),
+        "lrm_route": (i32, [rp] + [vp] * 8 + [sz, vp]),
+        "lrm_route_bwd": (i32, [rp] + [vp] * 8 + [sz, vp]),
+        "lrm_gate_grad": (i32, [sp] + [vp] * 5 + [sz, vp]),
+        "lrm_norm_workspace_bytes": (sz, [np_]),
+        "lrm_add_rmsnorm": (i32, [np_] + [vp] * 9),
+        "lrm_add_rmsnorm_bwd": (i32, [np_] + [vp] * 8 + [sz, vp]),
+        "lrm_adamw_step": (i32, [ap, tp, i32, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -300,3 +342,48 @@ def lrm_select_rate(shape, score, off, num, den, cap, quota, keep, sel_off, sel_
     _check("lrm_select_rate", _lib.lrm_select_rate(
         ctypes.byref(shape), _p(score), _p(off), num, den, cap, _p(quota), _p(keep), _p(sel_off),
         _p(sel_pos), _p(ws), ws_bytes, _s(stream)))
+
+
+def lrm_router_workspace_bytes(router: lrm_router) -> int:
+    return int(_lib.lrm_router_workspace_bytes(ctypes.byref(router)))
+
+
+def lrm_route(router, logits, mask, topk_idx, alpha, counts, prob_sum, loss, ws, ws_bytes,
+              stream=None):
+    _check("lrm_route", _lib.lrm_route(
+        ctypes.byref(router), _p(logits), _p(mask), _p(topk_idx), _p(alpha), _p(counts),
+        _p(prob_sum), _p(loss), _p(ws), ws_bytes, _s(stream)))
+
+
+def lrm_route_bwd(router, logits, mask, topk_idx, counts, dalpha, dloss, dlogits, ws, ws_bytes,
+                  stream=None):
+    _check("lrm_route_bwd", _lib.lrm_route_bwd(
+        ctypes.byref(router), _p(logits), _p(mask), _p(topk_idx), _p(counts), _p(dalpha),
+        _p(dloss), _p(dlogits), _p(ws), ws_bytes, _s(stream)))
+
+
+def lrm_gate_grad(shape, g, y, inv, dalpha, ws, ws_bytes, stream=None):
+    _check("lrm_gate_grad", _lib.lrm_gate_grad(
+        ctypes.byref(shape), _p(g), _p(y), _p(inv), _p(dalpha), _p(ws), ws_bytes, _s(stream)))
+
+
+def lrm_norm_workspace_bytes(norm: lrm_norm) -> int:
+    return int(_lib.lrm_norm_workspace_bytes(ctypes.byref(norm)))
+
+
+def lrm_add_rmsnorm(norm, x, res, w, h, y, q, q_scale, rstd, stream=None):
+    _check("lrm_add_rmsnorm", _lib.lrm_add_rmsnorm(
+        ctypes.byref(norm), _p(x), _p(res), _p(w), _p(h), _p(y), _p(q), _p(q_scale), _p(rstd),
+        _s(stream)))
+
+
+def lrm_add_rmsnorm_bwd(norm, dy, dh, h, w, rstd, dx, dw, ws, ws_bytes, stream=None):
+    _check("lrm_add_rmsnorm_bwd", _lib.lrm_add_rmsnorm_bwd(
+        ctypes.byref(norm), _p(dy), _p(dh), _p(h), _p(w), _p(rstd), _p(dx), _p(dw), _p(ws),
+        ws_bytes, _s(stream)))
+
+
+def lrm_adamw_step(adamw, tensors, count: int, stream=None):
+    """``tensors``: a ctypes array of lrm_adamw_tensor."""
+    _check("lrm_adamw_step", _lib.lrm_adamw_step(
+        ctypes.byref(adamw), tensors, count, _s(stream)))

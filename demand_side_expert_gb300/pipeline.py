@@ -106,6 +106,17 @@ class RecalibratedExpertBackward:
         lrm.lrm_combine(self.shape, self.y, alpha, self.inv, self.out, self.ws, self.ws_bytes,
                         stream)
 
+    def gate_grad(self, g, stream=None) -> torch.Tensor:
+        """Gradient of the routing weights [T, K] (float32) from the cotangent g
+        [T, D] of the layer output and the rows ``y`` of the last forward."""
+        self._forward_buffers()
+        if getattr(self, "dalpha", None) is None:
+            self.dalpha = torch.empty(max(self.T, 1), self.K, dtype=torch.float32,
+                                      device=self.device)[: self.T]
+        lrm.lrm_gate_grad(self.shape, g, self.y, self.inv, self.dalpha, self.ws, self.ws_bytes,
+                          stream)
+        return self.dalpha
+
     def to_dispatch_order(self, rows_by_pair: torch.Tensor, stream=None) -> torch.Tensor:
         """Lay per-pair rows out in dispatch order with the current perm."""
         out = torch.empty_like(rows_by_pair)

@@ -447,6 +447,168 @@ lrm_status lrm_select_rate(const lrm_shape* shape, const float* score, const int
                            uint8_t* keep, int32_t* sel_off, int32_t* sel_pos, void* ws,
                            size_t ws_bytes, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * What a training step needs around the expert passes: the router, the
+ * routing weights' gradient, the norm in front of the layer, the optimizer.
+ * The descriptors below are HOST structs, read during the call only.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Router: top-K of every token's logits, with the balance loss and the z-loss.
+ * A token takes part if its mask byte is not 0 (mask NULL: all) and at least
+ * one of its logits is above -inf. For those tokens, p_t = softmax(x_t) and
+ * lse_t = log sum_e exp(x_te); n is their number (at least 1 in the losses):
+ *   topk_idx[t] = the K largest logits, descending, equal ones by the lower
+ *     expert id (NaN ranks as -inf, -0 as 0)
+ *   alpha[t,k]  = p at topk_idx[t,k]; renorm != 0: divided by its sum over k
+ *   counts[e]   = number of (t, k) with topk_idx[t,k] = e
+ *   prob_sum[e] = sum_t p_te
+ *   loss[0] = balance_coef * E / (n^2 K) * sum_e counts[e] prob_sum[e]
+ *   loss[1] = z_coef / n * sum_t lse_t^2
+ * Tokens that take no part get alpha = 0 and K valid, distinct ids (of their
+ * logits, by the same rule); they count nowhere. In a token that takes part,
+ * NaN and +inf logits make its weights and the statistics NaN. FP32 arithmetic; the
+ * statistics are added in a fixed order (same inputs, same bits).
+ *   logits [T,E] dtype (read), rows `stride` elements apart (stride >= E).
+ *   mask [T] uint8 (read) or NULL, any alignment.
+ *   topk_idx [T,K] int32, alpha [T,K] float (written).
+ *   counts [E] int32, prob_sum [E] float, loss [2] float (written), or all
+ *     three NULL: no statistics (the serving form; balance_coef, z_coef unused).
+ * Limits: E <= 1024, K <= 32, T*K < 2^31, else LRM_ERR_UNSUPPORTED.
+ * ws: lrm_router_workspace_bytes, header as everywhere (zeroed once with
+ * lrm_clear_device_error; the statistics leave their ticket word at zero).
+ */
+typedef struct lrm_router {
+  int32_t T, E, K;
+  int32_t dtype;      /* lrm_dtype of logits and dlogits */
+  int64_t stride;     /* elements from one row of logits to the next */
+  int32_t renorm;
+  float balance_coef, z_coef;
+} lrm_router;
+size_t lrm_router_workspace_bytes(const lrm_router* router);
+lrm_status lrm_route(const lrm_router* router, const void* logits, const uint8_t* mask,
+                     int32_t* topk_idx, float* alpha, int32_t* counts, float* prob_sum,
+                     float* loss, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Gradient of the router with respect to its logits, of
+ *   sum alpha dalpha + dloss[0] loss[0] + dloss[1] loss[1],
+ * the choices and counts taken as constants:
+ *   renorm: dx at the choices  = alpha (dalpha - sum_k alpha dalpha)
+ *   else:   dx = p (dp - sum_e p dp), dp = dalpha at the choices, 0 elsewhere
+ *   balance: + p (c - sum_e p c), c_e = dloss[0] balance_coef E counts[e] / (n^2 K)
+ *   z:       + p dloss[1] 2 z_coef lse / n
+ * Tokens that take no part get zeros, whatever their dalpha. n = sum counts / K.
+ *   logits, mask as lrm_route (read); topk_idx [T,K], counts [E] from it (read).
+ *   dalpha [T,K] float (read) or NULL (0); dloss [2] float (read) or NULL (1, 1).
+ *   dlogits [T,E] dtype, contiguous (written).
+ * Ids outside [0,E) are skipped and flag LRM_DEVERR_EXPERT_ID.
+ */
+lrm_status lrm_route_bwd(const lrm_router* router, const void* logits, const uint8_t* mask,
+                         const int32_t* topk_idx, const int32_t* counts, const float* dalpha,
+                         const float* dloss, void* dlogits, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * Gradient of the routing weights through lrm_combine, for every routed pair:
+ *   dalpha[t,k] = <g_t, y[inv[t*K+k]]>   (FP32 accumulation)
+ *   g [T,D] dtype (cotangent at the MoE output), y [N,D] dtype (expert outputs
+ *   in dispatch order, as lrm_expert_fc2_fwd leaves them), inv [N] int32 (read);
+ *   dalpha [T,K] float (written).
+ * inv entries outside [0,N) give 0 and flag LRM_DEVERR_INDEX.
+ */
+lrm_status lrm_gate_grad(const lrm_shape* shape, const void* g, const void* y,
+                         const int32_t* inv, float* dalpha, void* ws, size_t ws_bytes,
+                         void* stream);
+
+/*
+ * Root-mean-square norm with the residual's addition and an 8-bit output.
+ *   h = x + res (res NULL: h = x),  rstd = 1 / sqrt(mean_d h^2 + eps),
+ *   y = h * rstd * w
+ *   q = e4m3(y / scale), scale = max(amax, 2^-100) / 448 with amax the largest
+ *     |y| of each q_cols columns of a row (the last group may be shorter), or
+ *     of the whole row for q_cols = 0
+ * FP32 arithmetic on the unrounded sum; h and y are rounded once to dtype, q is
+ * taken from the unrounded y. NaN and infinities stay in their row (NaN is
+ * ignored by amax and becomes the e4m3 NaN).
+ *   x [T,D] dtype, rows x_stride elements apart; res [T,D] dtype or NULL, rows
+ *     res_stride apart; w [D] dtype (read).
+ *   h [T,D] dtype or NULL; y [T,D] dtype or NULL; q [T,D] e4m3 bytes and
+ *     q_scale [T, ceil(D / q_cols)] float (one column for q_cols = 0), or both
+ *     NULL; rstd [T] float or NULL (written, contiguous). y or q is required.
+ * h or y may be x or res themselves (same pointer, contiguous rows); no other
+ * overlap is allowed.
+ * Limits: D a multiple of 8 up to 16384, strides multiples of 8, q_cols one of
+ * 0, 32, 64, 128, 256, else LRM_ERR_UNSUPPORTED.
+ */
+typedef struct lrm_norm {
+  int32_t T, D;
+  int32_t dtype;       /* of x, res, w, h, y */
+  int32_t grad_dtype;  /* of dy, dh, dx */
+  int32_t q_cols;
+  float eps;
+  int64_t x_stride, res_stride;
+} lrm_norm;
+size_t lrm_norm_workspace_bytes(const lrm_norm* norm);
+lrm_status lrm_add_rmsnorm(const lrm_norm* norm, const void* x, const void* res, const void* w,
+                           void* h, void* y, void* q, float* q_scale, float* rstd,
+                           void* stream);
+
+/*
+ * Its gradients, with xhat = h * rstd:
+ *   dx = rstd * (w dy - xhat * mean_d(w dy xhat)) + dh
+ *   dw = sum_t dy * xhat
+ * dx is the gradient of x and of res alike; dh is what reaches the stored sum h
+ * from elsewhere (the residual stream), NULL for none.
+ *   dy, dh [T,D] grad_dtype, h [T,D] dtype, w [D] dtype, rstd [T] float (read);
+ *   dx [T,D] grad_dtype, dw [D] float (overwritten). All contiguous; dx may be
+ *   dy or dh itself. The strides and q_cols of the descriptor are not used.
+ * Rows are added in a fixed order (same inputs, same bits).
+ * ws: lrm_norm_workspace_bytes.
+ */
+lrm_status lrm_add_rmsnorm_bwd(const lrm_norm* norm, const void* dy, const void* dh,
+                               const void* h, const void* w, const float* rstd, void* dx,
+                               float* dw, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One AdamW step (decoupled weight decay) over `count` tensors:
+ *   g' = grad * (*grad_scale),  m = beta1 m + (1 - beta1) g',
+ *   v = beta2 v + (1 - beta2) g'^2,
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * FP32 arithmetic. p is master where one is given (param then gets it rounded),
+ * else param itself, updated in FP32 and rounded once.
+ * LRM_STATE_F32: m, v float [n]. LRM_STATE_F8: m holds e4m3(m / scale) and v
+ * holds e4m3(sqrt(v) / scale), with one scale = max(amax, 2^-100) / 448 for
+ * each 256 consecutive values; a positive root is never stored as 0. Zero
+ * codes and scales are a valid start. The step uses the unrounded new moments.
+ * Buffers are the caller's, param, grad, master, m, v 16-byte aligned, not
+ * overlapping. `step` counts from 1. It is read on the host: a captured graph
+ * replays the bias correction of the step it was captured with.
+ */
+typedef enum lrm_state { LRM_STATE_F32 = 0, LRM_STATE_F8 = 1 } lrm_state;
+typedef struct lrm_adamw_tensor {
+  void* param;         /* [n] param_dtype, read and written */
+  const void* grad;    /* [n] grad_dtype */
+  float* master;       /* [n] float or NULL; only beside an LRM_BF16 param */
+  void *m, *v;         /* [n] */
+  float *m_scale, *v_scale; /* [ceil(n / 256)], LRM_STATE_F8 only */
+  int64_t n;
+  int32_t param_dtype, grad_dtype;
+  int32_t state;       /* lrm_state */
+  int32_t reserved;
+  double weight_decay;
+} lrm_adamw_tensor;
+typedef struct lrm_adamw {
+  double lr, beta1, beta2, eps;
+  int64_t step;
+  const float* grad_scale; /* device scalar, NULL: 1 */
+} lrm_adamw;
+lrm_status lrm_adamw_step(const lrm_adamw* adamw, const lrm_adamw_tensor* tensors,
+                          int32_t count, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
