@@ -206,14 +206,6 @@ constexpr int kFusedWarps = kFusedThreads / 32;
 #endif
 constexpr int64_t kFusedMaxPairs = LRM_DISPATCH_FUSED_MAX;
 
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-  uint32_t r;
-  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-  return r;
-}
 __device__ __forceinline__ int ld_peer_smem(const int32_t* local, uint32_t rank) {
   uint32_t laddr = static_cast<uint32_t>(__cvta_generic_to_shared(local)), raddr;
   int v;

@@ -10,9 +10,10 @@
 //   balance = c_b E / (n^2 K) sum_e counts_e P_e,   z = c_z / n sum_t lse_t^2
 // counts are constants to the gradient (they are piecewise constant).
 //
-// A warp per token: lane l holds the NI consecutive experts l*NI .. of the
-// row in registers, so a row is read once, the lowest lane of a tie is the
-// lowest expert, and no shared memory is touched before the statistics.
+// G lanes of a warp hold a token's row in registers, NI experts a lane, so a
+// row is read once and no shared memory is touched before the statistics. The
+// bytes are few; what bounds the kernels is the instructions of a token, so
+// many tokens share a warp (G = 8 or 16) and few get a whole one.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -25,63 +26,207 @@ constexpr int kRouterMaxE = 1024;
 constexpr int kRouterMaxK = 32;
 constexpr int kRouterMaxCtas = 160;  // partial statistics rows in the workspace
 
-// The statistics' ticket is word 1 of the workspace header.
-inline uint32_t* router_ticket(void* ws) { return static_cast<uint32_t*>(ws) + 1; }
-
 // Unsigned key in the order of the floats; -0 counts as 0 and NaN as -inf.
 // Every number's key is above 0, which marks "taken" or "no such expert".
 __device__ __forceinline__ uint32_t order_key(float x) {
-  if (x != x) x = -CUDART_INF_F;
-  const uint32_t u = __float_as_uint(x + 0.f);
-  return u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  const uint32_t u = __float_as_uint(fmaxf(x, -CUDART_INF_F) + 0.f);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
 }
 
-__device__ __forceinline__ float load_logit(const float* p) { return __ldg(p); }
-__device__ __forceinline__ float load_logit(const __nv_bfloat16* p) {
-  return __bfloat162float(*p);
+// A choice's key: the logit's order first, then the lower expert id, so that
+// keys are unique. A bfloat16 leaves the low half of its 32 bits free for the
+// id; a float32 needs 64 bits.
+template <typename T>
+struct ChoiceKey;
+template <>
+struct ChoiceKey<__nv_bfloat16> {
+  using Key = uint32_t;
+  __device__ __forceinline__ static Key make(float x, int e) {
+    return (order_key(x) & 0xffff0000u) | (0xffffu - (uint32_t)e);
+  }
+  __device__ __forceinline__ static int expert(Key k) { return 0xffff - (int)(k & 0xffffu); }
+  __device__ __forceinline__ static float value(Key k) {
+    return key_value((k >> 31) ? k & 0xffff0000u : k | 0xffffu);
+  }
+};
+template <>
+struct ChoiceKey<float> {
+  using Key = uint64_t;
+  __device__ __forceinline__ static Key make(float x, int e) {
+    return (uint64_t)order_key(x) << 32 | (0xffffffffu - (uint32_t)e);
+  }
+  __device__ __forceinline__ static int expert(Key k) { return (int)(0xffffffffu - (uint32_t)k); }
+  __device__ __forceinline__ static float value(Key k) { return key_value((uint32_t)(k >> 32)); }
+};
+
+// Reductions over the G lanes of a token (G = 32: the warp's own instructions).
+template <int G>
+__device__ __forceinline__ uint32_t group_max(uint32_t v) {
+  if constexpr (G == 32) {
+    return __reduce_max_sync(0xffffffffu, v);
+  } else {
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
 }
-__device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
-__device__ __forceinline__ void store_logit(__nv_bfloat16* p, float v) {
-  *p = __float2bfloat16_rn(v);
+template <int G>
+__device__ __forceinline__ uint64_t group_max(uint64_t v) {
+  if constexpr (G == 32) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+    const uint32_t lo =
+        __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+    return (uint64_t)hi << 32 | lo;
+  } else {
+#pragma unroll
+    for (int o = 1; o < G; o <<= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+  }
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_fmax(float v) {
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
 }
 
-template <typename T, int NI>
-__device__ __forceinline__ void load_row(const T* row, int e0, int E, float (&x)[NI]) {
+// exp(x) for x <= 0 and 1 / x for x in [1, E]: results below 2^-126 are 0.
+__device__ __forceinline__ float exp_neg(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+  return y;
+}
+__device__ __forceinline__ float inverse(float x) { return __fdividef(1.f, x); }
+
+// Which experts a lane holds: chunks of kVec consecutive ones (16 bytes at
+// most), the chunks of the G lanes side by side: expert of slot i of lane l is
+// (i / kVec * G + l) * kVec + i % kVec.
+template <typename T, int NI, int G>
+struct RowShape {
+  static constexpr int kVec = NI * (int)sizeof(T) < 16 ? NI : 16 / (int)sizeof(T);
+  __device__ __forceinline__ static int expert(int i, int lane) {
+    return (i / kVec * G + lane) * kVec + i % kVec;
+  }
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_bytes(void* dst, const void* src) {
+  if constexpr (BYTES == 16) *(uint4*)dst = *(const uint4*)src;
+  else if constexpr (BYTES == 8) *(uint2*)dst = *(const uint2*)src;
+  else if constexpr (BYTES == 4) *(uint32_t*)dst = *(const uint32_t*)src;
+  else *(uint16_t*)dst = *(const uint16_t*)src;
+}
+
+// The lane's logits, -inf past E. vec: rows begin on a multiple of a chunk, so
+// a chunk wholly inside the row is one load.
+template <typename T, int NI, int G>
+__device__ __forceinline__ void load_row(const T* row, int lane, int E, bool vec, float (&x)[NI]) {
+  using S = RowShape<T, NI, G>;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) x[i] = e0 + i < E ? load_logit(row + e0 + i) : -CUDART_INF_F;
+  for (int c = 0; c < NI / S::kVec; ++c) {
+    const int e = S::expert(c * S::kVec, lane);
+    alignas(16) T v[S::kVec];
+    if (vec && e + S::kVec <= E) {
+      copy_bytes<S::kVec * (int)sizeof(T)>(v, row + e);
+#pragma unroll
+      for (int i = 0; i < S::kVec; ++i) x[c * S::kVec + i] = (float)v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kVec; ++i)
+        x[c * S::kVec + i] = e + i < E ? (float)row[e + i] : -CUDART_INF_F;
+    }
+  }
 }
 
 // Whether token t takes part: its row maximum is above -inf, or it holds a
 // NaN (which then reaches the outputs), and it is not masked out.
-template <int NI>
-__device__ __forceinline__ bool takes_part(const float (&x)[NI], float top, const uint8_t* mask,
-                                           int64_t t) {
-  if (mask && mask[t] == 0) return false;
-  if (top > -CUDART_INF_F) return true;
-  bool nan = false;
+template <int NI, int G>
+__device__ __forceinline__ bool takes_part(const float (&x)[NI], float top, bool masked) {
+  bool some = top > -CUDART_INF_F;
+  if (__any_sync(0xffffffffu, !some)) {
+    bool nan = false;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) nan |= x[i] != x[i];
-  return __any_sync(0xffffffffu, nan);
+    for (int i = 0; i < NI; ++i) nan |= x[i] != x[i];
+    const uint32_t who = __ballot_sync(0xffffffffu, nan);
+    const int lane = threadIdx.x & 31;
+    if constexpr (G == 32) some |= who != 0;
+    else some |= (who >> (lane & ~(G - 1)) & ((1u << G) - 1)) != 0;
+  }
+  return some && !masked;
 }
 
-template <typename T, int NI, bool STATS>
-__global__ void __launch_bounds__(1024)
+// The lane's keys as sorted lists of (up to) 4, largest first: a choice is
+// the largest front over the token's lanes, and is taken from its list. A
+// longer list would cost more to sort than the shorter lists cost to look at.
+template <typename Key, int NI>
+struct KeyLists {
+  static constexpr int kLen = NI < 4 ? NI : 4;
+  Key key[NI];
+  __device__ __forceinline__ void exchange(int a, int b) {
+    const Key hi = max(key[a], key[b]), lo = min(key[a], key[b]);
+    key[a] = hi;
+    key[b] = lo;
+  }
+  __device__ __forceinline__ void sort() {
+#pragma unroll
+    for (int l = 0; l < NI; l += kLen) {
+      if constexpr (kLen == 2) exchange(l, l + 1);
+      if constexpr (kLen == 4) {
+        exchange(l, l + 1);
+        exchange(l + 2, l + 3);
+        exchange(l, l + 2);
+        exchange(l + 1, l + 3);
+        exchange(l + 1, l + 2);
+      }
+    }
+  }
+  __device__ __forceinline__ Key front() const {
+    Key m = key[0];
+#pragma unroll
+    for (int l = kLen; l < NI; l += kLen) m = max(m, key[l]);
+    return m;
+  }
+  __device__ __forceinline__ void take(Key k) {
+#pragma unroll
+    for (int l = 0; l < NI; l += kLen) {
+      const bool here = key[l] == k;
+#pragma unroll
+      for (int i = 0; i + 1 < kLen; ++i) key[l + i] = here ? key[l + i + 1] : key[l + i];
+      key[l + kLen - 1] = here ? (Key)0 : key[l + kLen - 1];
+    }
+  }
+};
+
+// Threads of a routing CTA: what NI experts a lane leave registers for.
+template <typename T>
+constexpr int router_threads(int ni) {
+  return ni <= 8 ? 1024 : ni == 16 ? (sizeof(T) == 2 ? 1024 : 512) : 256;
+}
+
+template <typename T, int NI, int G, bool STATS>
+__global__ void __launch_bounds__(router_threads<T>(NI))
 route_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask, int ntok, int E,
-             int K, int64_t stride, int renorm, float balance_coef, float z_coef,
+             int K, int64_t stride, int vec, int renorm, float balance_coef, float z_coef,
              int32_t* __restrict__ topk_idx, float* __restrict__ alpha,
              int32_t* __restrict__ counts, float* __restrict__ prob_sum,
-             float* __restrict__ loss, float* part_p, int32_t* part_c, float* part_z,
-             uint32_t* ticket) {
+             float* __restrict__ loss, float2* __restrict__ part, float* __restrict__ part_z) {
   pdl_begin();  // predecessor complete before any global access
-  extern __shared__ float sm[];  // STATS: [warps][E] sums of p, then [E] counts, [warps] lse^2
+  extern __shared__ float sm_p[];  // STATS: sums of p [warps][E], then counts [E]
+  using C = ChoiceKey<T>;
+  using S = RowShape<T, NI, G>;
+  constexpr int kTokens = 32 / G;  // tokens a warp
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
-  const int e0 = lane * NI;
-  float* sm_p = sm;
-  int32_t* sm_c = reinterpret_cast<int32_t*>(sm + (int64_t)nwarp * E);
-  float* sm_z = reinterpret_cast<float*>(sm_c + E);
+  const int gl = lane % G;
+  int32_t* sm_c = reinterpret_cast<int32_t*>(sm_p + nwarp * E);
   float acc[NI];
   float zacc = 0.f;
   if constexpr (STATS) {
@@ -90,220 +235,319 @@ route_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask, int
     for (int i = 0; i < NI; ++i) acc[i] = 0.f;
     __syncthreads();
   }
-  for (int64_t t = (int64_t)blockIdx.x * nwarp + warp; t < ntok; t += (int64_t)gridDim.x * nwarp) {
+  const int64_t step = (int64_t)gridDim.x * nwarp * kTokens;
+  for (int64_t first = ((int64_t)blockIdx.x * nwarp + warp) * kTokens; first < ntok;
+       first += step) {
+    // lanes of a token past the end follow token `first` and write nothing
+    const bool real = first + lane / G < ntok;
+    const int64_t t = real ? first + lane / G : first;
     float x[NI];
-    uint32_t key[NI];
-    load_row<T, NI>(logits + t * stride, e0, E, x);
-    uint32_t best = 0;
-    int at = 0;
+    load_row<T, NI, G>(logits + t * stride, gl, E, vec, x);
+    const bool masked = mask && mask[t] == 0;
+    KeyLists<typename C::Key, NI> list;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      key[i] = e0 + i < E ? order_key(x[i]) : 0u;
-      if (key[i] > best) { best = key[i]; at = i; }
+      const int e = S::expert(i, gl);
+      list.key[i] = e < E ? C::make(x[i], e) : (typename C::Key)0;
     }
-    // lane k keeps the k-th choice
-    uint32_t my_key = 0, top_key = 0;
-    int my_idx = 0;
+    list.sort();
+    // lane k of the token keeps its k-th choice
+    typename C::Key my_key = 0;
+    float top = 0.f;
     for (int k = 0; k < K; ++k) {
-      const uint32_t hi = __reduce_max_sync(0xffffffffu, best);
-      const int src = __ffs(__ballot_sync(0xffffffffu, best == hi)) - 1;
-      const int idx = __shfl_sync(0xffffffffu, e0 + at, src);
-      if (k == 0) top_key = hi;
-      if (lane == k) { my_key = hi; my_idx = idx; }
-      if (lane == src) {
-        best = 0;
-        const int gone = at;
-#pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          if (i == gone) key[i] = 0;
-          if (key[i] > best) { best = key[i]; at = i; }
-        }
-      }
+      const typename C::Key best = group_max<G>(list.front());
+      if (k == 0) top = C::value(best);
+      if (gl == k) my_key = best;
+      list.take(best);
     }
-    const float top = key_value(top_key);
-    const bool use = takes_part(x, top, mask, t);
+    const bool use = takes_part<NI, G>(x, top, masked) && real;
     // p, its sum over the row, and the weights of the K choices
     float total = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      x[i] = expf(x[i] - top);  // 0 past E: -inf - top
-      if (e0 + i >= E) x[i] = 0.f;
+      x[i] = S::expert(i, gl) < E ? exp_neg(x[i] - top) : 0.f;
       total += x[i];
     }
-    total = warp_sum(total);
-    float a = lane < K ? expf(key_value(my_key) - top) : 0.f;
-    const float den = renorm ? warp_sum(a) : total;
+    total = group_sum<G>(total);
+    const float inv_total = inverse(total);
+    const bool choice = gl < K;
+    float a = choice ? exp_neg(C::value(my_key) - top) : 0.f;
+    // every lane of the warp takes part in the sum, whatever its token holds
+    const float inv_a = renorm ? inverse(group_sum<G>(a)) : inv_total;
     // a NaN in the row makes every weight NaN, also where the choices' own sum has none
-    a = total != total ? total : a / den;
-    if (lane < K) {
-      topk_idx[t * K + lane] = my_idx;
-      alpha[t * K + lane] = use ? a : 0.f;
+    a = total != total ? total : a * inv_a;
+    const int my_idx = C::expert(my_key);
+    if (choice && real) {
+      topk_idx[t * K + gl] = my_idx;
+      alpha[t * K + gl] = use ? a : 0.f;
     }
     if constexpr (STATS) {
       if (use) {
-        const float inv_total = 1.f / total;
 #pragma unroll
         for (int i = 0; i < NI; ++i) acc[i] = fmaf(x[i], inv_total, acc[i]);
-        const float lse = top + logf(total);
+        const float lse = top + __logf(total);
         zacc = fmaf(lse, lse, zacc);
-        if (lane < K) atomicAdd(&sm_c[my_idx], 1);
+        if (choice) atomicAdd(&sm_c[my_idx], 1);
       }
     }
   }
   if constexpr (STATS) {
-    // CTA sums in a fixed order; then the last CTA to arrive adds the CTAs'
-    // sums, in CTA order: the result does not depend on the arrival order
+    // the CTA's sums, in a fixed order; a single CTA finishes by itself, the
+    // sums of several are added by route_sums_kernel
+    __shared__ float red[3][32];
 #pragma unroll
-    for (int i = 0; i < NI; ++i)
-      if (e0 + i < E) sm_p[(int64_t)warp * E + e0 + i] = acc[i];
-    if (lane == 0) sm_z[warp] = zacc;
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-      float s = 0.f;
-      for (int w = 0; w < nwarp; ++w) s += sm_p[(int64_t)w * E + e];
-      part_p[(int64_t)blockIdx.x * E + e] = s;
-      part_c[(int64_t)blockIdx.x * E + e] = sm_c[e];
+    for (int o = G; o < 32; o <<= 1) {  // over the warp's tokens
+      zacc += __shfl_xor_sync(0xffffffffu, zacc, o);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
     }
-    if (threadIdx.x == 0) {
-      float s = 0.f;
-      for (int w = 0; w < nwarp; ++w) s += sm_z[w];
-      part_z[blockIdx.x] = s;
+    if (lane < G) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const int e = S::expert(i, gl);
+        if (e < E) sm_p[warp * E + e] = acc[i];
+      }
     }
-    __shared__ bool last;
-    __threadfence();
+    if (lane == 0) red[2][warp] = zacc;
     __syncthreads();
-    if (threadIdx.x == 0) last = atomicInc(ticket, gridDim.x - 1) == gridDim.x - 1;
-    __syncthreads();
-    if (!last) return;
-    __threadfence();
-    float dot = 0.f, cnt = 0.f;
-    __shared__ float red[2][32];
+    float z = 0.f;  // warp 0: the CTA's sum of lse^2
+    if (warp == 0) z = warp_sum(lane < nwarp ? red[2][lane] : 0.f);
+    const bool alone = gridDim.x == 1;
+    float dot = 0.f;
     int64_t pairs = 0;
     for (int e = threadIdx.x; e < E; e += blockDim.x) {
       float s = 0.f;
-      int32_t c = 0;
-      for (int b = 0; b < (int)gridDim.x; ++b) {
-        s += __ldcg(part_p + (int64_t)b * E + e);
-        c += __ldcg(part_c + (int64_t)b * E + e);
+#pragma unroll 8
+      for (int w = 0; w < nwarp; ++w) s += sm_p[w * E + e];
+      const int c = sm_c[e];
+      if (alone) {
+        prob_sum[e] = s;
+        counts[e] = c;
+        dot = fmaf((float)c, s, dot);
+        pairs += c;
+      } else {
+        part[(int64_t)blockIdx.x * E + e] = make_float2(s, __int_as_float(c));
       }
+    }
+    if (!alone) {
+      if (threadIdx.x == 0) part_z[blockIdx.x] = z;
+      return;
+    }
+    // tokens that took part: every one chose K experts
+    dot = warp_sum(dot);
+    const float cnt = warp_sum((float)pairs);
+    if (lane == 0) { red[0][warp] = dot; red[1][warp] = cnt; }
+    __syncthreads();
+    if (warp == 0) {
+      const float d = warp_sum(lane < nwarp ? red[0][lane] : 0.f);
+      const float n = fmaxf(warp_sum(lane < nwarp ? red[1][lane] : 0.f) / (float)K, 1.f);
+      if (lane == 0) {
+        loss[0] = balance_coef * (float)E * (d / (n * n * (float)K));
+        loss[1] = z_coef * (z / n);
+      }
+    }
+  }
+}
+
+// Adds the routing CTAs' sums in CTA order and forms the losses: one cluster,
+// every CTA an eighth of the experts, 16 experts at a time by 32 shares of the
+// rows; the CTAs' parts of the loss meet in the first one's shared memory.
+constexpr int kSumCtas = 8, kSumThreads = 512, kSumCols = 16;
+__global__ void __cluster_dims__(kSumCtas, 1, 1) __launch_bounds__(kSumThreads)
+route_sums_kernel(const float2* __restrict__ part, const float* __restrict__ part_z, int rows,
+                  int E, int K, float balance_coef, float z_coef, int32_t* __restrict__ counts,
+                  float* __restrict__ prob_sum, float* __restrict__ loss) {
+  pdl_begin();  // predecessor complete before any global access
+  constexpr int kWarps = kSumThreads / 32;
+  __shared__ float2 sm[2][kWarps][kSumCols];
+  __shared__ float2 red[kWarps];
+  __shared__ float2 all[kSumCtas];  // (sum of counts P, sum of counts) of every CTA
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = (int)cluster_ctarank();
+  const int per = (E + kSumCtas - 1) / kSumCtas;
+  const int begin = rank * per, end = min(E, begin + per);
+  const int col = threadIdx.x % kSumCols, share = threadIdx.x / kSumCols;
+  float z = 0.f;
+  if (rank == 0 && warp == 0)
+    for (int r = lane; r < rows; r += 32) z += part_z[r];
+  float dot = 0.f, cnt = 0.f;
+  int buf = 0;
+  for (int e0 = begin; e0 < end; e0 += kSumCols, buf ^= 1) {
+    float s = 0.f;
+    int c = 0;
+    if (e0 + col < end) {
+#pragma unroll 5
+      for (int r = share; r < rows; r += kSumThreads / kSumCols) {
+        const float2 v = part[(int64_t)r * E + e0 + col];
+        s += v.x;
+        c += __float_as_int(v.y);
+      }
+    }
+    s += __shfl_xor_sync(0xffffffffu, s, 16);
+    c += __shfl_xor_sync(0xffffffffu, c, 16);
+    if (lane < kSumCols) sm[buf][warp][lane] = make_float2(s, __int_as_float(c));
+    __syncthreads();
+    // warp w adds column w
+    const float2 v = sm[buf][lane % kWarps][warp];
+    s = v.x;
+    c = __float_as_int(v.y);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) {
+      s += __shfl_xor_sync(0xffffffffu, s, o);
+      c += __shfl_xor_sync(0xffffffffu, c, o);
+    }
+    const int e = e0 + warp;
+    if (lane == 0 && e < end) {
       prob_sum[e] = s;
       counts[e] = c;
       dot = fmaf((float)c, s, dot);
-      pairs += c;
+      cnt += (float)c;
     }
+  }
+  if (lane == 0) red[warp] = make_float2(dot, cnt);
+  __syncthreads();
+  if (warp == 0) {
+    dot = warp_sum(lane < kWarps ? red[lane].x : 0.f);
+    cnt = warp_sum(lane < kWarps ? red[lane].y : 0.f);
+    z = warp_sum(z);
+    if (lane == 0) {
+      const uint32_t mine = (uint32_t)__cvta_generic_to_shared(&all[rank]);
+      uint32_t first;
+      asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(first) : "r"(mine));
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(first), "f"(dot), "f"(cnt)
+                   : "memory");
+    }
+  }
+  cluster_barrier();  // every CTA's part has arrived in the first one
+  if (rank == 0 && warp == 0) {
+    const float d = warp_sum(lane < kSumCtas ? all[lane].x : 0.f);
     // tokens that took part: every one chose K experts
-    cnt = (float)pairs;
-    dot = warp_sum(dot);
-    cnt = warp_sum(cnt);
-    if (lane == 0) { red[0][warp] = dot; red[1][warp] = cnt; }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      float d = 0.f, n = 0.f, z = 0.f;
-      for (int w = 0; w < nwarp; ++w) { d += red[0][w]; n += red[1][w]; }
-      for (int b = 0; b < (int)gridDim.x; ++b) z += __ldcg(part_z + b);
-      n = fmaxf(n / (float)K, 1.f);
+    const float n = fmaxf(warp_sum(lane < kSumCtas ? all[lane].y : 0.f) / (float)K, 1.f);
+    if (lane == 0) {
       loss[0] = balance_coef * (float)E * (d / (n * n * (float)K));
       loss[1] = z_coef * (z / n);
     }
   }
 }
 
-template <typename T, int NI>
-__global__ void __launch_bounds__(256)
+// The G lanes of a token write the gradient that every expert has; then lane k
+// adds what choice k has on top and writes that element again.
+constexpr int kRouteBwdThreads = 256;
+template <typename T, int NI, int G>
+__global__ void __launch_bounds__(kRouteBwdThreads)
 route_bwd_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask,
                  const int32_t* __restrict__ topk_idx, const int32_t* __restrict__ counts,
                  const float* __restrict__ dalpha, const float* __restrict__ dloss, int ntok,
-                 int E, int K, int64_t stride, int renorm, float balance_coef, float z_coef,
-                 T* __restrict__ dlogits, int32_t* err) {
+                 int E, int K, int64_t stride, int vec, int out_vec, int renorm,
+                 float balance_coef, float z_coef, T* dlogits, int32_t* err) {
   pdl_begin();  // predecessor complete before any global access
-  const int lane = threadIdx.x & 31;
-  const int e0 = lane * NI;
-  // d balance / d p_te of the lane's experts, and 2 c_z / n of the z-loss
-  float cost[NI];
+  using S = RowShape<T, NI, G>;
+  constexpr int kTokens = 32 / G;
+  constexpr int kPer = kRouterMaxK / G;  // choices a lane at most
+  const int lane = threadIdx.x & 31, gl = lane % G;
+  // tokens that took part: every one chose K experts
   int64_t pairs = 0;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int c = e0 + i < E ? counts[e0 + i] : 0;
-    pairs += c;
-    cost[i] = (float)c;
-  }
+  for (int e = lane; e < E; e += 32) pairs += counts[e];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
   const float n = fmaxf((float)pairs / (float)K, 1.f);
   const float d0 = dloss ? dloss[0] : 1.f, d1 = dloss ? dloss[1] : 1.f;
+  // d balance / d p_te = kb counts_e, and 2 c_z / n of the z-loss
   const float kb = d0 * balance_coef * (float)E / (n * n * (float)K);
   const float kz = d1 * 2.f * z_coef / n;
+  float cost[NI];
 #pragma unroll
-  for (int i = 0; i < NI; ++i) cost[i] *= kb;
-
-  const int64_t nwarps = ((int64_t)gridDim.x * blockDim.x) >> 5;
-  for (int64_t t = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; t < ntok; t += nwarps) {
-    float x[NI], d[NI];
-    load_row<T, NI>(logits + t * stride, e0, E, x);
-    uint32_t hi = 0;
+  for (int i = 0; i < NI; ++i) {
+    const int e = S::expert(i, gl);
+    cost[i] = e < E ? kb * (float)counts[e] : 0.f;
+  }
+  const int nwarp = kRouteBwdThreads / 32;
+  const int64_t step = (int64_t)gridDim.x * nwarp * kTokens;
+  for (int64_t first = ((int64_t)blockIdx.x * nwarp + (threadIdx.x >> 5)) * kTokens;
+       first < ntok; first += step) {
+    const bool real = first + lane / G < ntok;
+    const int64_t t = real ? first + lane / G : first;
+    const T* row = logits + t * stride;
+    float x[NI];
+    load_row<T, NI, G>(row, gl, E, vec, x);
+    const bool masked = mask && mask[t] == 0;
+    // the lane's own choices: expert, dalpha, logit
+    int idx[kPer];
+    float da[kPer], xc[kPer];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) hi = max(hi, e0 + i < E ? order_key(x[i]) : 0u);
-    const float top = key_value(__reduce_max_sync(0xffffffffu, hi));
-    const bool use = takes_part(x, top, mask, t);
-    int my_idx = -1;
-    float my_da = 0.f;
-    if (lane < K) {
-      const int q = topk_idx[t * K + lane];
-      if (q >= 0 && q < E) my_idx = q;
-      else flag_error(err, LRM_DEVERR_EXPERT_ID);
-      if (dalpha && my_idx >= 0) my_da = dalpha[t * K + lane];
+    for (int j = 0; j < kPer; ++j) {
+      const int k = j * G + gl;
+      idx[j] = -1;
+      da[j] = 0.f;
+      xc[j] = -CUDART_INF_F;
+      if (k < K) {
+        const int q = topk_idx[t * K + k];
+        if (q >= 0 && q < E) {
+          idx[j] = q;
+          xc[j] = (float)row[q];
+          if (dalpha) da[j] = dalpha[t * K + k];
+        } else {
+          flag_error(err, LRM_DEVERR_EXPERT_ID);
+        }
+      }
     }
-    float total = 0.f;
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) top = fmaxf(top, x[i]);
+    top = group_fmax<G>(top);
+    const bool use = takes_part<NI, G>(x, top, masked);
+    float total = 0.f, cdot = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      x[i] = e0 + i < E ? expf(x[i] - top) : 0.f;
-      d[i] = 0.f;
+      x[i] = S::expert(i, gl) < E ? exp_neg(x[i] - top) : 0.f;
       total += x[i];
+      cdot = fmaf(x[i], cost[i], cdot);
     }
-    total = warp_sum(total);
-    const float inv_total = 1.f / total;
-    // the lane of choice k gets dalpha_k at its expert
-    float my_ex = 0.f;  // exp(x - top) of the lane's own choice
-    for (int k = 0; k < K; ++k) {
-      const int idx = __shfl_sync(0xffffffffu, my_idx, k);
-      const float da = __shfl_sync(0xffffffffu, my_da, k);
-      const int owner = idx < 0 ? 0 : idx / NI;
-      float ex = 0.f;
+    total = group_sum<G>(total);
+    const float inv_total = inverse(total);
+    const float cmean = group_sum<G>(cdot) * inv_total;
+    float chosen = 0.f, adot = 0.f;
 #pragma unroll
-      for (int i = 0; i < NI; ++i)
-        if (e0 + i == idx) { d[i] = da; ex = x[i]; }
-      ex = __shfl_sync(0xffffffffu, ex, owner);
-      if (lane == k && idx >= 0) my_ex = ex;
+    for (int j = 0; j < kPer; ++j) {
+      xc[j] = idx[j] >= 0 ? exp_neg(xc[j] - top) : 0.f;
+      chosen += xc[j];
+      adot = fmaf(xc[j], da[j], adot);
     }
-    // sum over the choices of alpha dalpha (renorm), or of p dalpha
-    const float den = renorm ? warp_sum(my_ex) : total;
-    const float mean = warp_sum(my_ex * my_da) / den;
-    float cmean = 0.f;
+    // mean of dalpha under alpha (renorm), or under p
+    adot = group_sum<G>(adot);
+    const float inv_a = renorm ? inverse(group_sum<G>(chosen)) : inv_total;
+    const float mean = adot * inv_a;
+    // what p_e is multiplied by, but for its own balance cost
+    const float common = kz * (top + __logf(total)) - cmean - (renorm ? 0.f : mean);
+    T* out = dlogits + t * E;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) cmean = fmaf(x[i] * inv_total, cost[i], cmean);
-    cmean = warp_sum(cmean);
-    const float zterm = kz * (top + logf(total));
-    // lanes whose experts were chosen: under renorm only they see dalpha
-    uint32_t chosen = 0;
-    if (renorm) {
-      for (int k = 0; k < K; ++k) {
-        const int idx = __shfl_sync(0xffffffffu, my_idx, k);
+    for (int c = 0; c < NI / S::kVec; ++c) {
+      const int e = S::expert(c * S::kVec, gl);
+      alignas(16) T v[S::kVec];
 #pragma unroll
-        for (int i = 0; i < NI; ++i)
-          if (e0 + i == idx) chosen |= 1u << i;
+      for (int i = 0; i < S::kVec; ++i) {
+        const int s = c * S::kVec + i;
+        v[i] = (T)(use ? x[s] * inv_total * (cost[s] + common) : 0.f);
+      }
+      if (real) {
+        if (out_vec && e + S::kVec <= E) {
+          copy_bytes<S::kVec * (int)sizeof(T)>(out + e, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < S::kVec; ++i)
+            if (e + i < E) out[e + i] = v[i];
+        }
       }
     }
+    __syncwarp();  // the choices' elements are written after the row's
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      if (e0 + i >= E) continue;
-      const float p = x[i] * inv_total;
-      float v = p * (cost[i] - cmean + zterm);
-      if (renorm) {
-        if (chosen >> i & 1) v = fmaf(x[i] / den, d[i] - mean, v);
-      } else {
-        v = fmaf(p, d[i] - mean, v);
+    for (int j = 0; j < kPer; ++j) {
+      if (idx[j] >= 0 && use && real) {
+        const float p = xc[j] * inv_total;
+        const float base = p * (kb * (float)counts[idx[j]] + common);
+        const float own = xc[j] * inv_a * (renorm ? da[j] - mean : da[j]);
+        out[idx[j]] = (T)(base + own);
       }
-      store_logit(dlogits + t * E + e0 + i, use ? v : 0.f);
     }
   }
 }
@@ -337,56 +581,99 @@ static lrm_status check_aligned(std::initializer_list<const void*> ptrs) {
   return LRM_OK;
 }
 
-template <typename T, int NI>
+// Rows begin on a multiple of a lane's chunk (the base is 16-byte aligned).
+template <typename T, int NI, int G>
+static bool chunks_aligned(int64_t stride) {
+  return stride % RowShape<T, NI, G>::kVec == 0;
+}
+
+template <typename T, int NI, int G>
 static lrm_status launch_route(const lrm_router* r, const void* logits, const uint8_t* mask,
                                int32_t* topk_idx, float* alpha, int32_t* counts,
                                float* prob_sum, float* loss, void* ws, cudaStream_t cs) {
   const bool stats = counts != nullptr;
-  // as many warps as tokens up to 32 a CTA and one CTA an SM, the rounds even
-  const int max_warps = NI >= 32 ? 16 : 32;
-  const int64_t ctas = std::min(num_sms(), kRouterMaxCtas);
-  const int64_t rounds = std::max<int64_t>(1, (r->T + ctas * max_warps - 1) / (ctas * max_warps));
-  const int64_t need = std::max<int64_t>(1, (r->T + rounds - 1) / rounds);
-  const int nwarp = (int)std::min<int64_t>(max_warps, need);
-  const int grid = (int)((need + nwarp - 1) / nwarp);
-  float* part_p = reinterpret_cast<float*>((char*)ws + kWsHeaderBytes);
-  int32_t* part_c = reinterpret_cast<int32_t*>(part_p + (size_t)kRouterMaxCtas * r->E);
-  float* part_z = reinterpret_cast<float*>(part_c + (size_t)kRouterMaxCtas * r->E);
-  auto kern = stats ? route_kernel<T, NI, true> : route_kernel<T, NI, false>;
-  const size_t smem = stats ? ((size_t)nwarp * r->E + r->E + nwarp) * 4 : 0;
+  constexpr int kMaxWarps = router_threads<T>(NI) / 32, kTokens = 32 / G;
+  const int64_t warps = std::max<int64_t>(1, ((int64_t)r->T + kTokens - 1) / kTokens);
+  int nwarp;
+  int64_t grid;
+  if (stats) {
+    // one CTA an SM at most (each leaves a row for the last sums), its warps
+    // in even rounds; a single CTA, without that last step, up to its warps
+    const int64_t ctas = std::min(num_sms(), kRouterMaxCtas);
+    const int64_t rounds = (warps + ctas * kMaxWarps - 1) / (ctas * kMaxWarps);
+    const int64_t need = (warps + rounds - 1) / rounds;
+    nwarp = (int)std::min(need, std::max<int64_t>(std::min(16, kMaxWarps), (need + ctas - 1) / ctas));
+    grid = (need + nwarp - 1) / nwarp;
+  } else {
+    nwarp = (int)std::min<int64_t>(4, warps);  // a warp for each scheduler of an SM
+    grid = std::min<int64_t>((warps + nwarp - 1) / nwarp, 1 << 30);
+  }
+  float2* part = reinterpret_cast<float2*>((char*)ws + kWsHeaderBytes);
+  float* part_z = reinterpret_cast<float*>(part + (size_t)kRouterMaxCtas * r->E);
+  auto kern = stats ? route_kernel<T, NI, G, true> : route_kernel<T, NI, G, false>;
+  const size_t smem = stats ? ((size_t)nwarp + 1) * r->E * 4 : 0;
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
           cudaSuccess)
     return LRM_ERR_CUDA;
-  if (launch_k(kern, dim3(grid), dim3(nwarp * 32), smem, cs, (const T*)logits, mask, r->T, r->E,
-               r->K, r->stride, r->renorm, r->balance_coef, r->z_coef, topk_idx, alpha, counts,
-               prob_sum, loss, part_p, part_c, part_z, router_ticket(ws)) != cudaSuccess) {
+  if (launch_k(kern, dim3((unsigned)grid), dim3(nwarp * 32), smem, cs, (const T*)logits, mask,
+               r->T, r->E, r->K, r->stride, (int)chunks_aligned<T, NI, G>(r->stride), r->renorm,
+               r->balance_coef, r->z_coef, topk_idx, alpha, counts, prob_sum, loss, part, part_z) != cudaSuccess) {
     (void)cudaGetLastError();
     return LRM_ERR_CUDA;
   }
+  if (stats && grid > 1)
+    launch_k(route_sums_kernel, dim3(kSumCtas), dim3(kSumThreads), 0, cs, (const float2*)part,
+             (const float*)part_z, (int)grid, r->E, r->K, r->balance_coef, r->z_coef, counts,
+             prob_sum, loss);
   return launch_status();
 }
 
-template <typename T, int NI>
+template <typename T, int NI, int G>
 static lrm_status launch_route_bwd(const lrm_router* r, const void* logits, const uint8_t* mask,
                                    const int32_t* topk_idx, const int32_t* counts,
                                    const float* dalpha, const float* dloss, void* dlogits,
                                    int32_t* err, cudaStream_t cs) {
-  const int64_t blocks = std::min<int64_t>(((int64_t)r->T + 7) / 8, (int64_t)num_sms() * 8);
-  launch_k(route_bwd_kernel<T, NI>, dim3((unsigned)blocks), dim3(256), 0, cs, (const T*)logits,
-           mask, topk_idx, counts, dalpha, dloss, r->T, r->E, r->K, r->stride, r->renorm,
-           r->balance_coef, r->z_coef, (T*)dlogits, err);
+  constexpr int kTokens = 32 / G * (kRouteBwdThreads / 32);  // tokens a CTA and round
+  const int64_t blocks =
+      std::min<int64_t>(((int64_t)r->T + kTokens - 1) / kTokens, (int64_t)num_sms() * 8);
+  launch_k(route_bwd_kernel<T, NI, G>, dim3((unsigned)blocks), dim3(kRouteBwdThreads), 0, cs,
+           (const T*)logits, mask, topk_idx, counts, dalpha, dloss, r->T, r->E, r->K, r->stride,
+           (int)chunks_aligned<T, NI, G>(r->stride), (int)chunks_aligned<T, NI, G>(r->E),
+           r->renorm, r->balance_coef, r->z_coef, (T*)dlogits, err);
   return launch_status();
 }
 
-// Experts a lane: the smallest power of two that covers E with 32 lanes.
-#define LRM_ROUTER_NI(call, T)            \
-  (r->E <= 32    ? call<T, 1>             \
-   : r->E <= 64  ? call<T, 2>             \
-   : r->E <= 128 ? call<T, 4>             \
-   : r->E <= 256 ? call<T, 8>             \
-   : r->E <= 512 ? call<T, 16>            \
-                 : call<T, 32>)
+using RouteFn = lrm_status (*)(const lrm_router*, const void*, const uint8_t*, int32_t*, float*,
+                               int32_t*, float*, float*, void*, cudaStream_t);
+
+template <typename T>
+static RouteFn pick_route(const lrm_router* r) {
+  // From this many tokens on several share a warp
+  const bool many = (int64_t)r->T > (int64_t)num_sms() * 16;
+  if (many && r->E <= 128 && r->K <= 8) {
+    if (r->E <= 32) return launch_route<T, 4, 8>;
+    if (r->E <= 64) return launch_route<T, 8, 8>;
+    return launch_route<T, 16, 8>;
+  }
+  if (many && r->E > 128 && r->E <= 256 && r->K <= 16) return launch_route<T, 16, 16>;
+  if (r->E <= 32) return launch_route<T, 1, 32>;
+  if (r->E <= 64) return launch_route<T, 2, 32>;
+  if (r->E <= 128) return launch_route<T, 4, 32>;
+  if (r->E <= 256) return launch_route<T, 8, 32>;
+  if (r->E <= 512) return launch_route<T, 16, 32>;
+  return launch_route<T, 32, 32>;
+}
+
+template <typename T>
+static auto pick_route_bwd(const lrm_router* r) {
+  if (r->E <= 32) return launch_route_bwd<T, 4, 8>;
+  if (r->E <= 64) return launch_route_bwd<T, 8, 8>;
+  if (r->E <= 128) return launch_route_bwd<T, 16, 8>;
+  if (r->E <= 256) return launch_route_bwd<T, 16, 16>;
+  if (r->E <= 512) return launch_route_bwd<T, 16, 32>;
+  return launch_route_bwd<T, 32, 32>;
+}
 
 }  // namespace lrm
 
@@ -411,8 +698,7 @@ extern "C" lrm_status lrm_route(const lrm_router* r, const void* logits, const u
     return st;
   if (r->T == 0 && !counts) return LRM_OK;
   cudaStream_t cs = (cudaStream_t)stream;
-  auto go = r->dtype == LRM_BF16 ? LRM_ROUTER_NI(launch_route, __nv_bfloat16)
-                                 : LRM_ROUTER_NI(launch_route, float);
+  auto go = r->dtype == LRM_BF16 ? pick_route<__nv_bfloat16>(r) : pick_route<float>(r);
   return go(r, logits, mask, topk_idx, alpha, counts, prob_sum, loss, ws, cs);
 }
 
@@ -429,7 +715,6 @@ extern "C" lrm_status lrm_route_bwd(const lrm_router* r, const void* logits, con
   if ((st = check_aligned({logits, topk_idx, counts, dalpha, dloss, dlogits})) != LRM_OK)
     return st;
   cudaStream_t cs = (cudaStream_t)stream;
-  auto go = r->dtype == LRM_BF16 ? LRM_ROUTER_NI(launch_route_bwd, __nv_bfloat16)
-                                 : LRM_ROUTER_NI(launch_route_bwd, float);
+  auto go = r->dtype == LRM_BF16 ? pick_route_bwd<__nv_bfloat16>(r) : pick_route_bwd<float>(r);
   return go(r, logits, mask, topk_idx, counts, dalpha, dloss, dlogits, error_word(ws), cs);
 }
