@@ -353,6 +353,7 @@ route_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask, int
 // every CTA an eighth of the experts, 16 experts at a time by 32 shares of the
 // rows; the CTAs' parts of the loss meet in the first one's shared memory.
 constexpr int kSumCtas = 8, kSumThreads = 512, kSumCols = 16;
+static_assert(kRouterMaxCtas % 32 == 0 && kSumThreads / kSumCols == 32, "whole shares");
 __global__ void __cluster_dims__(kSumCtas, 1, 1) __launch_bounds__(kSumThreads)
 route_sums_kernel(const float2* __restrict__ part, const float* __restrict__ part_z, int rows,
                   int E, int K, float balance_coef, float z_coef, int32_t* __restrict__ counts,
@@ -368,29 +369,37 @@ route_sums_kernel(const float2* __restrict__ part, const float* __restrict__ par
   const int begin = rank * per, end = min(E, begin + per);
   const int col = threadIdx.x % kSumCols, share = threadIdx.x / kSumCols;
   float z = 0.f;
-  if (rank == 0 && warp == 0)
-    for (int r = lane; r < rows; r += 32) z += part_z[r];
+  if (rank == 0 && warp == 0) {
+#pragma unroll
+    for (int k = 0; k < kRouterMaxCtas / 32; ++k)
+      z += lane + 32 * k < rows ? part_z[lane + 32 * k] : 0.f;
+  }
   float dot = 0.f, cnt = 0.f;
   int buf = 0;
   for (int e0 = begin; e0 < end; e0 += kSumCols, buf ^= 1) {
+    // every load before any use
+    constexpr int kShares = kSumThreads / kSumCols;
+    float2 v[kRouterMaxCtas / kShares];
+#pragma unroll
+    for (int k = 0; k < kRouterMaxCtas / kShares; ++k) {
+      const int r = share + k * kShares;
+      v[k] = e0 + col < end && r < rows ? part[(int64_t)r * E + e0 + col] : make_float2(0.f, 0.f);
+    }
     float s = 0.f;
     int c = 0;
-    if (e0 + col < end) {
-#pragma unroll 5
-      for (int r = share; r < rows; r += kSumThreads / kSumCols) {
-        const float2 v = part[(int64_t)r * E + e0 + col];
-        s += v.x;
-        c += __float_as_int(v.y);
-      }
+#pragma unroll
+    for (int k = 0; k < kRouterMaxCtas / kShares; ++k) {
+      s += v[k].x;
+      c += __float_as_int(v[k].y);
     }
     s += __shfl_xor_sync(0xffffffffu, s, 16);
     c += __shfl_xor_sync(0xffffffffu, c, 16);
     if (lane < kSumCols) sm[buf][warp][lane] = make_float2(s, __int_as_float(c));
     __syncthreads();
     // warp w adds column w
-    const float2 v = sm[buf][lane % kWarps][warp];
-    s = v.x;
-    c = __float_as_int(v.y);
+    const float2 u = sm[buf][lane % kWarps][warp];
+    s = u.x;
+    c = __float_as_int(u.y);
 #pragma unroll
     for (int o = 8; o > 0; o >>= 1) {
       s += __shfl_xor_sync(0xffffffffu, s, o);
