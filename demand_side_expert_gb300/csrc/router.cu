@@ -206,14 +206,156 @@ struct KeyLists {
   }
 };
 
-// Threads of a routing CTA: what NI experts a lane leave registers for.
-template <typename T>
-constexpr int router_threads(int ni) {
-  return ni <= 8 ? 1024 : ni == 16 ? (sizeof(T) == 2 ? 1024 : 512) : 256;
+// Choices by merging, for tokens that share a warp: every lane sorts its keys
+// and keeps the KC >= K largest, then the token's lanes merge their lists
+// pairwise until all hold the token's. Minima and maxima on registers only, so
+// the keys are 32 bits: a logit's order with the expert id in the low bits (16
+// for bfloat16, where those are free; log2(NI G) for float32).
+__device__ __forceinline__ void exchange(uint32_t& a, uint32_t& b) {
+  const uint32_t hi = max(a, b), lo = min(a, b);
+  a = hi;
+  b = lo;
+}
+// Sorts v[0 .. N) descending (odd-even merge sort; N a power of two up to 8).
+template <int N>
+__device__ __forceinline__ void sort_desc(uint32_t* v) {
+#pragma unroll
+  for (int p = 1; p < N; p *= 2)
+#pragma unroll
+    for (int k = p; k >= 1; k /= 2)
+#pragma unroll
+      for (int j = k % p; j + k < N; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i)
+          if (i + j + k < N && (i + j) / (2 * p) == (i + j + k) / (2 * p))
+            exchange(v[i + j], v[i + j + k]);
+}
+// Sorts a bitonic sequence descending.
+template <int N>
+__device__ __forceinline__ void merge_desc(uint32_t* v) {
+#pragma unroll
+  for (int s = N / 2; s >= 1; s /= 2)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if ((i & s) == 0) exchange(v[i], v[i + s]);
+}
+// a := the N largest of two descending lists of N, descending.
+template <int N>
+__device__ __forceinline__ void top_of(uint32_t* a, const uint32_t* b) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) a[i] = max(a[i], b[N - 1 - i]);
+  merge_desc<N>(a);
+}
+// L sorted keys of this lane and of the lanes 1, 2, .. G / 2 away, KC kept.
+template <int G, int KC, int L, int O>
+__device__ __forceinline__ void merge_lanes(uint32_t (&v)[KC]) {
+  if constexpr (O < G) {
+    if constexpr (L < KC) {
+#pragma unroll
+      for (int i = 0; i < L; ++i) v[2 * L - 1 - i] = __shfl_xor_sync(0xffffffffu, v[i], O);
+      merge_desc<2 * L>(v);
+      merge_lanes<G, KC, 2 * L, 2 * O>(v);
+    } else {
+      uint32_t u[KC];
+#pragma unroll
+      for (int i = 0; i < KC; ++i) u[i] = __shfl_xor_sync(0xffffffffu, v[i], O);
+      top_of<KC>(v, u);
+      merge_lanes<G, KC, KC, 2 * O>(v);
+    }
+  }
 }
 
-template <typename T, int NI, int G, bool STATS>
-__global__ void __launch_bounds__(router_threads<T>(NI))
+template <typename T, int NI, int G, int KC>
+__device__ __forceinline__ uint32_t choose_merged(const float (&x)[NI], int gl, int E) {
+  using S = RowShape<T, NI, G>;
+  constexpr uint32_t kId = sizeof(T) == 2 ? 0xffffu : NI * G - 1;
+  static_assert((NI * G & (NI * G - 1)) == 0, "ids fill whole bits");
+  uint32_t key[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int e = S::expert(i, gl);
+    key[i] = e < E ? (order_key(x[i]) & ~kId) | (kId - (uint32_t)e) : 0u;
+  }
+  constexpr int L = NI < KC ? NI : KC;
+  uint32_t v[KC];
+#pragma unroll
+  for (int i = 0; i < NI; i += L) sort_desc<L>(key + i);
+#pragma unroll
+  for (int i = L; i < NI; i += L) top_of<L>(key, key + i);
+#pragma unroll
+  for (int i = 0; i < KC; ++i) v[i] = i < L ? key[i] : 0u;
+  merge_lanes<G, KC, L, 1>(v);
+  uint32_t mine = 0;  // lane k keeps the k-th choice
+#pragma unroll
+  for (int i = 0; i < KC; ++i) mine = gl == i ? v[i] : mine;
+  return mine;
+}
+
+// Mends choices by float32 keys whose order is not the logits'. Those whose
+// key (without the id) is above the last choice's are right as a set; the other
+// places go, one by one on the whole logits, to the row's experts with that
+// very key. Then a choice's place is its rank among the K.
+template <typename T, int NI, int G>
+__device__ __noinline__ void choose_again(const float (&x)[NI], int gl, int E, int K,
+                                          uint32_t mine, int& my_idx, float& my_x, int& place) {
+  using S = RowShape<T, NI, G>;
+  constexpr uint32_t kId = NI * G - 1;
+  const uint32_t last = __shfl_sync(0xffffffffu, mine, K - 1, G) & ~kId;
+  const uint32_t sure = __ballot_sync(0xffffffffu, gl < K && (mine & ~kId) > last);
+  const int lane = threadIdx.x & 31;
+  const int n = __popc(sure >> (lane & ~(G - 1)) & ((1u << G) - 1));
+  const int rounds = __reduce_max_sync(0xffffffffu, K - n);
+  uint32_t taken = 0;
+  for (int k = 0; k < rounds; ++k) {
+    uint32_t best = 0;
+    int at = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const uint32_t key = order_key(x[i]);
+      if (S::expert(i, gl) < E && (key & ~kId) == last && !(taken >> i & 1) && key > best) {
+        best = key;
+        at = i;
+      }
+    }
+    const uint32_t hi = group_max<G>(best);
+    // the lowest expert of the lanes that hold it
+    const uint32_t e = (uint32_t)S::expert(at, gl);
+    const uint32_t low = ~group_max<G>(best == hi ? ~e : 0u);
+    if (gl == n + k && gl < K) { my_idx = (int)low; my_x = key_value(hi); }
+    if (best == hi && e == low) taken |= 1u << at;
+  }
+  place = 0;
+  for (int j = 0; j < K; ++j) {
+    const float v = __shfl_sync(0xffffffffu, my_x, j, G);
+    const int e = __shfl_sync(0xffffffffu, my_idx, j, G);
+    place += v > my_x || (v == my_x && e < my_idx);
+  }
+}
+
+// Whether the choices by float32 keys whose low bits are the id's are the true
+// ones: descending, and nothing else in the row above the last of them. (Equal
+// logits have equal keys but for the id, which orders them.)
+template <int NI, int G>
+__device__ __forceinline__ bool choices_hold(const float (&x)[NI], int gl, int K, float my_x) {
+  const float last = __shfl_sync(0xffffffffu, my_x, K - 1, G);
+  const float next = __shfl_down_sync(0xffffffffu, my_x, 1, G);
+  int above = gl < K && my_x > last ? -1 : 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) above += x[i] > last;
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+  return above == 0 && !(gl + 1 < K && my_x < next);
+}
+
+// Threads of a routing CTA: what NI experts a lane leave registers for.
+template <typename T>
+constexpr int router_threads(int ni, int g) {
+  return ni <= 8 ? 1024 : ni == 16 ? (g < 32 || sizeof(T) == 2 ? 1024 : 512) : 256;
+}
+
+// KC: the length of the merged lists where several tokens share a warp (G < 32).
+template <typename T, int NI, int G, int KC, bool STATS>
+__global__ void __launch_bounds__(router_threads<T>(NI, G))
 route_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask, int ntok, int E,
              int K, int64_t stride, int vec, int renorm, float balance_coef, float z_coef,
              int32_t* __restrict__ topk_idx, float* __restrict__ alpha,
@@ -244,42 +386,58 @@ route_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask, int
     float x[NI];
     load_row<T, NI, G>(logits + t * stride, gl, E, vec, x);
     const bool masked = mask && mask[t] == 0;
-    KeyLists<typename C::Key, NI> list;
+    // lane k of the token gets its k-th choice: the expert and its logit
+    int my_idx = 0, place = gl;
+    float my_x = 0.f, top = 0.f;
+    if constexpr (G == 32) {
+      KeyLists<typename C::Key, NI> list;
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const int e = S::expert(i, gl);
-      list.key[i] = e < E ? C::make(x[i], e) : (typename C::Key)0;
-    }
-    list.sort();
-    // lane k of the token keeps its k-th choice
-    typename C::Key my_key = 0;
-    float top = 0.f;
-    for (int k = 0; k < K; ++k) {
-      const typename C::Key best = group_max<G>(list.front());
-      if (k == 0) top = C::value(best);
-      if (gl == k) my_key = best;
-      list.take(best);
+      for (int i = 0; i < NI; ++i) {
+        const int e = S::expert(i, gl);
+        list.key[i] = e < E ? C::make(x[i], e) : (typename C::Key)0;
+      }
+      list.sort();
+      typename C::Key my_key = 0;
+      for (int k = 0; k < K; ++k) {
+        const typename C::Key best = group_max<G>(list.front());
+        if (k == 0) top = C::value(best);
+        if (gl == k) my_key = best;
+        list.take(best);
+      }
+      my_idx = C::expert(my_key);
+      my_x = C::value(my_key);
+    } else {
+      const uint32_t mine = choose_merged<T, NI, G, KC>(x, gl, E);
+      if constexpr (sizeof(T) == 2) {
+        my_idx = ChoiceKey<T>::expert(mine);
+        my_x = ChoiceKey<T>::value(mine);
+      } else {
+        my_idx = (int)(NI * G - 1 - (mine & (NI * G - 1)));
+        my_x = gl < K ? fmaxf((float)logits[t * stride + my_idx], -CUDART_INF_F) : 0.f;
+        if (__any_sync(0xffffffffu, !choices_hold<NI, G>(x, gl, K, my_x)))
+          choose_again<T, NI, G>(x, gl, E, K, mine, my_idx, my_x, place);
+      }
+      top = group_fmax<G>(gl < K ? my_x : -CUDART_INF_F);
     }
     const bool use = takes_part<NI, G>(x, top, masked) && real;
     // p, its sum over the row, and the weights of the K choices
     float total = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      x[i] = S::expert(i, gl) < E ? exp_neg(x[i] - top) : 0.f;
+      x[i] = exp_neg(x[i] - top);  // 0 past E, where x is -inf
       total += x[i];
     }
     total = group_sum<G>(total);
     const float inv_total = inverse(total);
     const bool choice = gl < K;
-    float a = choice ? exp_neg(C::value(my_key) - top) : 0.f;
+    float a = choice ? exp_neg(my_x - top) : 0.f;
     // every lane of the warp takes part in the sum, whatever its token holds
     const float inv_a = renorm ? inverse(group_sum<G>(a)) : inv_total;
     // a NaN in the row makes every weight NaN, also where the choices' own sum has none
     a = total != total ? total : a * inv_a;
-    const int my_idx = C::expert(my_key);
     if (choice && real) {
-      topk_idx[t * K + gl] = my_idx;
-      alpha[t * K + gl] = use ? a : 0.f;
+      topk_idx[t * K + place] = my_idx;
+      alpha[t * K + place] = use ? a : 0.f;
     }
     if constexpr (STATS) {
       if (use) {
@@ -508,7 +666,7 @@ route_bwd_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask,
     float total = 0.f, cdot = 0.f;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      x[i] = S::expert(i, gl) < E ? exp_neg(x[i] - top) : 0.f;
+      x[i] = exp_neg(x[i] - top);  // 0 past E, where x is -inf
       total += x[i];
       cdot = fmaf(x[i], cost[i], cdot);
     }
@@ -596,12 +754,12 @@ static bool chunks_aligned(int64_t stride) {
   return stride % RowShape<T, NI, G>::kVec == 0;
 }
 
-template <typename T, int NI, int G>
+template <typename T, int NI, int G, int KC>
 static lrm_status launch_route(const lrm_router* r, const void* logits, const uint8_t* mask,
                                int32_t* topk_idx, float* alpha, int32_t* counts,
                                float* prob_sum, float* loss, void* ws, cudaStream_t cs) {
   const bool stats = counts != nullptr;
-  constexpr int kMaxWarps = router_threads<T>(NI) / 32, kTokens = 32 / G;
+  constexpr int kMaxWarps = router_threads<T>(NI, G) / 32, kTokens = 32 / G;
   const int64_t warps = std::max<int64_t>(1, ((int64_t)r->T + kTokens - 1) / kTokens);
   int nwarp;
   int64_t grid;
@@ -619,7 +777,7 @@ static lrm_status launch_route(const lrm_router* r, const void* logits, const ui
   }
   float2* part = reinterpret_cast<float2*>((char*)ws + kWsHeaderBytes);
   float* part_z = reinterpret_cast<float*>(part + (size_t)kRouterMaxCtas * r->E);
-  auto kern = stats ? route_kernel<T, NI, G, true> : route_kernel<T, NI, G, false>;
+  auto kern = stats ? route_kernel<T, NI, G, KC, true> : route_kernel<T, NI, G, KC, false>;
   const size_t smem = stats ? ((size_t)nwarp + 1) * r->E * 4 : 0;
   if (smem > 40 * 1024 &&
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
@@ -656,22 +814,28 @@ static lrm_status launch_route_bwd(const lrm_router* r, const void* logits, cons
 using RouteFn = lrm_status (*)(const lrm_router*, const void*, const uint8_t*, int32_t*, float*,
                                int32_t*, float*, float*, void*, cudaStream_t);
 
+template <typename T, int KC>
+static RouteFn pick_shared(int E) {
+  if (E <= 32) return launch_route<T, 4, 8, KC>;
+  if (E <= 64) return launch_route<T, 8, 8, KC>;
+  if (E <= 128) return launch_route<T, 16, 8, KC>;
+  return launch_route<T, 16, 16, KC>;
+}
+
 template <typename T>
 static RouteFn pick_route(const lrm_router* r) {
   // From this many tokens on several share a warp
-  const bool many = (int64_t)r->T > (int64_t)num_sms() * 16;
-  if (many && r->E <= 128 && r->K <= 8) {
-    if (r->E <= 32) return launch_route<T, 4, 8>;
-    if (r->E <= 64) return launch_route<T, 8, 8>;
-    return launch_route<T, 16, 8>;
-  }
-  if (many && r->E > 128 && r->E <= 256 && r->K <= 16) return launch_route<T, 16, 16>;
-  if (r->E <= 32) return launch_route<T, 1, 32>;
-  if (r->E <= 64) return launch_route<T, 2, 32>;
-  if (r->E <= 128) return launch_route<T, 4, 32>;
-  if (r->E <= 256) return launch_route<T, 8, 32>;
-  if (r->E <= 512) return launch_route<T, 16, 32>;
-  return launch_route<T, 32, 32>;
+  const bool many = (int64_t)r->T > (int64_t)num_sms() * 32;
+  if (many && r->E <= 256 && r->K <= 8)
+    return r->K <= 2   ? pick_shared<T, 2>(r->E)
+           : r->K <= 4 ? pick_shared<T, 4>(r->E)
+                       : pick_shared<T, 8>(r->E);
+  if (r->E <= 32) return launch_route<T, 1, 32, 0>;
+  if (r->E <= 64) return launch_route<T, 2, 32, 0>;
+  if (r->E <= 128) return launch_route<T, 4, 32, 0>;
+  if (r->E <= 256) return launch_route<T, 8, 32, 0>;
+  if (r->E <= 512) return launch_route<T, 16, 32, 0>;
+  return launch_route<T, 32, 32, 0>;
 }
 
 template <typename T>

@@ -22,25 +22,24 @@ from .pipeline import _TORCH_DTYPE, dtype_code
 
 def _need(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device):
     """A contiguous device tensor of this shape and type."""
-    if t.dtype is not dtype or tuple(t.shape) != shape or not t.is_contiguous() \
-            or t.device != device:
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name}: a contiguous {dtype} tensor {shape} on {device} is needed, got "
                          f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
     return t
 
 
-def _need_rows(t, name: str, cols: int, dtype: torch.dtype, device: torch.device,
-               rows: int) -> int:
+def _need_rows(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:
     """A device matrix whose rows are contiguous; returns its row stride."""
-    if t.dtype is not dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols \
-            or (cols > 1 and t.stride(1) != 1) or t.device != device:
-        raise ValueError(f"{name}: a {dtype} tensor ({rows}, {cols}) with contiguous rows on "
-                         f"{device} is needed, got {t.dtype} {tuple(t.shape)} strides "
-                         f"{t.stride()} on {t.device}")
-    stride = t.stride(0) if rows > 1 else max(t.stride(0), cols)
-    if stride < cols:
-        raise ValueError(f"{name}: rows overlap (stride {stride} for {cols} columns)")
-    return stride
+    if t.dtype is dtype and t.shape == shape and t.device == device:
+        rows, cols = shape
+        stride, step = t.stride()
+        if rows <= 1:  # the one row's stride means nothing
+            stride = cols
+        if (step == 1 or cols == 1) and stride >= cols:
+            return stride
+    raise ValueError(f"{name}: a {dtype} tensor {shape} with contiguous rows that do not overlap, "
+                     f"on {device}, is needed, got {t.dtype} {tuple(t.shape)} strides "
+                     f"{t.stride()} on {t.device}")
 
 
 def _device(device) -> torch.device:
@@ -64,6 +63,7 @@ class Router:
                  balance_coef: float = 0.01, z_coef: float = 0.0,
                  device: str | torch.device = "cuda"):
         self.T, self.E, self.K = T, E, K
+        self._shape = (T, E)
         self.tdtype = _TORCH_DTYPE[dtype_code(dtype)]
         self.desc = lrm.lrm_router(T, E, K, dtype_code(dtype), E, int(renorm), balance_coef,
                                    z_coef)
@@ -90,7 +90,7 @@ class Router:
         return self._dlogits
 
     def _inputs(self, logits, mask):
-        self.desc.stride = _need_rows(logits, "logits", self.E, self.tdtype, self.device, self.T)
+        self.desc.stride = _need_rows(logits, "logits", self._shape, self.tdtype, self.device)
         if mask is not None:
             if mask.dtype is torch.bool:
                 mask = mask.view(torch.uint8)
@@ -141,6 +141,7 @@ class AddRMSNorm:
                  q_cols: int | None = None, store_y: bool | None = None,
                  grad_dtype: str = "f32", device: str | torch.device = "cuda"):
         self.T, self.D = T, D
+        self._shape = (T, D)
         self.tdtype = _TORCH_DTYPE[dtype_code(dtype)]
         self.gdtype = _TORCH_DTYPE[dtype_code(grad_dtype)]
         self.desc = lrm.lrm_norm(T, D, dtype_code(dtype), dtype_code(grad_dtype), q_cols or 0,
@@ -193,10 +194,10 @@ class AddRMSNorm:
     def forward(self, x, w, residual=None, stream=None):
         """x, residual [T, D] (rows may be strided by a multiple of 8 elements), w [D]."""
         dt, dev = self.tdtype, self.device
-        self.desc.x_stride = _need_rows(x, "x", self.D, dt, dev, self.T)
+        self.desc.x_stride = _need_rows(x, "x", self._shape, dt, dev)
         h = None
         if residual is not None:
-            self.desc.res_stride = _need_rows(residual, "residual", self.D, dt, dev, self.T)
+            self.desc.res_stride = _need_rows(residual, "residual", self._shape, dt, dev)
             h = self.h
         _need(w, "w", (self.D,), dt, dev)
         lrm.lrm_add_rmsnorm(self.desc, x, residual, w, h, self.y, self.q, self.q_scale, self.rstd,
@@ -206,7 +207,7 @@ class AddRMSNorm:
         """dy [T, D]: the cotangent of y; dh: of the stored sum (the residual
         stream), or None. ``h``: the normed rows, self.h by default (pass x where
         there was no residual). Uses ``rstd`` of the last forward."""
-        dt, gt, dev, shape = self.tdtype, self.gdtype, self.device, (self.T, self.D)
+        dt, gt, dev, shape = self.tdtype, self.gdtype, self.device, self._shape
         h = self.h if h is None else _need(h, "h", shape, dt, dev)
         _need(dy, "dy", shape, gt, dev)
         if dh is not None:
