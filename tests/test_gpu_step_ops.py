@@ -135,6 +135,54 @@ def test_route_and_gradient(dev, T, E, K, dtype, off, renorm):
     close(to64(r.dlogits), want, lim + 1e-37, "dlogits")
 
 
+MANY = [(5000, 20, 1, "f32"), (6001, 32, 5, "bf16"), (5000, 60, 2, "bf16"), (5000, 64, 8, "f32"),
+        (7003, 100, 3, "bf16"), (9000, 128, 8, "f32"), (5000, 200, 4, "f32"), (5001, 256, 8, "bf16"),
+        (5000, 256, 12, "f32"), (5000, 130, 1, "f32")]
+
+
+@pytest.mark.parametrize("kind", ["normal", "equal", "near", "zeros", "closed", "nan"])
+@pytest.mark.parametrize("T,E,K,dtype", MANY)
+def test_route_many_tokens(dev, T, E, K, dtype, kind):
+    """Enough tokens that they share warps, and logits that are hard to rank: equal
+    ones, ones that differ in the last bits only, zeros of both signs, mostly closed
+    experts, NaN. The choices have to be those of a stable sort, bit for bit."""
+    gen = torch.Generator().manual_seed(E)
+    x = torch.randn(T, E, generator=gen)
+    if kind == "equal":
+        x = (x * 2).round() / 2
+    if kind == "near":
+        x = 1 + torch.randint(0, 300, (T, E), generator=gen) * 2.0 ** -23
+        x = torch.where(torch.rand(T, E, generator=gen) < 0.3, x, -x)
+    if kind == "zeros":
+        x = torch.where(torch.rand(T, E, generator=gen) < 0.5, 0.0, -0.0)
+    if kind == "closed":
+        x = x.masked_fill(torch.rand(T, E, generator=gen) < 0.95, -math.inf)
+    if kind == "nan":
+        x = x.masked_fill(torch.rand(T, E, generator=gen) < 0.01, math.nan)
+    x = x.to(DT[dtype])
+    r, _ = route_on(dev, x, K, K > 2)
+    x64 = to64(x)
+    idx = so.topk(x64, K)
+    assert np.array_equal(r.topk_idx.cpu().numpy(), idx)
+    use = so.takes_part(x64)
+    counts = np.bincount(idx[use].reshape(-1), minlength=E)
+    assert np.array_equal(r.counts.cpu().numpy(), counts)
+    good = use & ~np.isnan(x64).any(1)
+    top = np.where(good, np.max(np.where(np.isnan(x64), -np.inf, x64), 1), 0.0)
+    with np.errstate(invalid="ignore"):
+        p = np.where(good[:, None], np.exp(x64 - top[:, None]), 0.0)
+    p /= np.where(good, p.sum(1), 1.0)[:, None]
+    want = np.take_along_axis(p, idx.astype(np.int64), 1)
+    if K > 2:
+        want = want / np.where(good, want.sum(1), 1.0)[:, None]
+    got = to64(r.alpha)
+    close(got[good], want[good], 2 * router_tol(x64) * want[good] + 1e-37, "alpha")
+    assert np.isnan(got[use & ~good]).all() and (got[~use] == 0).all()
+    if kind != "nan":
+        close(to64(r.prob_sum), p.sum(0), (router_tol(x64) + (T + 8) * U) * p.sum(0) + 1e-37,
+              "prob_sum")
+
+
 def test_route_gradient_matches_differences(dev):
     """The kernel's own gradient against central differences of the float64 loss."""
     T, E, K = 4, 9, 3
