@@ -40,8 +40,7 @@ struct AdamSeg {
   void *m, *v;
   float *m_scale, *v_scale;
   int64_t n;
-  float keep;       // 1 - lr wd
-  uint32_t first;   // first chunk of the launch that is this tensor's
+  float keep;  // 1 - lr wd
 };
 struct AdamStep {
   int nseg;
@@ -50,6 +49,7 @@ struct AdamStep {
 };
 template <int SEGS>
 struct AdamArgs : AdamStep {
+  uint32_t first[SEGS];  // first chunk of the launch that is the tensor's
   AdamSeg seg[SEGS];
 };
 static_assert(sizeof(AdamArgs<kAdamMany>) <= 32764, "kernel parameters");
@@ -142,11 +142,11 @@ adamw_kernel(const __grid_constant__ AdamArgs<SEGS> a) {
   int lo = 0, hi = a.nseg - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a.seg[mid].first <= blockIdx.x) lo = mid;
+    if (a.first[mid] <= blockIdx.x) lo = mid;
     else hi = mid - 1;
   }
   const AdamSeg& sg = a.seg[lo];
-  const int64_t at = (int64_t)(blockIdx.x - sg.first) * kAdamChunk + threadIdx.x * kAdamUnit;
+  const int64_t at = (int64_t)(blockIdx.x - a.first[lo]) * kAdamChunk + threadIdx.x * kAdamUnit;
   const int lane = threadIdx.x & 31;
   const int64_t left = sg.n - at;
   const int count = left >= 8 ? 8 : left > 0 ? (int)left : 0;
@@ -252,8 +252,9 @@ static lrm_status adam_launch(const AdamStep& step, double lr, int kind,
     }
     if (end) break;
     const lrm_adamw_tensor& t = tensors[i];
+    a.first[a.nseg] = (uint32_t)chunks;
     a.seg[a.nseg++] = {t.param, t.grad, t.master, t.m, t.v, t.m_scale, t.v_scale, t.n,
-                       (float)(1.0 - lr * t.weight_decay), (uint32_t)chunks};
+                       (float)(1.0 - lr * t.weight_decay)};
     chunks += more;
   }
   return LRM_OK;

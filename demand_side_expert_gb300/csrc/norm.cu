@@ -260,7 +260,6 @@ __global__ void __launch_bounds__(kNormThreads)
 rmsnorm_bwd_kernel(const G* dy, const G* dh, const T* __restrict__ h, const T* __restrict__ w,
                    const float* __restrict__ rstd, G* dx, float* __restrict__ dw_part, int rows,
                    int D, int tpr, int stages) {
-  pdl_begin();  // predecessor complete before any global access
   constexpr int TP = sizeof(T) / 2, GP = sizeof(G) / 2;  // 16-byte pieces of a unit
   extern __shared__ uint4 ring[];  // [stages][pieces][threads]
   __shared__ float4 red[2][kNormThreads / 64][kNormThreads / 128];
@@ -273,15 +272,7 @@ rmsnorm_bwd_kernel(const G* dy, const G* dh, const T* __restrict__ h, const T* _
   const int per_unit = TP + GP * (dh ? 2 : 1), pieces = UPT * per_unit;
   const int units = D / kUnit;
   const float inv_d = 1.f / (float)D;
-  Unit8<T> vw[UPT];
-  float acc[UPT][kUnit];
-#pragma unroll
-  for (int i = 0; i < UPT; ++i) {
-    vw[i].zero();
-    if (tl + i * tpr < units) vw[i].load_cached(w + (tl + i * tpr) * kUnit);
-#pragma unroll
-    for (int j = 0; j < kUnit; ++j) acc[i][j] = 0.f;
-  }
+  pdl_begin();  // predecessor complete before any global access
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring + threadIdx.x);
   auto copy_row = [&](int64_t r, int slot) {
     if (r < rows) {
@@ -312,6 +303,15 @@ rmsnorm_bwd_kernel(const G* dy, const G* dh, const T* __restrict__ h, const T* _
   int64_t base = (int64_t)blockIdx.x * groups;
   const int64_t dr = (int64_t)gridDim.x * groups;
   for (int i = 0; i < stages - 1; ++i) copy_row(base + row.group + i * dr, i);
+  Unit8<T> vw[UPT];
+  float acc[UPT][kUnit];
+#pragma unroll
+  for (int i = 0; i < UPT; ++i) {
+    vw[i].zero();
+    if (tl + i * tpr < units) vw[i].load_cached(w + (tl + i * tpr) * kUnit);
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) acc[i][j] = 0.f;
+  }
   float next_rs = base + row.group < rows ? __ldg(rstd + base + row.group) : 0.f;
   int slot = 0;
   for (; base < rows; base += dr) {
