@@ -205,6 +205,8 @@ static lrm_status check_tensor(const lrm_adamw_tensor& t) {
   if (!aligned16(t.param) || !aligned16(t.grad) || !aligned16(t.master) || !aligned16(t.m) ||
       !aligned16(t.v))
     return LRM_ERR_UNSUPPORTED;
+  if (((reinterpret_cast<uintptr_t>(t.m_scale) | reinterpret_cast<uintptr_t>(t.v_scale)) & 3u) != 0)
+    return LRM_ERR_UNSUPPORTED;
   // chunk numbers are 32-bit
   if (t.n > (int64_t)kAdamChunk * 0x7fffffff) return LRM_ERR_UNSUPPORTED;
   return LRM_OK;
@@ -271,6 +273,7 @@ extern "C" lrm_status lrm_adamw_step(const lrm_adamw* h, const lrm_adamw_tensor*
   if (!(h->beta1 >= 0 && h->beta1 < 1) || !(h->beta2 >= 0 && h->beta2 < 1) ||
       !(h->eps >= 0) || h->step < 1)
     return LRM_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(h->grad_scale) & 3u) != 0) return LRM_ERR_UNSUPPORTED;
   for (int i = 0; i < count; ++i) {
     const lrm_status st = check_tensor(tensors[i]);
     if (st != LRM_OK) return st;

@@ -291,13 +291,28 @@ __device__ __forceinline__ uint32_t choose_merged(const float (&x)[NI], int gl, 
   return mine;
 }
 
-// Mends choices by float32 keys whose order is not the logits'. Those whose
-// key (without the id) is above the last choice's are right as a set; the other
-// places go, one by one on the whole logits, to the row's experts with that
-// very key. Then a choice's place is its rank among the K.
+// What is wrong with choices by float32 keys, whose low bits are the id's: bit
+// 0, they do not descend; bit 1, the row has something above the least of them
+// that is not among them. (Equal logits have equal keys but for the id, which
+// orders them.)
+template <int NI, int G>
+__device__ __forceinline__ int choices_wrong(const float (&x)[NI], int gl, int K, float my_x) {
+  const float least = -group_fmax<G>(gl < K ? -my_x : -CUDART_INF_F);
+  const float next = __shfl_down_sync(0xffffffffu, my_x, 1, G);
+  int above = gl < K && my_x > least ? -1 : 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) above += x[i] > least;
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+  return (above != 0 ? 2 : 0) | (gl + 1 < K && my_x < next ? 1 : 0);
+}
+
+// The second fault: the choices whose key (without the id) is above the last
+// one's are right as a set; the other places go, one by one on the whole
+// logits, to the row's experts with that very key.
 template <typename T, int NI, int G>
 __device__ __noinline__ void choose_again(const float (&x)[NI], int gl, int E, int K,
-                                          uint32_t mine, int& my_idx, float& my_x, int& place) {
+                                          uint32_t mine, int& my_idx, float& my_x) {
   using S = RowShape<T, NI, G>;
   constexpr uint32_t kId = NI * G - 1;
   const uint32_t last = __shfl_sync(0xffffffffu, mine, K - 1, G) & ~kId;
@@ -324,27 +339,18 @@ __device__ __noinline__ void choose_again(const float (&x)[NI], int gl, int E, i
     if (gl == n + k && gl < K) { my_idx = (int)low; my_x = key_value(hi); }
     if (best == hi && e == low) taken |= 1u << at;
   }
-  place = 0;
+}
+
+// The first fault: a choice's place is its rank among the token's K.
+template <int G>
+__device__ __forceinline__ int rank_of(int K, int my_idx, float my_x) {
+  int place = 0;
   for (int j = 0; j < K; ++j) {
     const float v = __shfl_sync(0xffffffffu, my_x, j, G);
     const int e = __shfl_sync(0xffffffffu, my_idx, j, G);
     place += v > my_x || (v == my_x && e < my_idx);
   }
-}
-
-// Whether the choices by float32 keys whose low bits are the id's are the true
-// ones: descending, and nothing else in the row above the last of them. (Equal
-// logits have equal keys but for the id, which orders them.)
-template <int NI, int G>
-__device__ __forceinline__ bool choices_hold(const float (&x)[NI], int gl, int K, float my_x) {
-  const float last = __shfl_sync(0xffffffffu, my_x, K - 1, G);
-  const float next = __shfl_down_sync(0xffffffffu, my_x, 1, G);
-  int above = gl < K && my_x > last ? -1 : 0;
-#pragma unroll
-  for (int i = 0; i < NI; ++i) above += x[i] > last;
-#pragma unroll
-  for (int o = 1; o < G; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
-  return above == 0 && !(gl + 1 < K && my_x < next);
+  return place;
 }
 
 // Threads of a routing CTA: what NI experts a lane leave registers for.
@@ -414,8 +420,12 @@ route_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask, int
       } else {
         my_idx = (int)(NI * G - 1 - (mine & (NI * G - 1)));
         my_x = gl < K ? fmaxf((float)logits[t * stride + my_idx], -CUDART_INF_F) : 0.f;
-        if (__any_sync(0xffffffffu, !choices_hold<NI, G>(x, gl, K, my_x)))
-          choose_again<T, NI, G>(x, gl, E, K, mine, my_idx, my_x, place);
+        const int wrong = choices_wrong<NI, G>(x, gl, K, my_x);
+        if (__any_sync(0xffffffffu, wrong)) {
+          if (__any_sync(0xffffffffu, wrong & 2))
+            choose_again<T, NI, G>(x, gl, E, K, mine, my_idx, my_x);
+          place = rank_of<G>(K, my_idx, my_x);
+        }
       }
       top = group_fmax<G>(gl < K ? my_x : -CUDART_INF_F);
     }

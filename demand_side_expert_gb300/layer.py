@@ -234,7 +234,8 @@ class AdamW:
     parameters.
 
     The state lives in flat buffers over all tensors, each tensor beginning on a
-    whole block of 256: ``m``, ``v`` (float32, or float8_e4m3fn with v holding the
+    whole block of 256 (the tensors' storage is taken at construction: one that
+    is given other storage needs a new AdamW, or ``set_grads``): ``m``, ``v`` (float32, or float8_e4m3fn with v holding the
     root), ``m_scale``, ``v_scale``, ``master`` (or None); tensor i holds
     [starts[i], starts[i] + numel).
     """

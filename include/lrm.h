@@ -478,7 +478,7 @@ lrm_status lrm_select_rate(const lrm_shape* shape, const float* score, const int
  *     three NULL: no statistics (the serving form; balance_coef, z_coef unused).
  * Limits: E <= 1024, K <= 32, T*K < 2^31, else LRM_ERR_UNSUPPORTED.
  * ws: lrm_router_workspace_bytes, header as everywhere (zeroed once with
- * lrm_clear_device_error; the statistics leave their ticket word at zero).
+ * lrm_clear_device_error).
  */
 typedef struct lrm_router {
   int32_t T, E, K;
@@ -538,8 +538,8 @@ lrm_status lrm_gate_grad(const lrm_shape* shape, const void* g, const void* y,
  *   h [T,D] dtype or NULL; y [T,D] dtype or NULL; q [T,D] e4m3 bytes and
  *     q_scale [T, ceil(D / q_cols)] float (one column for q_cols = 0), or both
  *     NULL; rstd [T] float or NULL (written, contiguous). y or q is required.
- * h or y may be x or res themselves (same pointer, contiguous rows); no other
- * overlap is allowed.
+ * h or y may be x or res themselves (the same pointer; LRM_ERR_INVALID_ARG where
+ * that input's rows are not contiguous); no other overlap is allowed.
  * Limits: D a multiple of 8 up to 16384, strides multiples of 8, q_cols one of
  * 0, 32, 64, 128, 256, else LRM_ERR_UNSUPPORTED.
  */
@@ -584,8 +584,8 @@ lrm_status lrm_add_rmsnorm_bwd(const lrm_norm* norm, const void* dy, const void*
  * holds e4m3(sqrt(v) / scale), with one scale = max(amax, 2^-100) / 448 for
  * each 256 consecutive values; a positive root is never stored as 0. Zero
  * codes and scales are a valid start. The step uses the unrounded new moments.
- * Buffers are the caller's, param, grad, master, m, v 16-byte aligned, not
- * overlapping. `step` counts from 1. It is read on the host: a captured graph
+ * Buffers are the caller's, param, grad, master, m, v 16-byte aligned, the scales
+ * 4-byte, not overlapping. `step` counts from 1. It is read on the host: a captured graph
  * replays the bias correction of the step it was captured with.
  */
 typedef enum lrm_state { LRM_STATE_F32 = 0, LRM_STATE_F8 = 1 } lrm_state;

@@ -213,6 +213,9 @@ def test_norm_refuses_pointers(lib):
     assert fwd(b, 256, 256, 256, 256, 256, 256, None, 256, None) == lib.LRM_ERR_INVALID_ARG
     assert fwd(b, None, 256, 256, 256, 256, None, None, 256, None) == lib.LRM_ERR_INVALID_ARG
     assert fwd(b, 256, 264, 256, 256, 256, None, None, 256, None) == lib.LRM_ERR_UNSUPPORTED
+    # in place over rows that are not contiguous
+    wide = ctypes.byref(_norm(lib, x_stride=128))
+    assert fwd(wide, 512, None, 256, None, 512, None, None, 256, None) == lib.LRM_ERR_INVALID_ARG
     # dy, dh, h, w, rstd, dx, dw, ws, bytes
     assert bwd(b, *[256] * 7, None, need, None) == lib.LRM_ERR_WORKSPACE
     assert bwd(b, *[256] * 7, 256, need - 1, None) == lib.LRM_ERR_WORKSPACE
@@ -239,6 +242,8 @@ def test_adamw_refuses(lib):
     assert call(param_dtype=9) == bad and call(master=256) == bad  # a master of a float32 param
     assert call(state=lib.LRM_STATE_F8, m_scale=None) == bad
     assert call(param=264) == no and call(m=264) == no
+    assert call(state=lib.LRM_STATE_F8, v_scale=258) == no
+    assert call(hyper=dict(grad_scale=257)) == no
     assert lib._lib.lrm_adamw_step(None, None, 0, None) == bad
 
 
