@@ -178,7 +178,12 @@ static lrm_status launch_gate(const lrm_shape* s, const void* g, const void* y,
   constexpr int64_t kPerSm = 4;  // CTAs that fit an SM's shared memory
   static_assert(kPerSm * (kSmem + 2048) <= 227 * 1024, "the rings of an SM's CTAs");
   const int64_t need = ((int64_t)s->T * TPT + kGateThreads - 1) / kGateThreads;
-  const int blocks = (int)std::min<int64_t>(need, num_sms() * kPerSm);
+  // More CTAs than fit at once, so that an SM which starts late or reads slowly
+  // gets fewer tokens. Behind lrm_route_bwd (T 16384 D 4096, both, us): 210, 187,
+  // 181 and 177 for 1, 4, 8 and 16 times as many as fit; a warp a token
+  // (D 256): 27.4, 24.0 and 24.5 for 1, 3 and 4.
+  constexpr int64_t kTimes = TPT == 32 ? 3 : 16;
+  const int blocks = (int)std::min<int64_t>(need, num_sms() * kPerSm * kTimes);
   auto kern = gate_grad_kernel<T, TPT, kGateSteps>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
       cudaSuccess) {
