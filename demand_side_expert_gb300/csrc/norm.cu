@@ -6,8 +6,10 @@
 //   dx = rstd (w dy - xhat mean(w dy xhat)) + dh,  dw = sum_t dy xhat,
 //   xhat = h rstd
 // The sum h is rounded to the layer type only where it is stored: the norm is
-// taken of the 32-bit sum. All of it is HBM-bound; a row is read once into
-// registers by one group of threads and everything is computed from there.
+// taken of the 32-bit sum. Few operations a byte: HBM-bound from some MB on
+// (T 32768 D 2048 bfloat16, residual and 8-bit rows: 472 MB in 71 us, 0.97 of the
+// copy bandwidth; T 16384 D 4096 backward, float32 gradients: 940 MB in 138 us,
+// 1.00), and bound by latency and launches below.
 #include <cuda_fp8.h>
 
 #include <algorithm>
@@ -108,7 +110,9 @@ __device__ __forceinline__ float row_reduce(float v, float (*red)[32], int slot)
 // row stays in registers from its loads to its stores. Many small CTAs keep an
 // SM loading while some of them sum: a persistent form with the rows copied
 // ahead into shared memory, as the backward pass has it, measured 101-113 us
-// against 74 us (T 32768 D 2048, residual, 8-bit rows).
+// against 71 us (T 32768 D 2048, residual, 8-bit rows). Every load of a row comes
+// before any use and the group of a unit is found by shifts: with branches
+// between the loads it took 91 us, with divisions 76.
 template <int TPR>
 constexpr int norm_threads() { return TPR < 64 ? 128 : TPR; }
 
@@ -538,23 +542,35 @@ static lrm_status launch_norm_bwd(const lrm_norm* n, const NormBwd& a, cudaStrea
   return launch_status();
 }
 
-// Threads a row and units a thread. Many rows: up to 4 units a thread (several
-// rows an SM keep it loading while one is summed). Few rows: one unit where a
-// CTA holds the row so, for the latency of a row is all there is. Measured
-// (bf16, residual, 8-bit rows, few | many, us): T 4 D 4096 2.7 | 4.0, T 1021
-// D 2048 5.2 | 5.7, T 32768 D 2048 97 | 75, T 16384 D 4096 113 | 74.
+// Threads a row and units a thread. Up to 16384 values an SM the latency of a
+// row is all there is: one unit a thread, where a CTA holds the row so. Beyond,
+// two units (several rows an SM keep it loading while one is summed); four where
+// that makes a row a warp's (a CTA for each row of 1024 columns takes longer to
+// start than to run) or keeps it to 256 threads. Measured (bf16, residual, 8-bit
+// rows, 1 | 2 | 4 units, us): T 4 D 4096 2.8 | 3.0 | 3.9, T 1021 D 2048 4.6 | 5.2 |
+// 5.1, T 2432 D 4096 14.6 | 12.2 | 12.9, T 32768 D 2048 90.7 | 70.8 | 72.1,
+// T 16384 D 4096 96.5 | 71.6 | 71.6, T 2432 D 8192 (2 | 4) 26.7 | 23.0. A bfloat16
+// row without a residual is half the bytes and wants four units: T 16384 D 4096,
+// y alone, 45.5 us with two and 41.2 with four.
 template <typename T>
 static lrm_status pick_norm(const lrm_norm* n, const NormFwd& a, cudaStream_t cs) {
-  const bool few = (int64_t)n->T <= (int64_t)num_sms() * 8;
   const int D = n->D;
+  const bool few = (int64_t)n->T * D <= (int64_t)num_sms() * 16384;
   if (D <= 32) return launch_norm<T, 4, 1>(n, a, cs);
   if (D <= 64) return launch_norm<T, 8, 1>(n, a, cs);
   if (D <= 128) return launch_norm<T, 16, 1>(n, a, cs);
   if (D <= 256) return launch_norm<T, 32, 1>(n, a, cs);
-  if (D <= 512) return few ? launch_norm<T, 64, 1>(n, a, cs) : launch_norm<T, 32, 2>(n, a, cs);
+  if (D <= 512) return launch_norm<T, 32, 2>(n, a, cs);
   if (D <= 1024) return few ? launch_norm<T, 128, 1>(n, a, cs) : launch_norm<T, 32, 4>(n, a, cs);
-  if (D <= 2048) return few ? launch_norm<T, 256, 1>(n, a, cs) : launch_norm<T, 64, 4>(n, a, cs);
-  if (D <= 4096) return few ? launch_norm<T, 512, 1>(n, a, cs) : launch_norm<T, 128, 4>(n, a, cs);
+  const bool light = sizeof(T) == 2 && !a.res;
+  if (D <= 2048)
+    return few     ? launch_norm<T, 256, 1>(n, a, cs)
+           : light ? launch_norm<T, 64, 4>(n, a, cs)
+                   : launch_norm<T, 128, 2>(n, a, cs);
+  if (D <= 4096)
+    return few     ? launch_norm<T, 512, 1>(n, a, cs)
+           : light ? launch_norm<T, 128, 4>(n, a, cs)
+                   : launch_norm<T, 256, 2>(n, a, cs);
   if (D <= 8192) return few ? launch_norm<T, 512, 2>(n, a, cs) : launch_norm<T, 256, 4>(n, a, cs);
   return launch_norm<T, 512, 4>(n, a, cs);
 }
