@@ -158,7 +158,7 @@ adamw_kernel(const __grid_constant__ AdamArgs<SEGS> a) {
   else adam_load<P>((const P*)sg.param + at, count, p);
   if constexpr (F8) {
     const int64_t blk = at / kAdamBlock;
-    const float ms = __ldg(sg.m_scale + blk), vs = __ldg(sg.v_scale + blk);
+    const float ms = __ldcs(sg.m_scale + blk), vs = __ldcs(sg.v_scale + blk);
     e4m3_load((const uint8_t*)sg.m + at, count, ms, m);
     e4m3_load((const uint8_t*)sg.v + at, count, vs, v);
 #pragma unroll

@@ -520,25 +520,25 @@ route_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask, int
   }
 }
 
-// Adds the routing CTAs' sums in CTA order and forms the losses: one cluster,
-// every CTA an eighth of the experts, 16 experts at a time by 32 shares of the
-// rows; the CTAs' parts of the loss meet in the first one's shared memory.
-constexpr int kSumCtas = 8, kSumThreads = 512, kSumCols = 16;
-static_assert(kRouterMaxCtas % 32 == 0 && kSumThreads / kSumCols == 32, "whole shares");
+// Adds the routing CTAs' sums in a fixed order and forms the losses: one cluster,
+// every CTA an eighth of the experts, 32 experts at a time (a lane each) by 16
+// shares of the rows (a warp each); the CTAs' parts of the loss meet in the first
+// one's shared memory. 2 us at E 128, launch included.
+constexpr int kSumCtas = 8, kSumThreads = 512, kSumWarps = kSumThreads / 32;
+static_assert(kRouterMaxCtas % 32 == 0, "whole shares");
 __global__ void __cluster_dims__(kSumCtas, 1, 1) __launch_bounds__(kSumThreads)
 route_sums_kernel(const float2* __restrict__ part, const float* __restrict__ part_z, int rows,
                   int E, int K, float balance_coef, float z_coef, int32_t* __restrict__ counts,
                   float* __restrict__ prob_sum, float* __restrict__ loss) {
-  pdl_begin();  // predecessor complete before any global access
-  constexpr int kWarps = kSumThreads / 32;
-  __shared__ float2 sm[2][kWarps][kSumCols];
+  constexpr int kWarps = kSumWarps;
+  __shared__ float2 sm[2][kWarps][33];
   __shared__ float2 red[kWarps];
   __shared__ float2 all[kSumCtas];  // (sum of counts P, sum of counts) of every CTA
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int rank = (int)cluster_ctarank();
   const int per = (E + kSumCtas - 1) / kSumCtas;
   const int begin = rank * per, end = min(E, begin + per);
-  const int col = threadIdx.x % kSumCols, share = threadIdx.x / kSumCols;
+  pdl_begin();  // predecessor complete before any global access
   float z = 0.f;
   if (rank == 0 && warp == 0) {
 #pragma unroll
@@ -547,28 +547,27 @@ route_sums_kernel(const float2* __restrict__ part, const float* __restrict__ par
   }
   float dot = 0.f, cnt = 0.f;
   int buf = 0;
-  for (int e0 = begin; e0 < end; e0 += kSumCols, buf ^= 1) {
+  for (int e0 = begin; e0 < end; e0 += 32, buf ^= 1) {
     // every load before any use
-    constexpr int kShares = kSumThreads / kSumCols;
-    float2 v[kRouterMaxCtas / kShares];
+    float2 v[kRouterMaxCtas / kWarps];
 #pragma unroll
-    for (int k = 0; k < kRouterMaxCtas / kShares; ++k) {
-      const int r = share + k * kShares;
-      v[k] = e0 + col < end && r < rows ? part[(int64_t)r * E + e0 + col] : make_float2(0.f, 0.f);
+    for (int k = 0; k < kRouterMaxCtas / kWarps; ++k) {
+      const int r = warp + k * kWarps;
+      v[k] = e0 + lane < end && r < rows ? part[(int64_t)r * E + e0 + lane]
+                                         : make_float2(0.f, 0.f);
     }
     float s = 0.f;
     int c = 0;
 #pragma unroll
-    for (int k = 0; k < kRouterMaxCtas / kShares; ++k) {
+    for (int k = 0; k < kRouterMaxCtas / kWarps; ++k) {
       s += v[k].x;
       c += __float_as_int(v[k].y);
     }
-    s += __shfl_xor_sync(0xffffffffu, s, 16);
-    c += __shfl_xor_sync(0xffffffffu, c, 16);
-    if (lane < kSumCols) sm[buf][warp][lane] = make_float2(s, __int_as_float(c));
+    sm[buf][warp][lane] = make_float2(s, __int_as_float(c));
     __syncthreads();
-    // warp w adds column w
-    const float2 u = sm[buf][lane % kWarps][warp];
+    // warp w adds experts 2 w and 2 w + 1, half a warp each
+    const int col = 2 * warp + lane / 16;
+    const float2 u = sm[buf][lane % 16][col];
     s = u.x;
     c = __float_as_int(u.y);
 #pragma unroll
@@ -576,14 +575,16 @@ route_sums_kernel(const float2* __restrict__ part, const float* __restrict__ par
       s += __shfl_xor_sync(0xffffffffu, s, o);
       c += __shfl_xor_sync(0xffffffffu, c, o);
     }
-    const int e = e0 + warp;
-    if (lane == 0 && e < end) {
+    const int e = e0 + col;
+    if (lane % 16 == 0 && e < end) {
       prob_sum[e] = s;
       counts[e] = c;
       dot = fmaf((float)c, s, dot);
       cnt += (float)c;
     }
   }
+  dot = warp_sum(dot);
+  cnt = warp_sum(cnt);
   if (lane == 0) red[warp] = make_float2(dot, cnt);
   __syncthreads();
   if (warp == 0) {

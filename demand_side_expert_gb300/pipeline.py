@@ -109,7 +109,8 @@ class RecalibratedExpertBackward:
     def gate_grad(self, g, stream=None) -> torch.Tensor:
         """Gradient of the routing weights [T, K] (float32) from the cotangent g
         [T, D] of the layer output and the rows ``y`` of the last forward."""
-        self._forward_buffers()
+        if getattr(self, "y", None) is None:
+            raise RuntimeError("gate_grad needs the expert outputs of a forward call")
         if getattr(self, "dalpha", None) is None:
             self.dalpha = torch.empty(max(self.T, 1), self.K, dtype=torch.float32,
                                       device=self.device)[: self.T]
