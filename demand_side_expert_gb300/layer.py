@@ -14,10 +14,25 @@ stream wrote or will read is the caller's to order, as for every call here.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import lrm
 from .pipeline import _TORCH_DTYPE, dtype_code
+
+_route, _route_bwd = lrm.entry("lrm_route"), lrm.entry("lrm_route_bwd")
+_norm, _norm_bwd = lrm.entry("lrm_add_rmsnorm"), lrm.entry("lrm_add_rmsnorm_bwd")
+
+
+def _owned(name: str) -> property:
+    """A buffer of the object's own. It cannot be replaced: its address is read once."""
+    attr = "_" + name
+    return property(lambda self: getattr(self, attr))
+
+
+def _address(t):
+    return None if t is None else t.data_ptr()
 
 
 def _need(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device):
@@ -76,12 +91,18 @@ class Router:
         def empty(*shape, dtype=torch.float32):
             return torch.empty(*shape, dtype=dtype, device=dev)
 
-        self.ws = empty(self.ws_bytes, dtype=torch.uint8)
-        self.topk_idx, self.alpha = empty(T, K, dtype=torch.int32), empty(T, K)
-        self.counts, self.prob_sum = empty(E, dtype=torch.int32), empty(E)
-        self.loss = empty(2)
+        self._ws = empty(self.ws_bytes, dtype=torch.uint8)
+        self._topk_idx, self._alpha = empty(T, K, dtype=torch.int32), empty(T, K)
+        self._counts, self._prob_sum = empty(E, dtype=torch.int32), empty(E)
+        self._loss = empty(2)
         self._dlogits = None
-        lrm.lrm_clear_device_error(self.ws, self.ws_bytes)
+        self._ref = ctypes.byref(self.desc)
+        self._at = tuple(t.data_ptr() for t in (self._topk_idx, self._alpha, self._counts,
+                                                self._prob_sum, self._loss, self._ws))
+        lrm.lrm_clear_device_error(self._ws, self.ws_bytes)
+
+    topk_idx, alpha, counts = _owned("topk_idx"), _owned("alpha"), _owned("counts")
+    prob_sum, loss, ws = _owned("prob_sum"), _owned("loss"), _owned("ws")
 
     @property
     def dlogits(self) -> torch.Tensor:
@@ -102,12 +123,11 @@ class Router:
         bool or uint8: tokens that are 0 there get weight 0 and count nowhere.
         ``stats=False`` skips counts and losses (serving)."""
         mask = self._inputs(logits, mask)
-        if stats:
-            lrm.lrm_route(self.desc, logits, mask, self.topk_idx, self.alpha, self.counts,
-                          self.prob_sum, self.loss, self.ws, self.ws_bytes, stream)
-        else:
-            lrm.lrm_route(self.desc, logits, mask, self.topk_idx, self.alpha, None, None, None,
-                          self.ws, self.ws_bytes, stream)
+        topk_idx, alpha, counts, prob_sum, loss, ws = self._at
+        if not stats:
+            counts = prob_sum = loss = None
+        _route(self._ref, logits.data_ptr(), _address(mask), topk_idx, alpha, counts, prob_sum,
+               loss, ws, self.ws_bytes, lrm.stream_address(stream))
 
     def backward(self, logits, dalpha=None, mask=None, dloss=None, stream=None):
         """The logits' gradient, from the choices and counts of the last ``route``
@@ -119,11 +139,13 @@ class Router:
             _need(dalpha, "dalpha", (self.T, self.K), torch.float32, self.device)
         if dloss is not None:
             _need(dloss, "dloss", (2,), torch.float32, self.device)
-        lrm.lrm_route_bwd(self.desc, logits, mask, self.topk_idx, self.counts, dalpha, dloss,
-                          self.dlogits, self.ws, self.ws_bytes, stream)
+        topk_idx, _, counts, _, _, ws = self._at
+        _route_bwd(self._ref, logits.data_ptr(), _address(mask), topk_idx, counts,
+                   _address(dalpha), _address(dloss), self.dlogits.data_ptr(), ws, self.ws_bytes,
+                   lrm.stream_address(stream))
 
     def device_error(self, stream=None) -> int:
-        return lrm.lrm_get_device_error(self.ws, self.ws_bytes, stream)
+        return lrm.lrm_get_device_error(self._ws, self.ws_bytes, stream)
 
 
 class AddRMSNorm:
@@ -141,7 +163,7 @@ class AddRMSNorm:
                  q_cols: int | None = None, store_y: bool | None = None,
                  grad_dtype: str = "f32", device: str | torch.device = "cuda"):
         self.T, self.D = T, D
-        self._shape = (T, D)
+        self._shape, self._columns = (T, D), (D,)
         self.tdtype = _TORCH_DTYPE[dtype_code(dtype)]
         self.gdtype = _TORCH_DTYPE[dtype_code(grad_dtype)]
         self.desc = lrm.lrm_norm(T, D, dtype_code(dtype), dtype_code(grad_dtype), q_cols or 0,
@@ -156,16 +178,21 @@ class AddRMSNorm:
         def empty(*shape, dtype=torch.float32):
             return torch.empty(*shape, dtype=dtype, device=dev)
 
-        self.rstd = empty(T)
+        self._rstd = empty(T)
         store_y = q_cols is None if store_y is None else store_y
         if q_cols is None and not store_y:
             raise ValueError("store_y=False leaves no output without q_cols")
-        self.y = empty(T, D, dtype=self.tdtype) if store_y else None
-        self.q = self.q_scale = None
+        self._y = empty(T, D, dtype=self.tdtype) if store_y else None
+        self._q = self._q_scale = None
         if q_cols is not None:
-            self.q = empty(T, D, dtype=torch.float8_e4m3fn)
-            self.q_scale = empty(T, -(-D // q_cols) if q_cols else 1)
+            self._q = empty(T, D, dtype=torch.float8_e4m3fn)
+            self._q_scale = empty(T, -(-D // q_cols) if q_cols else 1)
         self._h = self._dx = self._dw = self._ws = None
+        self._summed = False  # the last forward had a residual: h is its sum
+        self._ref = ctypes.byref(self.desc)
+        self._at = tuple(_address(t) for t in (self._y, self._q, self._q_scale, self._rstd))
+
+    y, q, q_scale, rstd = _owned("y"), _owned("q"), _owned("q_scale"), _owned("rstd")
 
     @property
     def h(self) -> torch.Tensor:
@@ -194,28 +221,37 @@ class AddRMSNorm:
     def forward(self, x, w, residual=None, stream=None):
         """x, residual [T, D] (rows may be strided by a multiple of 8 elements), w [D]."""
         dt, dev = self.tdtype, self.device
-        self.desc.x_stride = _need_rows(x, "x", self._shape, dt, dev)
-        h = None
+        desc = self.desc
+        desc.x_stride = _need_rows(x, "x", self._shape, dt, dev)
+        res = h = None
+        self._summed = residual is not None
         if residual is not None:
-            self.desc.res_stride = _need_rows(residual, "residual", self._shape, dt, dev)
-            h = self.h
-        _need(w, "w", (self.D,), dt, dev)
-        lrm.lrm_add_rmsnorm(self.desc, x, residual, w, h, self.y, self.q, self.q_scale, self.rstd,
-                            stream)
+            desc.res_stride = _need_rows(residual, "residual", self._shape, dt, dev)
+            res, h = residual.data_ptr(), self.h.data_ptr()
+        _need(w, "w", self._columns, dt, dev)
+        y, q, q_scale, rstd = self._at
+        _norm(self._ref, x.data_ptr(), res, w.data_ptr(), h, y, q, q_scale, rstd,
+              lrm.stream_address(stream))
 
     def backward(self, dy, w, dh=None, h=None, stream=None):
         """dy [T, D]: the cotangent of y; dh: of the stored sum (the residual
         stream), or None. ``h``: the normed rows, self.h by default (pass x where
         there was no residual). Uses ``rstd`` of the last forward."""
         dt, gt, dev, shape = self.tdtype, self.gdtype, self.device, self._shape
-        h = self.h if h is None else _need(h, "h", shape, dt, dev)
+        if h is not None:
+            _need(h, "h", shape, dt, dev)
+        elif self._summed:
+            h = self._h
+        else:
+            raise ValueError("h: the last forward had no residual, so pass its x")
         _need(dy, "dy", shape, gt, dev)
         if dh is not None:
             _need(dh, "dh", shape, gt, dev)
-        _need(w, "w", (self.D,), dt, dev)
+        _need(w, "w", self._columns, dt, dev)
         self._backward_buffers()
-        lrm.lrm_add_rmsnorm_bwd(self.desc, dy, dh, h, w, self.rstd, self._dx, self._dw, self._ws,
-                                self.ws_bytes, stream)
+        _norm_bwd(self._ref, dy.data_ptr(), _address(dh), h.data_ptr(), w.data_ptr(), self._at[3],
+                  self._dx.data_ptr(), self._dw.data_ptr(), self._ws.data_ptr(), self.ws_bytes,
+                  lrm.stream_address(stream))
 
 
 _STATE = {"f32": lrm.LRM_STATE_F32, "f8": lrm.LRM_STATE_F8}

@@ -184,6 +184,24 @@ def _check(fn: str, status: int):
         raise LrmError(fn, status)
 
 
+def entry(name: str):
+    """An entry point for callers that keep its arguments as ctypes ones (descriptors
+    by reference, addresses, the stream): no marshalling, the same errors."""
+    fn = getattr(_lib, name)
+
+    def call(*args):
+        status = fn(*args)
+        if status != LRM_OK:
+            raise LrmError(name, status)
+
+    return call
+
+
+def stream_address(stream=None) -> int:
+    """Address of a stream (a torch stream, an address, None: torch's current one)."""
+    return _s(stream)
+
+
 def make_shape(T: int, D: int, H: int, E: int, K: int, dtype: int) -> lrm_shape:
     return lrm_shape(T, D, H, E, K, dtype)
 

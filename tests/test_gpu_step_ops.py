@@ -567,6 +567,11 @@ def test_norm_refuses_tensors(dev):
         n.forward(x, w, residual=x[:, :32])
     with pytest.raises(ValueError):
         n.backward(x, w, h=x)  # float32 gradients are expected
+    n.forward(x, w)
+    with pytest.raises(ValueError):
+        n.backward(x.float(), w)  # no residual, no sum of one
+    with pytest.raises(AttributeError):
+        n.rstd = torch.zeros(4, device=dev)
 
 
 # -- AdamW --------------------------------------------------------------------------
