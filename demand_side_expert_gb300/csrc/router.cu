@@ -17,7 +17,7 @@
 // pipe while a CTA runs) and, for few tokens, latency. So many tokens share a
 // warp (G = 8 or 16) and few get a whole one. Measured at T 32768 E 128 K 8:
 // choices and weights 7.3 us (bfloat16) and 9.5 us (float32), with the
-// statistics 11.6 and 15.0 us, the gradient 7.4 and 8.6 us.
+// statistics 11.8 and 15.2 us, the gradient 6.8 and 7.4 us.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -626,26 +626,54 @@ route_bwd_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask,
   using S = RowShape<T, NI, G>;
   constexpr int kTokens = 32 / G;
   const int lane = threadIdx.x & 31, gl = lane % G;
-  // tokens that took part: every one chose K experts
-  int64_t pairs = 0;
-  for (int e = lane; e < E; e += 32) pairs += counts[e];
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
-  const float n = fmaxf((float)pairs / (float)K, 1.f);
-  const float d0 = dloss ? dloss[0] : 1.f, d1 = dloss ? dloss[1] : 1.f;
-  // d balance / d p_te = kb counts_e, and 2 c_z / n of the z-loss
-  const float kb = d0 * balance_coef * (float)E / (n * n * (float)K);
-  const float kz = d1 * 2.f * z_coef / n;
-  float cost[NI];
-#pragma unroll
-  for (int i = 0; i < NI; ++i) {
-    const int e = S::expert(i, gl);
-    cost[i] = e < E ? kb * (float)counts[e] : 0.f;
-  }
   const int nwarp = kRouteBwdThreads / 32;
   const int64_t step = (int64_t)gridDim.x * nwarp * kTokens;
-  for (int64_t first = ((int64_t)blockIdx.x * nwarp + (threadIdx.x >> 5)) * kTokens;
-       first < ntok; first += step) {
+  int64_t first = ((int64_t)blockIdx.x * nwarp + (threadIdx.x >> 5)) * kTokens;
+  // the lane's own choices of token t: read a round ahead, because their logits
+  // are read by them
+  int next[kPer];
+  auto read_choices = [&](int64_t t) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int k = j * G + gl;
+      next[j] = t < ntok && k < K ? topk_idx[t * K + k] : 0;
+    }
+  };
+  read_choices(first + lane / G);
+  // the token's lanes hold every expert's count once
+  float cost[NI];
+  int pairs = 0;
+#pragma unroll
+  for (int c = 0; c < NI / S::kVec; ++c) {
+    const int e = S::expert(c * S::kVec, gl);
+    alignas(16) int32_t v[S::kVec];
+    if (e + S::kVec <= E) {
+      constexpr int kWord = S::kVec * 4 < 16 ? S::kVec * 4 : 16;
+#pragma unroll
+      for (int i = 0; i < S::kVec * 4 / kWord; ++i)
+        copy_bytes<kWord>(v + i * (kWord / 4), counts + e + i * (kWord / 4));
+    } else {
+#pragma unroll
+      for (int i = 0; i < S::kVec; ++i) v[i] = e + i < E ? counts[e + i] : 0;
+    }
+#pragma unroll
+    for (int i = 0; i < S::kVec; ++i) {
+      cost[c * S::kVec + i] = (float)v[i];
+      pairs += v[i];
+    }
+  }
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+  // tokens that took part: every one chose K experts
+  const float n = fmaxf((float)pairs / (float)K, 1.f);
+  const float inv_n = 1.f / n;
+  const float d0 = dloss ? dloss[0] : 1.f, d1 = dloss ? dloss[1] : 1.f;
+  // d balance / d p_te = kb counts_e, and 2 c_z / n of the z-loss
+  const float kb = d0 * balance_coef * (float)E * inv_n * (inv_n / (float)K);
+  const float kz = d1 * 2.f * z_coef * inv_n;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) cost[i] *= kb;
+  for (; first < ntok; first += step) {
     const bool real = first + lane / G < ntok;
     const int64_t t = real ? first + lane / G : first;
     const T* row = logits + t * stride;
@@ -661,8 +689,8 @@ route_bwd_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask,
       idx[j] = -1;
       da[j] = 0.f;
       xc[j] = -CUDART_INF_F;
-      if (k < K) {
-        const int q = topk_idx[t * K + k];
+      if (k < K && real) {
+        const int q = next[j];
         if (q >= 0 && q < E) {
           idx[j] = q;
           xc[j] = (float)row[q];
@@ -672,6 +700,7 @@ route_bwd_kernel(const T* __restrict__ logits, const uint8_t* __restrict__ mask,
         }
       }
     }
+    read_choices(first + step + lane / G);
     float top = -CUDART_INF_F;
 #pragma unroll
     for (int i = 0; i < NI; ++i) top = fmaxf(top, x[i]);
