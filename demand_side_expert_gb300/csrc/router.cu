@@ -807,12 +807,14 @@ static lrm_status launch_route(const lrm_router* r, const void* logits, const ui
   int nwarp;
   int64_t grid;
   if (stats) {
-    // one CTA an SM at most (each leaves a row for the last sums), its warps
-    // in even rounds; a single CTA, without that last step, up to its warps
+    // one CTA an SM at most (each leaves a row for the last sums), its warps in
+    // even rounds; tokens that fit one CTA stay in one, without that second launch
     const int64_t ctas = std::min(num_sms(), kRouterMaxCtas);
     const int64_t rounds = (warps + ctas * kMaxWarps - 1) / (ctas * kMaxWarps);
     const int64_t need = (warps + rounds - 1) / rounds;
-    nwarp = (int)std::min(need, std::max<int64_t>(std::min(16, kMaxWarps), (need + ctas - 1) / ctas));
+    nwarp = (int)(need <= kMaxWarps
+                      ? need
+                      : std::max<int64_t>(std::min(16, kMaxWarps), (need + ctas - 1) / ctas));
     grid = (need + nwarp - 1) / nwarp;
   } else {
     nwarp = (int)std::min<int64_t>(4, warps);  // a warp for each scheduler of an SM
