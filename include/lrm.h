@@ -584,6 +584,8 @@ lrm_status lrm_add_rmsnorm_bwd(const lrm_norm* norm, const void* dy, const void*
  * holds e4m3(sqrt(v) / scale), with one scale = max(amax, 2^-100) / 448 for
  * each 256 consecutive values; a positive root is never stored as 0. Zero
  * codes and scales are a valid start. The step uses the unrounded new moments.
+ * A NaN gradient makes its own value and moments NaN; an infinite one also the
+ * 8-bit moments of its block.
  * Buffers are the caller's, param, grad, master, m, v 16-byte aligned, the scales
  * 4-byte, not overlapping. `step` counts from 1. It is read on the host: a captured graph
  * replays the bias correction of the step it was captured with.
