@@ -137,7 +137,8 @@ def test_route_and_gradient(dev, T, E, K, dtype, off, renorm):
 
 MANY = [(5000, 20, 1, "f32"), (6001, 32, 5, "bf16"), (5000, 60, 2, "bf16"), (5000, 64, 8, "f32"),
         (7003, 100, 3, "bf16"), (9000, 128, 8, "f32"), (5000, 200, 4, "f32"), (5001, 256, 8, "bf16"),
-        (5000, 256, 12, "f32"), (5000, 130, 1, "f32")]
+        (5000, 256, 12, "f32"), (5000, 130, 1, "f32"), (5000, 5, 5, "f32"), (5000, 8, 8, "bf16"),
+        (5000, 1, 1, "f32")]
 
 
 @pytest.mark.parametrize("kind", ["normal", "equal", "near", "zeros", "closed", "nan"])
@@ -322,6 +323,58 @@ def test_route_repeats_bit_for_bit_and_in_a_graph(dev):
     assert not torch.equal(got[3], first[3])
 
 
+def test_route_past_2_31_elements(dev):
+    """Rows of logits whose offsets need 64 bits, forward and backward."""
+    from demand_side_expert_gb300 import Router
+
+    T, E, K = (1 << 21) + 77, 1024, 4
+    x = torch.empty(T, E, dtype=torch.bfloat16, device=dev).normal_()
+    r = Router(T, E, K, "bf16", renorm=True, balance_coef=0.0)
+    r.route(x)
+    da = torch.ones(T, K, device=dev)
+    da[:, 1] = -1
+    r.backward(x, da)
+    assert r.counts.sum().item() == T * K
+    tail = x[-5:].cpu()
+    ref = so.route(to64(tail), K, True)
+    assert np.array_equal(r.topk_idx[-5:].cpu().numpy(), ref["topk_idx"])
+    tol = router_tol(to64(tail))
+    close(to64(r.alpha[-5:]), ref["alpha"], 2 * tol * ref["alpha"], "alpha")
+    want = so.route_bwd(to64(tail), ref["topk_idx"], ref["counts"], to64(da[-5:]), (0, 0), True)
+    a = np.zeros((5, E))
+    np.put_along_axis(a, ref["topk_idx"].astype(np.int64), ref["alpha"], 1)
+    lim = (3 * tol + (K + 16) * U) * a * 2 * np.abs(to64(da[-5:])).max() + BF16 * np.abs(want)
+    close(to64(r.dlogits[-5:]), want, lim + 1e-37, "dlogits")
+
+
+def test_calls_on_a_stream_of_their_own(dev):
+    """The stream argument: work ordered on it alone gives the current stream's bits."""
+    from demand_side_expert_gb300 import AddRMSNorm, AdamW, Router
+
+    gen = torch.Generator().manual_seed(4)
+    x = torch.randn(700, 64, generator=gen).to(dev)
+    w = torch.ones(64, device=dev)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for stream in (None, side, side.cuda_stream):
+        norm, router = AddRMSNorm(700, 64, "f32"), Router(700, 64, 4, "f32")
+        p, g = torch.ones(5000, device=dev), torch.full((5000,), 0.5, device=dev)
+        opt = AdamW([p], [g], state="f8")
+        torch.cuda.synchronize()
+        norm.forward(x, w, residual=x, stream=stream)
+        router.route(norm.y, stream=stream)
+        router.backward(norm.y, router.alpha, stream=stream)
+        norm.backward(router.dlogits, w, stream=stream)
+        opt.step(stream=stream)
+        side.synchronize()
+        torch.cuda.synchronize()
+        got.append([t.clone() for t in (norm.y, router.alpha, router.loss, router.dlogits,
+                                        norm.dx, norm.dw, p)])
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+
+
 # -- routing weights' gradient ----------------------------------------------------
 @pytest.mark.parametrize("T,D,K,dtype", [
     (1, 8, 1, "f32"), (5, 64, 2, "bf16"), (33, 1000, 8, "bf16"), (17, 2048, 9, "f32"),
@@ -347,6 +400,26 @@ def test_gate_grad(dev, T, D, K, dtype):
     lrm.lrm_gate_grad(shape, g.to(dev), y.to(dev), bad.to(dev), out, ws, n)
     assert out[0, 0].item() == 0
     assert lrm.lrm_get_device_error(ws, n) == lrm.LRM_DEVERR_INDEX
+
+
+def test_gate_grad_past_2_31_elements(dev):
+    """Rows of y whose offsets need 64 bits."""
+    from demand_side_expert_gb300 import lrm
+
+    T, D, K = 34000, 8192, 8
+    g = torch.empty(T, D, dtype=torch.bfloat16, device=dev).normal_()
+    y = torch.empty(T * K, D, dtype=torch.bfloat16, device=dev).normal_()
+    inv = torch.arange(T * K, dtype=torch.int32, device=dev).flip(0)
+    shape = lrm.make_shape(T, D, 8, 8, K, lrm.LRM_BF16)
+    n = lrm.lrm_workspace_bytes(shape)
+    ws = torch.zeros(n, dtype=torch.uint8, device=dev)
+    out = torch.empty(T, K, device=dev)
+    lrm.lrm_gate_grad(shape, g, y, inv, out, ws, n)
+    for t in (0, 1, T - 2, T - 1):
+        rows = y[inv[t * K:(t + 1) * K].long()]
+        want = (rows.double() * g[t].double()).sum(1).cpu().numpy()
+        mag = (rows.double().abs() * g[t].double().abs()).sum(1).cpu().numpy()
+        close(to64(out[t]), want, (D + 1) * U * mag, "dalpha")
 
 
 # -- norm -------------------------------------------------------------------------
