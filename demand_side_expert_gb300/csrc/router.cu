@@ -538,6 +538,8 @@ route_sums_kernel(const float2* __restrict__ part, const float* __restrict__ par
   const int rank = (int)cluster_ctarank();
   const int per = (E + kSumCtas - 1) / kSumCtas;
   const int begin = rank * per, end = min(E, begin + per);
+  // every CTA has started before another writes to its shared memory; waited for below
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
   pdl_begin();  // predecessor complete before any global access
   float z = 0.f;
   if (rank == 0 && warp == 0) {
@@ -587,6 +589,7 @@ route_sums_kernel(const float2* __restrict__ part, const float* __restrict__ par
   cnt = warp_sum(cnt);
   if (lane == 0) red[warp] = make_float2(dot, cnt);
   __syncthreads();
+  asm volatile("barrier.cluster.wait;" ::: "memory");
   if (warp == 0) {
     dot = warp_sum(lane < kWarps ? red[lane].x : 0.f);
     cnt = warp_sum(lane < kWarps ? red[lane].y : 0.f);
