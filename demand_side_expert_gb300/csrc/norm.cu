@@ -322,7 +322,7 @@ rmsnorm_bwd_kernel(const G* dy, const G* dh, const T* __restrict__ h, const T* _
     const int64_t r = base + row.group;
     copy_row(r + (stages - 1) * dr, slot == 0 ? stages - 1 : slot - 1);
     const float rs = next_rs;
-    if (r + dr < rows) next_rs = __ldg(rstd + r + dr);
+    next_rs = r + dr < rows ? __ldg(rstd + r + dr) : 0.f;
     copies_wait(stages);
     const uint4* v = ring + slot * pieces * threads + threadIdx.x;
     float fd[UPT][kUnit], xhat[UPT][kUnit];

@@ -590,6 +590,24 @@ def test_norm_zero_rows_nan_and_inf(dev):
     assert torch.isnan(z.y).all()
 
 
+def test_norm_backward_keeps_infinities_apart(dev):
+    """A row whose 1/rms is infinite (zeros and eps = 0) leaves the other rows' gradients
+    alone, and reaches dw as its formula says: 0 * inf in every column."""
+    from demand_side_expert_gb300 import AddRMSNorm
+
+    T, D = 5, 64
+    x, _, w, gen = norm_inputs(T, D, "f32")
+    x[0] = 0
+    n = AddRMSNorm(T, D, "f32", eps=0.0)
+    n.forward(x.to(dev), w.to(dev))
+    assert torch.isinf(n.rstd[0])
+    dy = torch.randn(T, D, generator=gen)
+    n.backward(dy.to(dev), w.to(dev), h=x.to(dev))
+    dx, _ = so.add_rmsnorm_bwd(to64(dy[1:]), None, to64(x[1:]), to64(w), to64(n.rstd[1:]))
+    close(to64(n.dx[1:]), dx, 64 * U * (np.abs(dx) + 8), "dx")
+    assert torch.isnan(n.dx[0]).all() and torch.isnan(n.dw).all()
+
+
 def test_norm_no_rows(dev):
     from demand_side_expert_gb300 import AddRMSNorm
 
