@@ -5,10 +5,11 @@
 // it was routed to (y in dispatch order, as the forward pass leaves it).
 //
 // HBM-bound: every y row is read once (K rows a token against one row of g).
-// What counts is the bytes an SM keeps in flight: loads into registers got to
-// 0.70-0.90 of the copy bandwidth (257-198 us at T 16384 D 4096 K 8, bf16, by
-// how many were unrolled), a ring of asynchronous copies in shared memory gets
-// to 1.00 (178 us, 6.8 TB/s).
+// What counts is the bytes an SM keeps in flight and the instructions for them:
+// loads into registers got to 0.70-0.90 of the copy bandwidth (257-198 us at
+// T 16384 D 4096 K 8, bf16, by how many were unrolled), a ring of asynchronous
+// copies in shared memory gets to 1.05 (169 us, 7.1 TB/s); with its step made for
+// 8 rows whatever K, K 2 took 99 us where it takes 62.
 #include <algorithm>
 
 #include "common.cuh"
@@ -16,33 +17,31 @@
 namespace lrm {
 
 constexpr int kGateThreads = 128;
-constexpr int kGateRows = 8;   // y rows summed per pass over g_t
-// Steps in flight. 2, 3, 4 and 6 measured 191, 178, 192 and 239 us at T 16384
-// D 4096 K 8 (fewer CTAs fit an SM where the rings are deeper).
+constexpr int kGateRows = 8;  // y rows summed in one pass over g_t, at most
+// Steps of copies in flight. With 8 rows 2, 3, 4 and 6 measured 191, 178, 192 and
+// 239 us at T 16384 D 4096 (fewer CTAs fit an SM where the rings are deeper).
 constexpr int kGateSteps = 3;
+// Pieces of every row in a step of R rows: a step has 8 to 10 pieces in all.
+constexpr int gate_pieces(int R) { return R == 8 ? 1 : R == 4 ? 2 : R == 2 ? 3 : 4; }
 
-// Adds kGateRows values over the warp: lane r (mod 8) ends with row r's sum.
-// Three steps trade half of the values against half of the lanes, so that 9
-// exchanges do the work of 40.
-__device__ __forceinline__ float fold_rows(const float (&v)[kGateRows]) {
-  static_assert(kGateRows == 8, "three halvings");
+// Adds R values over the warp: lane r (mod R) ends with row r's sum. Every
+// halving trades half of the values against half of the lanes, so that 9
+// exchanges do the work of 40 for R = 8.
+template <int R>
+__device__ __forceinline__ float fold_rows(float (&v)[R]) {
   const int lane = threadIdx.x & 31;
-  float a[4], b[2];
-  const bool h4 = lane & 4, h2 = lane & 2, h1 = lane & 1;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float keep = h4 ? v[i + 4] : v[i], give = h4 ? v[i] : v[i + 4];
-    a[i] = keep + __shfl_xor_sync(0xffffffffu, give, 4);
-  }
+  for (int o = R / 2; o > 0; o >>= 1) {
+    const bool high = lane & o;
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const float keep = h2 ? a[i + 2] : a[i], give = h2 ? a[i] : a[i + 2];
-    b[i] = keep + __shfl_xor_sync(0xffffffffu, give, 2);
+    for (int i = 0; i < o; ++i) {
+      const float keep = high ? v[i + o] : v[i], give = high ? v[i] : v[i + o];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
   }
-  const float keep = h1 ? b[1] : b[0], give = h1 ? b[0] : b[1];
-  float s = keep + __shfl_xor_sync(0xffffffffu, give, 1);
-  s += __shfl_xor_sync(0xffffffffu, s, 8);
-  s += __shfl_xor_sync(0xffffffffu, s, 16);
+  float s = v[0];
+#pragma unroll
+  for (int o = R; o < 32; o <<= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s;
 }
 
@@ -53,12 +52,12 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool valid
                : "memory");
 }
 
-// TPT threads a token (a warp, or the CTA), S steps of its rows in flight.
-// A step is one 16-byte piece of g_t and of up to 8 y rows for every thread;
-// it is copied to the thread's own places in shared memory, S - 1 steps ahead
-// of the one being summed, across the ends of tokens. Nobody else reads them,
-// so a thread waits for its own copies and there is no barrier.
-template <typename T, int TPT, int S>
+// TPT threads a token (a warp, or the CTA), R rows of y a pass. A step is a few
+// 16-byte pieces of g_t and of the rows for every thread; it is copied to the
+// thread's own places in shared memory, kGateSteps - 1 steps ahead of the one
+// being summed, across the ends of tokens. Nobody else reads them, so a thread
+// waits for its own copies and there is no barrier.
+template <typename T, int TPT, int R>
 __global__ void __launch_bounds__(kGateThreads)
 gate_grad_kernel(const T* __restrict__ g, const T* __restrict__ y,
                  const int32_t* __restrict__ inv, float* __restrict__ dalpha, int ntok, int D,
@@ -67,23 +66,26 @@ gate_grad_kernel(const T* __restrict__ g, const T* __restrict__ y,
   constexpr int V = Vec16<T>::kElems;
   constexpr int W = kGateThreads / 32;
   constexpr int kTokens = kGateThreads / TPT;
-  extern __shared__ uint4 ring[];  // [S][kGateRows + 1][threads]
-  __shared__ float part[2][W][kGateRows];
+  constexpr int U = gate_pieces(R), S = kGateSteps;
+  extern __shared__ uint4 ring[];  // [S][U][R + 1][threads]
+  __shared__ float part[2][W][R];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int tl = threadIdx.x % TPT;
   const int64_t N = (int64_t)ntok * K;
   const int nv = D / V;
-  const int steps = (nv + TPT - 1) / TPT;
+  const int steps = (nv + TPT * U - 1) / (TPT * U);
   const int64_t t0 = (int64_t)blockIdx.x * kTokens + threadIdx.x / TPT;
   const int64_t dt = (int64_t)gridDim.x * kTokens;
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring + threadIdx.x);
 
-  // copies: token, first row of the pass, step; lane r has row r's position
+  // copies: token, first row of the pass, step, the rows' positions
   int64_t ct = t0;
   int ck = 0, cs = 0;
+  int row[R];
+  // lane r: position of row r of a pass; a bad entry reads nothing and yields 0
   auto positions = [&](int64_t t, int k0) {
     int q = -1;
-    if (t < ntok && lane < kGateRows && k0 + lane < K) {
+    if (t < ntok && lane < R && k0 + lane < K) {
       q = inv[t * K + k0 + lane];
       if (q < 0 || q >= N) {
         flag_error(err, LRM_DEVERR_INDEX);
@@ -92,31 +94,38 @@ gate_grad_kernel(const T* __restrict__ g, const T* __restrict__ y,
     }
     return q;
   };
-  int pos = positions(ct, 0);
-  // of the pass after that one, read a pass ahead
-  int64_t nt = K > kGateRows ? ct : ct + dt;
-  int nk = K > kGateRows ? kGateRows : 0;
+  auto spread = [&](int pos) {
+#pragma unroll
+    for (int r = 0; r < R; ++r) row[r] = __shfl_sync(0xffffffffu, pos, r);
+  };
+  // positions of the pass after that one, read a pass ahead
+  int64_t nt = K > R ? ct : ct + dt;
+  int nk = K > R ? R : 0;
+  const int first_pos = positions(ct, 0);
   int next_pos = positions(nt, nk);
+  spread(first_pos);
   auto copy_step = [&](int slot) {
     if (ct < ntok) {
-      const int c = tl + cs * TPT;
-      const bool in = c < nv;
-      const uint32_t dst = mine + (uint32_t)slot * (kGateRows + 1) * kGateThreads * 16;
-      const int at = in ? c : 0;
-      copy16(dst, reinterpret_cast<const uint4*>(g + ct * D) + at, in);
+      uint32_t dst = mine + (uint32_t)slot * U * (R + 1) * kGateThreads * 16;
 #pragma unroll
-      for (int r = 0; r < kGateRows; ++r) {
-        const int q = __shfl_sync(0xffffffffu, pos, r);
-        if (ck + r < K)
+      for (int u = 0; u < U; ++u) {
+        const int c = tl + (cs * U + u) * TPT;
+        const bool in = c < nv;
+        const int at = in ? c : 0;
+        copy16(dst, reinterpret_cast<const uint4*>(g + ct * D) + at, in);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
           copy16(dst + (r + 1) * kGateThreads * 16,
-                 reinterpret_cast<const uint4*>(y + (int64_t)max(q, 0) * D) + at, in && q >= 0);
+                 reinterpret_cast<const uint4*>(y + (int64_t)max(row[r], 0) * D) + at,
+                 in && row[r] >= 0);
+        dst += (R + 1) * kGateThreads * 16;
       }
       if (++cs == steps) {
         cs = 0;
         ct = nt;
         ck = nk;
-        pos = next_pos;
-        nk += kGateRows;
+        spread(next_pos);
+        nk += R;
         if (nk >= K) {
           nk = 0;
           nt += dt;
@@ -130,34 +139,35 @@ gate_grad_kernel(const T* __restrict__ g, const T* __restrict__ y,
   for (int i = 0; i < S - 1; ++i) copy_step(i);
   int slot = 0, buf = 0;
   for (int64_t t = t0; t < ntok; t += dt) {
-    for (int k0 = 0; k0 < K; k0 += kGateRows) {
-      float acc[kGateRows];
+    for (int k0 = 0; k0 < K; k0 += R) {
+      float acc[R];
 #pragma unroll
-      for (int r = 0; r < kGateRows; ++r) acc[r] = 0.f;
+      for (int r = 0; r < R; ++r) acc[r] = 0.f;
       for (int i = 0; i < steps; ++i) {
         copy_step(slot == 0 ? S - 1 : slot - 1);  // the place of the step summed last
         asm volatile("cp.async.wait_group %0;" ::"n"(S - 1) : "memory");
-        const uint4* v = ring + slot * (kGateRows + 1) * kGateThreads + threadIdx.x;
-        float fg[V];
-        Vec16<T>::unpack(v[0], fg);
+        const uint4* v = ring + slot * U * (R + 1) * kGateThreads + threadIdx.x;
 #pragma unroll
-        for (int r = 0; r < kGateRows; ++r) {
-          if (k0 + r < K) {
+        for (int u = 0; u < U; ++u) {
+          float fg[V];
+          Vec16<T>::unpack(v[u * (R + 1) * kGateThreads], fg);
+#pragma unroll
+          for (int r = 0; r < R; ++r) {
             float fy[V];
-            Vec16<T>::unpack(v[(r + 1) * kGateThreads], fy);
+            Vec16<T>::unpack(v[(u * (R + 1) + r + 1) * kGateThreads], fy);
 #pragma unroll
             for (int j = 0; j < V; ++j) acc[r] = fmaf(fg[j], fy[j], acc[r]);
           }
         }
         slot = slot + 1 == S ? 0 : slot + 1;
       }
-      float s = fold_rows(acc);
+      float s = fold_rows<R>(acc);
       if constexpr (TPT == 32) {
-        if (lane < kGateRows && k0 + lane < K) dalpha[t * K + k0 + lane] = s;
+        if (lane < R && k0 + lane < K) dalpha[t * K + k0 + lane] = s;
       } else {
-        if (lane < kGateRows) part[buf][warp][lane] = s;
+        if (lane < R) part[buf][warp][lane] = s;
         __syncthreads();
-        if (threadIdx.x < kGateRows && k0 + (int)threadIdx.x < K) {
+        if (threadIdx.x < R && k0 + (int)threadIdx.x < K) {
           s = 0.f;
 #pragma unroll
           for (int w = 0; w < W; ++w) s += part[buf][w][threadIdx.x];
@@ -170,13 +180,13 @@ gate_grad_kernel(const T* __restrict__ g, const T* __restrict__ y,
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
-template <typename T, int TPT>
+template <typename T, int TPT, int R>
 static lrm_status launch_gate(const lrm_shape* s, const void* g, const void* y,
                               const int32_t* inv, float* dalpha, int32_t* err,
                               cudaStream_t cs) {
-  constexpr size_t kSmem = (size_t)kGateSteps * (kGateRows + 1) * kGateThreads * 16;
-  constexpr int64_t kPerSm = 4;  // CTAs that fit an SM's shared memory
-  static_assert(kPerSm * (kSmem + 2048) <= 227 * 1024, "the rings of an SM's CTAs");
+  constexpr size_t kSmem =
+      (size_t)kGateSteps * gate_pieces(R) * (R + 1) * kGateThreads * 16;
+  constexpr int64_t kPerSm = 227 * 1024 / (kSmem + 2048);  // CTAs that fit an SM's shared memory
   const int64_t need = ((int64_t)s->T * TPT + kGateThreads - 1) / kGateThreads;
   // More CTAs than fit at once, so that an SM which starts late or reads slowly
   // gets fewer tokens. Behind lrm_route_bwd (T 16384 D 4096, both, us): 210, 187,
@@ -184,7 +194,7 @@ static lrm_status launch_gate(const lrm_shape* s, const void* g, const void* y,
   // (D 256): 27.4, 24.0 and 24.5 for 1, 3 and 4.
   constexpr int64_t kTimes = TPT == 32 ? 3 : 16;
   const int blocks = (int)std::min<int64_t>(need, num_sms() * kPerSm * kTimes);
-  auto kern = gate_grad_kernel<T, TPT, kGateSteps>;
+  auto kern = gate_grad_kernel<T, TPT, R>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
       cudaSuccess) {
     (void)cudaGetLastError();
@@ -195,15 +205,28 @@ static lrm_status launch_gate(const lrm_shape* s, const void* g, const void* y,
   return launch_status();
 }
 
-// A CTA a token from rows of 4 KB on, a warp a token below. Measured (bf16, K 8
-// unless said, warp | CTA, us): T 16384 D 4096 195 | 178, T 200 D 4096 13.9 | 5.5,
-// T 3000 D 2048 25.7 | 21.6, T 8192 D 704 K 4 15.8 | 24.1, T 16384 D 256 18.0 | 51.
+template <typename T, int TPT>
+static lrm_status pick_rows(const lrm_shape* s, const void* g, const void* y, const int32_t* inv,
+                            float* dalpha, int32_t* err, cudaStream_t cs) {
+  if (s->K == 1) return launch_gate<T, TPT, 1>(s, g, y, inv, dalpha, err, cs);
+  if (s->K == 2) return launch_gate<T, TPT, 2>(s, g, y, inv, dalpha, err, cs);
+  if (s->K <= 4) return launch_gate<T, TPT, 4>(s, g, y, inv, dalpha, err, cs);
+  return launch_gate<T, TPT, kGateRows>(s, g, y, inv, dalpha, err, cs);
+}
+
+// A CTA a token where a token's rows are 36 KB or more, or where there are at
+// most two tokens an SM; a warp a token else. Measured (bf16, warp | CTA, us):
+// T 16384: D 4096 K 8 (72 KB) 178.6 | 169.2, D 4096 K 4 (40 KB) 99.4 | 101.1,
+// D 2048 K 8 (36 KB) 92.1 | 91.2, D 4096 K 2 (24 KB) 61.8 | 69.1, D 1024 K 8 48.9 |
+// 55.8, D 2048 K 1 23.7 | 42.8; T 200: D 4096 K 8 6.9 | 4.3, D 1024 K 8 3.2 | 2.7,
+// D 512 K 8 2.6 | 2.6.
 template <typename T>
 static lrm_status pick_gate(const lrm_shape* s, const void* g, const void* y, const int32_t* inv,
                             float* dalpha, int32_t* err, cudaStream_t cs) {
-  if ((int64_t)s->D * (int64_t)sizeof(T) >= 4096)
-    return launch_gate<T, kGateThreads>(s, g, y, inv, dalpha, err, cs);
-  return launch_gate<T, 32>(s, g, y, inv, dalpha, err, cs);
+  const int64_t token = ((int64_t)s->K + 1) * s->D * (int64_t)sizeof(T);
+  if (token >= 36 * 1024 || s->T <= 2 * num_sms())
+    return pick_rows<T, kGateThreads>(s, g, y, inv, dalpha, err, cs);
+  return pick_rows<T, 32>(s, g, y, inv, dalpha, err, cs);
 }
 
 }  // namespace lrm
