@@ -335,8 +335,10 @@ class AdamW:
             if g.dtype not in _CODE:
                 raise ValueError(f"grads[{i}]: float32 or bfloat16 is needed, got {g.dtype}")
             _need(g, f"grads[{i}]", tuple(p.shape), g.dtype, self.device)
-            self._table[i].grad, self._table[i].grad_dtype = g.data_ptr(), _CODE[g.dtype]
+        # all of them checked: the table never points to a tensor that is not held
         self.grads = grads
+        for s, g in zip(self._table, grads):
+            s.grad, s.grad_dtype = g.data_ptr(), _CODE[g.dtype]
 
     def step(self, lr: float | None = None, grad_scale=None, stream=None):
         """One update. ``lr`` for this step only; ``grad_scale``: a float32 device
