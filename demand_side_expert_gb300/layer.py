@@ -259,6 +259,15 @@ _STATE_BLOCK = 256
 _CODE = {torch.float32: lrm.LRM_F32, torch.bfloat16: lrm.LRM_BF16}
 
 
+def _addresses(tensors) -> list:
+    return list(map(torch.Tensor.data_ptr, tensors))
+
+
+def _moved(name: str, tensors, at) -> str:
+    which = [f"{name}[{i}]" for i, (t, a) in enumerate(zip(tensors, at)) if t.data_ptr() != a]
+    return f"{', '.join(which) or name}: not the storage taken before; "
+
+
 class AdamW:
     """AdamW over a list of tensors, all of them in one call of liblrm.
 
@@ -269,12 +278,16 @@ class AdamW:
     for 256 values each). ``master=True`` keeps float32 copies beside bfloat16
     parameters.
 
-    The state lives in flat buffers over all tensors, each tensor beginning on a
-    whole block of 256 (the tensors' storage is taken at construction: one that
-    is given other storage needs a new AdamW, or ``set_grads``): ``m``, ``v`` (float32, or float8_e4m3fn with v holding the
-    root), ``m_scale``, ``v_scale``, ``master`` (or None); tensor i holds
+    The tensors' storage is taken at construction: ``step`` refuses one that was
+    given other storage since (a new AdamW, or ``set_grads``, takes it). The state
+    lives in flat buffers over all tensors, each tensor beginning on a whole block
+    of 256: ``m``, ``v`` (float32, or float8_e4m3fn with v holding the root),
+    ``m_scale``, ``v_scale``, ``master`` (or None); tensor i holds
     [starts[i], starts[i] + numel).
     """
+
+    m, v, master = _owned("m"), _owned("v"), _owned("master")
+    m_scale, v_scale = _owned("m_scale"), _owned("v_scale")
 
     def __init__(self, params, grads, lr: float = 1e-3, betas=(0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.01, state: str = "f32", master: bool = False):
@@ -302,12 +315,12 @@ class AdamW:
         blocks = total // _STATE_BLOCK
         f8 = state == "f8"
         st = torch.float8_e4m3fn if f8 else torch.float32
-        self.m = torch.zeros(total, dtype=torch.uint8 if f8 else st, device=dev).view(st)
-        self.v = torch.zeros(total, dtype=torch.uint8 if f8 else st, device=dev).view(st)
-        self.m_scale = torch.zeros(blocks, device=dev) if f8 else None
-        self.v_scale = torch.zeros(blocks, device=dev) if f8 else None
+        self._m = torch.zeros(total, dtype=torch.uint8 if f8 else st, device=dev).view(st)
+        self._v = torch.zeros(total, dtype=torch.uint8 if f8 else st, device=dev).view(st)
+        self._m_scale = torch.zeros(blocks, device=dev) if f8 else None
+        self._v_scale = torch.zeros(blocks, device=dev) if f8 else None
         master = master and any(p.dtype is torch.bfloat16 for p in self.params)
-        self.master = torch.zeros(total, device=dev) if master else None
+        self._master = torch.zeros(total, device=dev) if master else None
         if master:
             for p, a in zip(self.params, self.starts):
                 self.master[a:a + p.numel()].copy_(p.reshape(-1))
@@ -324,6 +337,7 @@ class AdamW:
                 s.m_scale = self.m_scale.data_ptr() + 4 * (a // _STATE_BLOCK)
                 s.v_scale = self.v_scale.data_ptr() + 4 * (a // _STATE_BLOCK)
             s.state, s.weight_decay = _STATE[state], decay[i]
+        self._params_at = _addresses(self.params)
         self.set_grads(self.grads)
 
     def set_grads(self, grads):
@@ -339,6 +353,7 @@ class AdamW:
         self.grads = grads
         for s, g in zip(self._table, grads):
             s.grad, s.grad_dtype = g.data_ptr(), _CODE[g.dtype]
+        self._grads_at = _addresses(grads)
 
     def step(self, lr: float | None = None, grad_scale=None, stream=None):
         """One update. ``lr`` for this step only; ``grad_scale``: a float32 device
@@ -347,6 +362,10 @@ class AdamW:
             if grad_scale.numel() != 1:
                 raise ValueError("grad_scale: one float32 value is needed")
             _need(grad_scale, "grad_scale", tuple(grad_scale.shape), torch.float32, self.device)
+        if _addresses(self.params) != self._params_at:
+            raise ValueError(_moved("params", self.params, self._params_at) + "make a new AdamW")
+        if _addresses(self.grads) != self._grads_at:
+            raise ValueError(_moved("grads", self.grads, self._grads_at) + "call set_grads")
         h = self._hyper
         h.lr = self.lr if lr is None else lr
         h.step = self.t + 1

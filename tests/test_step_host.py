@@ -50,3 +50,38 @@ def test_adamw_refused_gradients_leave_the_table(host):
     opt.set_grads(new)
     assert [s.grad for s in opt._table] == [g.data_ptr() for g in new]
     assert all(s.grad_dtype == host.lrm.LRM_BF16 for s in opt._table)
+
+
+def test_adamw_refuses_tensors_that_got_other_storage(host):
+    """A parameter or a gradient whose storage was replaced is not stepped at its old
+    place, which is not its own any more."""
+    params, grads = [torch.zeros(8), torch.zeros(300)], [torch.zeros(8), torch.zeros(300)]
+    opt = host.layer.AdamW(params, grads)
+    opt.step()
+    assert opt.t == 1
+    old = params[1].data
+    params[1].data = torch.ones(300)
+    with pytest.raises(ValueError, match=r"params\[1\]"):
+        opt.step()
+    params[1].data = old
+    opt.step()
+    grads[0].data = torch.ones(8)
+    with pytest.raises(ValueError, match=r"grads\[0\]"):
+        opt.step()
+    opt.set_grads(grads)
+    opt.step()
+    opt.grads.append(torch.zeros(8))
+    with pytest.raises(ValueError):
+        opt.step()
+    assert opt.t == 3 and [name for name, _ in host.calls] == ["lrm_adamw_step"] * 3
+
+
+@pytest.mark.parametrize("state", ["f32", "f8"])
+def test_adamw_state_buffers_cannot_be_replaced(host, state):
+    """Their addresses are in the table, as the ones of Router's and AddRMSNorm's buffers."""
+    opt = host.layer.AdamW([torch.zeros(8, dtype=torch.bfloat16)], [torch.zeros(8)], state=state,
+                           master=True)
+    for name in ("m", "v", "m_scale", "v_scale", "master"):
+        with pytest.raises(AttributeError):
+            setattr(opt, name, torch.zeros(256))
+    assert opt.m.numel() == 256 and (opt.m_scale is None) == (state == "f32")
