@@ -15,6 +15,7 @@ stream wrote or will read is the caller's to order, as for every call here.
 from __future__ import annotations
 
 import ctypes
+from bisect import bisect_right
 
 import torch
 
@@ -263,6 +264,12 @@ def _addresses(tensors) -> list:
     return list(map(torch.Tensor.data_ptr, tensors))
 
 
+def _spans(tensors) -> list:
+    """(first byte, one past the last, index) of the tensors that hold any, in order."""
+    return sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i)
+                  for i, t in enumerate(tensors) if t.numel())
+
+
 def _moved(name: str, tensors, at) -> str:
     which = [f"{name}[{i}]" for i, (t, a) in enumerate(zip(tensors, at)) if t.data_ptr() != a]
     return f"{', '.join(which) or name}: not the storage taken before; "
@@ -273,7 +280,7 @@ class AdamW:
 
     ``params`` and ``grads``: contiguous float32 or bfloat16 device tensors, read
     and updated in place (the framework's dw_gate, dw_up, dw_down are such
-    gradients). ``weight_decay``: one number, or one a tensor. ``state``: "f32",
+    gradients). No parameter may overlap another, nor a gradient but its own. ``weight_decay``: one number, or one a tensor. ``state``: "f32",
     or "f8" for 8-bit moments (e4m3 codes of m and of sqrt(v), one float32 scale
     for 256 values each). ``master=True`` keeps float32 copies beside bfloat16
     parameters.
@@ -312,6 +319,10 @@ class AdamW:
             _need(p, f"params[{i}]", tuple(p.shape), p.dtype, dev)
             self.starts.append(total)
             total += -(-p.numel() // _STATE_BLOCK) * _STATE_BLOCK
+        self._spans = _spans(self.params)
+        for (_, end, i), (begin, _, j) in zip(self._spans, self._spans[1:]):
+            if begin < end:  # two CTAs would update that memory at once
+                raise ValueError(f"params[{i}] and params[{j}] overlap")
         blocks = total // _STATE_BLOCK
         f8 = state == "f8"
         st = torch.float8_e4m3fn if f8 else torch.float32
@@ -349,6 +360,12 @@ class AdamW:
             if g.dtype not in _CODE:
                 raise ValueError(f"grads[{i}]: float32 or bfloat16 is needed, got {g.dtype}")
             _need(g, f"grads[{i}]", tuple(p.shape), g.dtype, self.device)
+        for begin, end, i in _spans(grads):
+            k = bisect_right(self._spans, (begin, float("inf")))
+            for lo, hi, j in self._spans[max(k - 1, 0):k + 1]:
+                # a gradient that is its own parameter is read where it is written
+                if begin < hi and lo < end and not (i == j and (begin, end) == (lo, hi)):
+                    raise ValueError(f"grads[{i}] and params[{j}] overlap")
         # all of them checked: the table never points to a tensor that is not held
         self.grads = grads
         for s, g in zip(self._table, grads):

@@ -85,3 +85,21 @@ def test_adamw_state_buffers_cannot_be_replaced(host, state):
         with pytest.raises(AttributeError):
             setattr(opt, name, torch.zeros(256))
     assert opt.m.numel() == 256 and (opt.m_scale is None) == (state == "f32")
+
+
+def test_adamw_refuses_parameters_that_overlap(host):
+    """Two parameters on the same memory would be read and written by two CTAs of a
+    launch at once. Neighbours are fine, and one gradient for several parameters."""
+    flat, g = torch.zeros(4096), torch.zeros(64)
+    p = flat[:64]
+    for params in ([p, p], [p, torch.zeros(64), flat[32:96]], [flat[32:96], p],
+                   [p, p.view(8, 8)]):
+        with pytest.raises(ValueError, match="overlap"):
+            host.layer.AdamW(params, [torch.zeros(q.shape) for q in params])
+    host.layer.AdamW([flat[64:128], p, flat[:0], flat[:0]], [g, g, g[:0], g[:0]])
+    with pytest.raises(ValueError, match="overlap"):  # a gradient on a parameter's memory
+        host.layer.AdamW([p, flat[64:128]], [g, flat[32:96]])
+    opt = host.layer.AdamW([p], [p])  # in place: the gradient of p^2 / 2 is p
+    with pytest.raises(ValueError, match="overlap"):
+        opt.set_grads([flat[16:80]])
+    assert opt.grads == [p]
