@@ -20,7 +20,7 @@ from bisect import bisect_right
 import torch
 
 from . import lrm
-from .pipeline import _TORCH_DTYPE, dtype_code
+from .pipeline import _TORCH_DTYPE, _need, dtype_code
 
 _route, _route_bwd = lrm.entry("lrm_route"), lrm.entry("lrm_route_bwd")
 _norm, _norm_bwd = lrm.entry("lrm_add_rmsnorm"), lrm.entry("lrm_add_rmsnorm_bwd")
@@ -34,14 +34,6 @@ def _owned(name: str) -> property:
 
 def _address(t):
     return None if t is None else t.data_ptr()
-
-
-def _need(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device):
-    """A contiguous device tensor of this shape and type."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: a contiguous {dtype} tensor {shape} on {device} is needed, got "
-                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
-    return t
 
 
 def _need_rows(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device) -> int:

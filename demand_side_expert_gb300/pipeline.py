@@ -27,6 +27,14 @@ def dtype_code(name: str) -> int:
     return {"f32": lrm.LRM_F32, "bf16": lrm.LRM_BF16}[name]
 
 
+def _need(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device):
+    """A contiguous device tensor of this shape and type."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: a contiguous {dtype} tensor {shape} on {device} is needed, got "
+                         f"{t.dtype} {tuple(t.shape)} strides {t.stride()} on {t.device}")
+    return t
+
+
 class RecalibratedExpertBackward:
     """Buffers + call sequence for one (T, D, H, E, K, dtype) layer shape."""
 
@@ -108,9 +116,11 @@ class RecalibratedExpertBackward:
 
     def gate_grad(self, g, stream=None) -> torch.Tensor:
         """Gradient of the routing weights [T, K] (float32) from the cotangent g
-        [T, D] of the layer output and the rows ``y`` of the last forward."""
+        [T, D] of the layer output, in the layer's type, and the rows ``y`` of the
+        last forward."""
         if getattr(self, "y", None) is None:
             raise RuntimeError("gate_grad needs the expert outputs of a forward call")
+        _need(g, "g", (self.T, self.D), self.tdtype, self.ws.device)
         if getattr(self, "dalpha", None) is None:
             self.dalpha = torch.empty(max(self.T, 1), self.K, dtype=torch.float32,
                                       device=self.device)[: self.T]

@@ -103,3 +103,25 @@ def test_adamw_refuses_parameters_that_overlap(host):
     with pytest.raises(ValueError, match="overlap"):
         opt.set_grads([flat[16:80]])
     assert opt.grads == [p]
+
+
+def _pipe(host, T=6, D=64, K=2, dtype="bf16"):
+    return host.pipeline.RecalibratedExpertBackward(T, D, 64, 8, K, dtype, "cpu")
+
+
+def test_gate_grad_refuses_other_cotangents(host):
+    """g is read as [T, D] of the layer's type, whatever it is: another type or shape
+    would be read past its end or as other numbers, a strided one as its neighbours."""
+    pipe = _pipe(host)
+    pipe.forward(None, None, None, None, None, None)
+    good = torch.zeros(6, 64, dtype=torch.bfloat16)
+    for bad in (good.float(), good[:5], good[:, :32], torch.zeros(64, 6, dtype=good.dtype).t(),
+                torch.zeros(6, 128, dtype=good.dtype)[:, :64], good.view(-1)):
+        with pytest.raises(ValueError, match="^g: "):
+            pipe.gate_grad(bad)
+    wide = _pipe(host, dtype="f32")
+    wide.forward(None, None, None, None, None, None)
+    with pytest.raises(ValueError, match="^g: "):
+        wide.gate_grad(good)
+    assert "lrm_gate_grad" not in [name for name, _ in host.calls]
+    assert pipe.gate_grad(good).shape == (6, 2) and host.calls[-1][0] == "lrm_gate_grad"
