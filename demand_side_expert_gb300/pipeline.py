@@ -70,6 +70,7 @@ class RecalibratedExpertBackward:
         self.dw_gate, self.dw_up = empty(E, D, H, dtype=f32), empty(E, D, H, dtype=f32)
         self.dw_down = empty(E, H, D, dtype=f32)
         self.dx = empty(max(T, 1), D, dtype=f32)
+        self._y = None
         lrm.lrm_clear_device_error(self.ws, self.ws_bytes)
 
     # -- forward side -------------------------------------------------------
@@ -84,8 +85,20 @@ class RecalibratedExpertBackward:
             self.x_disp = torch.empty(rows, self.D, dtype=dt, device=dev)
             self.ab = torch.empty(rows, 2 * self.H, dtype=dt, device=dev)
             self.phi = torch.empty(rows, self.H, dtype=dt, device=dev)
-            self.y = torch.empty(rows, self.D, dtype=dt, device=dev)
             self.out = torch.empty(max(self.T, 1), self.D, dtype=torch.float32, device=dev)
+
+    @property
+    def y(self) -> torch.Tensor:
+        """Expert outputs [N, D] in dispatch order. Allocated by the first forward product
+        that writes it, or for a caller who asks for it: until then there is nothing
+        for ``gate_grad`` to read."""
+        if self._y is None:
+            self._y = torch.empty(max(self.N, 1), self.D, dtype=self.tdtype, device=self.device)
+        return self._y
+
+    @y.setter
+    def y(self, rows):
+        self._y = rows
 
     def forward(self, topk_idx, alpha, x, w_gate, w_up, w_down, stream=None):
         """Forward expert pass: dispatch, gather, gate/up + SwiGLU, down,
@@ -118,13 +131,13 @@ class RecalibratedExpertBackward:
         """Gradient of the routing weights [T, K] (float32) from the cotangent g
         [T, D] of the layer output, in the layer's type, and the rows ``y`` of the
         last forward."""
-        if getattr(self, "y", None) is None:
+        if self._y is None:
             raise RuntimeError("gate_grad needs the expert outputs of a forward call")
         _need(g, "g", (self.T, self.D), self.tdtype, self.ws.device)
         if getattr(self, "dalpha", None) is None:
             self.dalpha = torch.empty(max(self.T, 1), self.K, dtype=torch.float32,
                                       device=self.device)[: self.T]
-        lrm.lrm_gate_grad(self.shape, g, self.y, self.inv, self.dalpha, self.ws, self.ws_bytes,
+        lrm.lrm_gate_grad(self.shape, g, self._y, self.inv, self.dalpha, self.ws, self.ws_bytes,
                           stream)
         return self.dalpha
 

@@ -125,3 +125,27 @@ def test_gate_grad_refuses_other_cotangents(host):
         wide.gate_grad(good)
     assert "lrm_gate_grad" not in [name for name, _ in host.calls]
     assert pipe.gate_grad(good).shape == (6, 2) and host.calls[-1][0] == "lrm_gate_grad"
+
+
+def test_gate_grad_needs_expert_outputs(host):
+    """y holds something once a forward product (or the caller, who asked for the buffer)
+    wrote it; gathering the tokens alone does not."""
+    g = torch.zeros(6, 64, dtype=torch.bfloat16)
+    pipe = _pipe(host)
+    with pytest.raises(RuntimeError):
+        pipe.gate_grad(g)
+    pipe.gather_tokens(None)
+    with pytest.raises(RuntimeError):
+        pipe.gate_grad(g)
+    pipe.fc1_fwd(None, None)
+    pipe.fc2_fwd(None)
+    pipe.gate_grad(g)
+    other = _pipe(host)
+    other.gather_tokens(None)
+    assert other.y.shape == (12, 64)
+    other.y.fill_(1)
+    other.gate_grad(g)
+    third = _pipe(host)
+    third.y = other.y
+    third.gate_grad(g)
+    assert host.calls[-1][1][2] is other.y
