@@ -4,12 +4,14 @@
 ``AddRMSNorm``  residual addition, RMS norm, 8-bit rows with scales; and back
 ``AdamW``       one optimizer step over many tensors, moments in 32 bits or in 8
 
-Each owns its output buffers and workspace (allocated once through PyTorch,
-reused every call: a call overwrites what the one before it returned) and
-issues the C-ABI calls of liblrm on the stream it is given, else on torch's
-current one. Inputs are checked for type, shape, layout and device on the host;
-a mismatch raises ValueError before anything is launched. A buffer that another
-stream wrote or will read is the caller's to order, as for every call here.
+Each owns its output buffers and workspace (allocated once through PyTorch on
+its current stream, some of them by the first call that writes them, whose own
+stream then waits for the current one; reused every call: a call overwrites what
+the one before it returned) and issues the C-ABI calls of liblrm on the stream
+it is given, else on torch's current one. Inputs are checked for type, shape,
+layout and device on the host; a mismatch raises ValueError before anything is
+launched. A buffer that another stream wrote or will read is the caller's to
+order, as for every call here.
 """
 
 from __future__ import annotations
@@ -20,7 +22,7 @@ from bisect import bisect_right
 import torch
 
 from . import lrm
-from .pipeline import _TORCH_DTYPE, _need, dtype_code
+from .pipeline import _TORCH_DTYPE, _after_current, _need, dtype_code
 
 _route, _route_bwd = lrm.entry("lrm_route"), lrm.entry("lrm_route_bwd")
 _norm, _norm_bwd = lrm.entry("lrm_add_rmsnorm"), lrm.entry("lrm_add_rmsnorm_bwd")
@@ -133,6 +135,8 @@ class Router:
         if dloss is not None:
             _need(dloss, "dloss", (2,), torch.float32, self.device)
         topk_idx, _, counts, _, _, ws = self._at
+        if self._dlogits is None:
+            _after_current(stream)
         _route_bwd(self._ref, logits.data_ptr(), _address(mask), topk_idx, counts,
                    _address(dalpha), _address(dloss), self.dlogits.data_ptr(), ws, self.ws_bytes,
                    lrm.stream_address(stream))
@@ -216,12 +220,14 @@ class AddRMSNorm:
         dt, dev = self.tdtype, self.device
         desc = self.desc
         desc.x_stride = _need_rows(x, "x", self._shape, dt, dev)
+        _need(w, "w", self._columns, dt, dev)
         res = h = None
         self._summed = residual is not None
         if residual is not None:
             desc.res_stride = _need_rows(residual, "residual", self._shape, dt, dev)
+            if self._h is None:
+                _after_current(stream)
             res, h = residual.data_ptr(), self.h.data_ptr()
-        _need(w, "w", self._columns, dt, dev)
         y, q, q_scale, rstd = self._at
         _norm(self._ref, x.data_ptr(), res, w.data_ptr(), h, y, q, q_scale, rstd,
               lrm.stream_address(stream))
@@ -241,6 +247,8 @@ class AddRMSNorm:
         if dh is not None:
             _need(dh, "dh", shape, gt, dev)
         _need(w, "w", self._columns, dt, dev)
+        if self._dx is None:
+            _after_current(stream)
         self._backward_buffers()
         _norm_bwd(self._ref, dy.data_ptr(), _address(dh), h.data_ptr(), w.data_ptr(), self._at[3],
                   self._dx.data_ptr(), self._dw.data_ptr(), self._ws.data_ptr(), self.ws_bytes,

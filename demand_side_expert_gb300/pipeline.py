@@ -35,6 +35,21 @@ def _need(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device):
     return t
 
 
+def _after_current(stream):
+    """Makes ``stream`` wait for torch's current one, for a buffer that a call on it
+    allocates: the memory comes from the current stream's pool, and what it held
+    before may have work pending there."""
+    if stream is None:
+        return
+    current = torch.cuda.current_stream()
+    address = lrm.stream_address(stream)
+    if address == current.cuda_stream:
+        return
+    # ExternalStream takes address 0 for a new stream
+    other = torch.cuda.ExternalStream(address) if address else torch.cuda.default_stream()
+    other.wait_stream(current)
+
+
 class RecalibratedExpertBackward:
     """Buffers + call sequence for one (T, D, H, E, K, dtype) layer shape."""
 
@@ -78,23 +93,28 @@ class RecalibratedExpertBackward:
         lrm.lrm_dispatch_permute(self.shape, topk_idx, self.perm, self.inv, self.counts,
                                  self.off, self.ws, self.ws_bytes, stream)
 
-    def _forward_buffers(self):
+    def _forward_buffers(self, stream):
         """Forward outputs, allocated on the first forward call only."""
         if getattr(self, "x_disp", None) is None:
+            _after_current(stream)
             rows, dt, dev = max(self.N, 1), self.tdtype, self.device
             self.x_disp = torch.empty(rows, self.D, dtype=dt, device=dev)
             self.ab = torch.empty(rows, 2 * self.H, dtype=dt, device=dev)
             self.phi = torch.empty(rows, self.H, dtype=dt, device=dev)
             self.out = torch.empty(max(self.T, 1), self.D, dtype=torch.float32, device=dev)
 
+    def _expert_outputs(self, stream):
+        if self._y is None:
+            _after_current(stream)
+            self._y = torch.empty(max(self.N, 1), self.D, dtype=self.tdtype, device=self.device)
+        return self._y
+
     @property
     def y(self) -> torch.Tensor:
         """Expert outputs [N, D] in dispatch order. Allocated by the first forward product
         that writes it, or for a caller who asks for it: until then there is nothing
         for ``gate_grad`` to read."""
-        if self._y is None:
-            self._y = torch.empty(max(self.N, 1), self.D, dtype=self.tdtype, device=self.device)
-        return self._y
+        return self._expert_outputs(None)
 
     @y.setter
     def y(self, rows):
@@ -104,14 +124,15 @@ class RecalibratedExpertBackward:
         """Forward expert pass: dispatch, gather, gate/up + SwiGLU, down,
         combine. Leaves the saved state in ``ab`` / ``phi`` (dispatch order)
         and the layer output in ``out`` (float32 [T, D])."""
-        self._forward_buffers()
+        self._forward_buffers(stream)
+        self._expert_outputs(stream)
         self.dispatch(topk_idx, stream)
         lrm.lrm_expert_fwd_grouped(self.shape, self.perm, self.inv, self.off, alpha, x, w_gate,
                                    w_up, w_down, self.x_disp, self.ab, self.phi, self.y,
                                    self.out, self.ws, self.ws_bytes, stream)
 
     def gather_tokens(self, x, stream=None):
-        self._forward_buffers()
+        self._forward_buffers(stream)
         lrm.lrm_gather_tokens(self.shape, self.perm, x, self.x_disp, self.ws, self.ws_bytes,
                               stream)
 
@@ -120,6 +141,7 @@ class RecalibratedExpertBackward:
                                self.phi, self.ws, self.ws_bytes, stream)
 
     def fc2_fwd(self, w_down, stream=None):
+        self._expert_outputs(stream)
         lrm.lrm_expert_fc2_fwd(self.shape, self.off, self.phi, w_down, self.y, self.ws,
                                self.ws_bytes, stream)
 
@@ -135,6 +157,7 @@ class RecalibratedExpertBackward:
             raise RuntimeError("gate_grad needs the expert outputs of a forward call")
         _need(g, "g", (self.T, self.D), self.tdtype, self.ws.device)
         if getattr(self, "dalpha", None) is None:
+            _after_current(stream)
             self.dalpha = torch.empty(max(self.T, 1), self.K, dtype=torch.float32,
                                       device=self.device)[: self.T]
         lrm.lrm_gate_grad(self.shape, g, self._y, self.inv, self.dalpha, self.ws, self.ws_bytes,
