@@ -8,10 +8,11 @@ Each owns its output buffers and workspace (allocated once through PyTorch on
 its current stream, some of them by the first call that writes them, whose own
 stream then waits for the current one; reused every call: a call overwrites what
 the one before it returned) and issues the C-ABI calls of liblrm on the stream
-it is given, else on torch's current one. Inputs are checked for type, shape,
-layout and device on the host; a mismatch raises ValueError before anything is
-launched. A buffer that another stream wrote or will read is the caller's to
-order, as for every call here.
+it is given, else on torch's current one; the current device has to be the one
+of the buffers. Inputs are checked for type, shape, layout and device on the
+host; a mismatch raises ValueError before anything is launched. A buffer that
+another stream wrote or will read is the caller's to order, as for every call
+here.
 """
 
 from __future__ import annotations
@@ -22,7 +23,7 @@ from bisect import bisect_right
 import torch
 
 from . import lrm
-from .pipeline import _TORCH_DTYPE, _after_current, _need, dtype_code
+from .pipeline import _TORCH_DTYPE, _after_current, _need, _stream, dtype_code
 
 _route, _route_bwd = lrm.entry("lrm_route"), lrm.entry("lrm_route_bwd")
 _norm, _norm_bwd = lrm.entry("lrm_add_rmsnorm"), lrm.entry("lrm_add_rmsnorm_bwd")
@@ -56,7 +57,10 @@ def _device(device) -> torch.device:
     dev = torch.device(device)
     if dev.type != "cuda":
         raise ValueError(f"a CUDA device is needed, got {dev}")
-    return torch.device("cuda", torch.cuda.current_device()) if dev.index is None else dev
+    here = torch.device("cuda", lrm.current_device())
+    if dev.index is not None and dev != here:  # kernels launch on the current device
+        raise ValueError(f"{dev} is not the current device, {here}")
+    return here
 
 
 class Router:
@@ -118,11 +122,12 @@ class Router:
         bool or uint8: tokens that are 0 there get weight 0 and count nowhere.
         ``stats=False`` skips counts and losses (serving)."""
         mask = self._inputs(logits, mask)
+        at = _stream(self.device, stream)
         topk_idx, alpha, counts, prob_sum, loss, ws = self._at
         if not stats:
             counts = prob_sum = loss = None
         _route(self._ref, logits.data_ptr(), _address(mask), topk_idx, alpha, counts, prob_sum,
-               loss, ws, self.ws_bytes, lrm.stream_address(stream))
+               loss, ws, self.ws_bytes, at)
 
     def backward(self, logits, dalpha=None, mask=None, dloss=None, stream=None):
         """The logits' gradient, from the choices and counts of the last ``route``
@@ -134,12 +139,13 @@ class Router:
             _need(dalpha, "dalpha", (self.T, self.K), torch.float32, self.device)
         if dloss is not None:
             _need(dloss, "dloss", (2,), torch.float32, self.device)
+        at = _stream(self.device, stream)
         topk_idx, _, counts, _, _, ws = self._at
         if self._dlogits is None:
             _after_current(stream)
         _route_bwd(self._ref, logits.data_ptr(), _address(mask), topk_idx, counts,
                    _address(dalpha), _address(dloss), self.dlogits.data_ptr(), ws, self.ws_bytes,
-                   lrm.stream_address(stream))
+                   at)
 
     def device_error(self, stream=None) -> int:
         return lrm.lrm_get_device_error(self._ws, self.ws_bytes, stream)
@@ -221,6 +227,7 @@ class AddRMSNorm:
         desc = self.desc
         desc.x_stride = _need_rows(x, "x", self._shape, dt, dev)
         _need(w, "w", self._columns, dt, dev)
+        at = _stream(dev, stream)
         res = h = None
         self._summed = residual is not None
         if residual is not None:
@@ -229,8 +236,7 @@ class AddRMSNorm:
                 _after_current(stream)
             res, h = residual.data_ptr(), self.h.data_ptr()
         y, q, q_scale, rstd = self._at
-        _norm(self._ref, x.data_ptr(), res, w.data_ptr(), h, y, q, q_scale, rstd,
-              lrm.stream_address(stream))
+        _norm(self._ref, x.data_ptr(), res, w.data_ptr(), h, y, q, q_scale, rstd, at)
 
     def backward(self, dy, w, dh=None, h=None, stream=None):
         """dy [T, D]: the cotangent of y; dh: of the stored sum (the residual
@@ -247,12 +253,12 @@ class AddRMSNorm:
         if dh is not None:
             _need(dh, "dh", shape, gt, dev)
         _need(w, "w", self._columns, dt, dev)
+        at = _stream(dev, stream)
         if self._dx is None:
             _after_current(stream)
         self._backward_buffers()
         _norm_bwd(self._ref, dy.data_ptr(), _address(dh), h.data_ptr(), w.data_ptr(), self._at[3],
-                  self._dx.data_ptr(), self._dw.data_ptr(), self._ws.data_ptr(), self.ws_bytes,
-                  lrm.stream_address(stream))
+                  self._dx.data_ptr(), self._dw.data_ptr(), self._ws.data_ptr(), self.ws_bytes, at)
 
 
 _STATE = {"f32": lrm.LRM_STATE_F32, "f8": lrm.LRM_STATE_F8}
@@ -383,11 +389,12 @@ class AdamW:
             raise ValueError(_moved("params", self.params, self._params_at) + "make a new AdamW")
         if _addresses(self.grads) != self._grads_at:
             raise ValueError(_moved("grads", self.grads, self._grads_at) + "call set_grads")
+        at = _stream(self.device, stream)
         h = self._hyper
         h.lr = self.lr if lr is None else lr
         h.step = self.t + 1
         h.grad_scale = None if grad_scale is None else grad_scale.data_ptr()
-        lrm.lrm_adamw_step(h, self._table, len(self._table), stream)
+        lrm.lrm_adamw_step(h, self._table, len(self._table), at)
         self.t += 1
 
     def state_dict(self) -> dict:

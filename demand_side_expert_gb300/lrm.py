@@ -168,6 +168,20 @@ def _current_stream_fn():
 _current_stream = None
 
 
+def current_device() -> int:
+    """Index of the device that kernels launch on: torch's current one."""
+    global _current_device
+    if _current_device is None:
+        import torch
+
+        torch.cuda.init()
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _current_device()
+
+
+_current_device = None
+
+
 def _s(stream):
     if stream is None:
         global _current_stream

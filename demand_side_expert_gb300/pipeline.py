@@ -35,6 +35,15 @@ def _need(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.device):
     return t
 
 
+def _stream(device: torch.device, stream) -> int:
+    """Address of a call's stream. Kernels launch on the current device, so that has to be
+    the one of the call's buffers."""
+    if lrm.current_device() != device.index:
+        raise ValueError(f"the buffers are on {device}, the current device is "
+                         f"cuda:{lrm.current_device()}")
+    return lrm.stream_address(stream)
+
+
 def _after_current(stream):
     """Makes ``stream`` wait for torch's current one, for a buffer that a call on it
     allocates: the memory comes from the current stream's pool, and what it held
@@ -155,13 +164,15 @@ class RecalibratedExpertBackward:
         last forward."""
         if self._y is None:
             raise RuntimeError("gate_grad needs the expert outputs of a forward call")
-        _need(g, "g", (self.T, self.D), self.tdtype, self.ws.device)
+        device = self.ws.device
+        _need(g, "g", (self.T, self.D), self.tdtype, device)
+        at = _stream(device, stream)
         if getattr(self, "dalpha", None) is None:
             _after_current(stream)
             self.dalpha = torch.empty(max(self.T, 1), self.K, dtype=torch.float32,
                                       device=self.device)[: self.T]
         lrm.lrm_gate_grad(self.shape, g, self._y, self.inv, self.dalpha, self.ws, self.ws_bytes,
-                          stream)
+                          at)
         return self.dalpha
 
     def to_dispatch_order(self, rows_by_pair: torch.Tensor, stream=None) -> torch.Tensor:

@@ -29,7 +29,8 @@ def host(monkeypatch):
                  "lrm_dispatch_permute", "lrm_gather_tokens", "lrm_expert_fwd_grouped",
                  "lrm_expert_fc1_fwd", "lrm_expert_fc2_fwd"):
         monkeypatch.setattr(lrm, name, recorder(name))
-    monkeypatch.setattr(lrm, "stream_address", lambda stream=None: stream or 0)
+    for module in (layer, pipeline):
+        monkeypatch.setattr(module, "_stream", lambda device, stream: stream or 0)
     return types.SimpleNamespace(layer=layer, lrm=lrm, pipeline=pipeline, calls=calls)
 
 
@@ -149,3 +150,40 @@ def test_gate_grad_needs_expert_outputs(host):
     third.y = other.y
     third.gate_grad(g)
     assert host.calls[-1][1][2] is other.y
+
+
+def test_other_devices_are_refused(monkeypatch):
+    """The kernels launch on the current device: an object on another one's memory is
+    refused where it is made, and its calls are while another device is current."""
+    from demand_side_expert_gb300 import layer, lrm
+
+    monkeypatch.setattr(lrm, "current_device", lambda: 0)
+    assert layer._device("cuda") == torch.device("cuda", 0) == layer._device("cuda:0")
+    for other in ("cuda:1", torch.device("cuda", 7)):
+        with pytest.raises(ValueError, match="current device"):
+            layer._device(other)
+    monkeypatch.setattr(lrm, "stream_address", lambda stream=None: 5)
+    assert layer._stream(torch.device("cuda", 0), None) == 5
+    with pytest.raises(ValueError, match="current device"):
+        layer._stream(torch.device("cuda", 1), None)
+
+
+def test_calls_run_on_the_device_of_their_buffers(host, monkeypatch):
+    r = host.layer.Router(4, 8, 2)
+    n = host.layer.AddRMSNorm(4, 8, "f32")
+    o = host.layer.AdamW([torch.zeros(8)], [torch.zeros(8)])
+    x, w = torch.zeros(4, 8), torch.zeros(8)
+
+    def refuse(device, stream):
+        assert device == torch.device("cpu")
+        raise ValueError("current device")
+
+    r.route(x)
+    n.forward(x, w)
+    monkeypatch.setattr(host.layer, "_stream", refuse)
+    calls = len(host.calls)
+    for call in (lambda: r.route(x), lambda: r.backward(x), lambda: n.forward(x, w),
+                 lambda: n.backward(x, w, h=x), o.step):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    assert len(host.calls) == calls and o.t == 0
