@@ -90,11 +90,15 @@ class Router:
         def empty(*shape, dtype=torch.float32):
             return torch.empty(*shape, dtype=dtype, device=dev)
 
-        self._ws = empty(self.ws_bytes, dtype=torch.uint8)
-        self._topk_idx, self._alpha = empty(T, K, dtype=torch.int32), empty(T, K)
-        self._counts, self._prob_sum = empty(E, dtype=torch.int32), empty(E)
-        self._loss = empty(2)
+        with torch.inference_mode(False):  # inference tensors do not count their writes
+            self._ws = empty(self.ws_bytes, dtype=torch.uint8)
+            self._topk_idx, self._alpha = empty(T, K, dtype=torch.int32), empty(T, K)
+            self._counts, self._prob_sum = empty(E, dtype=torch.int32), empty(E)
+            self._loss = empty(2)
         self._dlogits = None
+        # what backward may read: ids and counts of a route, or written by the caller since
+        self._routed = self._counted = False
+        self._idx_at, self._counts_at = self._topk_idx._version, self._counts._version
         self._ref = ctypes.byref(self.desc)
         self._at = tuple(t.data_ptr() for t in (self._topk_idx, self._alpha, self._counts,
                                                 self._prob_sum, self._loss, self._ws))
@@ -128,13 +132,24 @@ class Router:
             counts = prob_sum = loss = None
         _route(self._ref, logits.data_ptr(), _address(mask), topk_idx, alpha, counts, prob_sum,
                loss, ws, self.ws_bytes, at)
+        self._routed, self._counted = True, stats
+        if not stats:
+            self._counts_at = self._counts._version
 
     def backward(self, logits, dalpha=None, mask=None, dloss=None, stream=None):
         """The logits' gradient, from the choices and counts of the last ``route``
         (with statistics) on the same logits and mask. ``dalpha`` [T, K] float32
         (``RecalibratedExpertBackward.gate_grad``), ``dloss`` [2] float32: what the
-        two losses weigh in the total (1 each by default)."""
+        two losses weigh in the total (1 each by default). Choices and counts that the
+        caller wrote into ``topk_idx`` and ``counts`` serve as well; without either
+        the call is refused (counts are not needed where both coefficients are 0)."""
         mask = self._inputs(logits, mask)
+        if not self._routed and self._topk_idx._version == self._idx_at:
+            raise ValueError("no choices to take the gradient of: call route before")
+        if not self._counted and self._counts._version == self._counts_at and \
+                (self.desc.balance_coef != 0 or self.desc.z_coef != 0):
+            raise ValueError("the last route had no statistics, and the losses' gradient needs "
+                             "its counts")
         if dalpha is not None:
             _need(dalpha, "dalpha", (self.T, self.K), torch.float32, self.device)
         if dloss is not None:

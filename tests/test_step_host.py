@@ -187,3 +187,45 @@ def test_calls_run_on_the_device_of_their_buffers(host, monkeypatch):
         with pytest.raises(ValueError, match="current device"):
             call()
     assert len(host.calls) == calls and o.t == 0
+
+
+def test_router_gradient_needs_choices_and_counts(host):
+    """The gradient reads the ids and, with a loss that weighs something, the counts: of a
+    route with statistics, or written by the caller. Those of nothing are refused."""
+    Router = host.layer.Router
+    x = torch.zeros(4, 8)
+    r = Router(4, 8, 2)
+    with pytest.raises(ValueError, match="route"):
+        r.backward(x)
+    r.route(x, stats=False)
+    with pytest.raises(ValueError, match="statistics"):
+        r.backward(x)
+    r.route(x)
+    r.backward(x)
+    r.route(x, stats=False)  # its counts are of other choices
+    with pytest.raises(ValueError, match="statistics"):
+        r.backward(x)
+    r.counts.fill_(1)
+    r.backward(x)
+    with pytest.raises(ValueError):  # a refused call is no route
+        r.route(x[:, :4], stats=False)
+    r.backward(x)
+    # the losses weigh nothing: the counts do not matter
+    free = Router(4, 8, 2, balance_coef=0.0, z_coef=0.0)
+    free.route(x, stats=False)
+    free.backward(x)
+    # the caller's own choices and counts
+    own = Router(4, 8, 2, z_coef=0.1)
+    own.topk_idx.fill_(0)
+    with pytest.raises(ValueError, match="statistics"):
+        own.backward(x)
+    own.counts.fill_(1)
+    own.backward(x)
+    with torch.inference_mode():
+        served = Router(4, 8, 2)
+        with pytest.raises(ValueError, match="route"):
+            served.backward(x)
+        served.route(x)
+        served.backward(x)
+    names = [name for name, _ in host.calls if name.startswith("_route")]
+    assert names.count("_route_bwd") == 6
