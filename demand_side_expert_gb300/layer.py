@@ -239,19 +239,26 @@ class AddRMSNorm:
     def forward(self, x, w, residual=None, stream=None):
         """x, residual [T, D] (rows may be strided by a multiple of 8 elements), w [D]."""
         dt, dev = self.tdtype, self.device
-        desc = self.desc
-        desc.x_stride = _need_rows(x, "x", self._shape, dt, dev)
+        x_stride = _need_rows(x, "x", self._shape, dt, dev)
         _need(w, "w", self._columns, dt, dev)
-        at = _stream(dev, stream)
-        res = h = None
-        self._summed = residual is not None
+        res, h, res_stride = None, None, self.D
         if residual is not None:
-            desc.res_stride = _need_rows(residual, "residual", self._shape, dt, dev)
+            res_stride = _need_rows(residual, "residual", self._shape, dt, dev)
+            res = residual.data_ptr()
+        at = _stream(dev, stream)
+        if residual is not None:
             if self._h is None:
                 _after_current(stream)
-            res, h = residual.data_ptr(), self.h.data_ptr()
+            h = self.h.data_ptr()
+        desc = self.desc
+        desc.x_stride, desc.res_stride = x_stride, res_stride
         y, q, q_scale, rstd = self._at
-        _norm(self._ref, x.data_ptr(), res, w.data_ptr(), h, y, q, q_scale, rstd, at)
+        try:
+            _norm(self._ref, x.data_ptr(), res, w.data_ptr(), h, y, q, q_scale, rstd, at)
+        except lrm.LrmError:
+            desc.x_stride = desc.res_stride = self.D  # backward is not refused for them
+            raise
+        self._summed = residual is not None
 
     def backward(self, dy, w, dh=None, h=None, stream=None):
         """dy [T, D]: the cotangent of y; dh: of the stored sum (the residual

@@ -229,3 +229,30 @@ def test_router_gradient_needs_choices_and_counts(host):
         served.backward(x)
     names = [name for name, _ in host.calls if name.startswith("_route")]
     assert names.count("_route_bwd") == 6
+
+
+def test_refused_norm_calls_change_nothing(host, monkeypatch):
+    """backward takes the sum and the 1/rms of the last forward that ran."""
+    x, w = torch.zeros(4, 8), torch.ones(8)
+    n = host.layer.AddRMSNorm(4, 8, "f32")
+    n.forward(x, w)
+    for bad in (dict(x=x[:3], w=w, residual=x), dict(x=x, w=w[:4], residual=x),
+                dict(x=x, w=w, residual=x[:2])):
+        with pytest.raises(ValueError):
+            n.forward(**bad)
+        with pytest.raises(ValueError, match="no residual"):
+            n.backward(x, w)
+    n.forward(x, w, residual=x)
+    with pytest.raises(ValueError):
+        n.forward(x, w[:4])
+    n.backward(x, w)
+    assert host.calls[-1][0] == "_norm_bwd" and host.calls[-1][1][3] == n.h.data_ptr()
+
+    def refuse(*args):
+        raise host.lrm.LrmError("lrm_add_rmsnorm", host.lrm.LRM_ERR_UNSUPPORTED)
+
+    monkeypatch.setattr(host.layer, "_norm", refuse)
+    with pytest.raises(host.lrm.LrmError):  # rows 12 elements apart
+        n.forward(torch.zeros(4, 12)[:, :8], w, residual=torch.zeros(4, 12)[:, :8])
+    assert n.desc.x_stride == n.desc.res_stride == 8
+    assert n._summed
