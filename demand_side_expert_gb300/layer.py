@@ -196,7 +196,9 @@ class AddRMSNorm:
         def empty(*shape, dtype=torch.float32):
             return torch.empty(*shape, dtype=dtype, device=dev)
 
-        self._rstd = empty(T)
+        with torch.inference_mode(False):  # inference tensors do not count their writes
+            self._rstd = empty(T)
+        self._rstd_at = self._rstd._version  # another one: the caller wrote it
         store_y = q_cols is None if store_y is None else store_y
         if q_cols is None and not store_y:
             raise ValueError("store_y=False leaves no output without q_cols")
@@ -206,6 +208,7 @@ class AddRMSNorm:
             self._q = empty(T, D, dtype=torch.float8_e4m3fn)
             self._q_scale = empty(T, -(-D // q_cols) if q_cols else 1)
         self._h = self._dx = self._dw = self._ws = None
+        self._normed = T == 0  # there is a 1/rms to take the gradient with
         self._summed = False  # the last forward had a residual: h is its sum
         self._ref = ctypes.byref(self.desc)
         self._at = tuple(_address(t) for t in (self._y, self._q, self._q_scale, self._rstd))
@@ -258,13 +261,16 @@ class AddRMSNorm:
         except lrm.LrmError:
             desc.x_stride = desc.res_stride = self.D  # backward is not refused for them
             raise
-        self._summed = residual is not None
+        self._normed, self._summed = True, residual is not None
 
     def backward(self, dy, w, dh=None, h=None, stream=None):
         """dy [T, D]: the cotangent of y; dh: of the stored sum (the residual
         stream), or None. ``h``: the normed rows, self.h by default (pass x where
-        there was no residual). Uses ``rstd`` of the last forward."""
+        there was no residual). Uses ``rstd`` of the last forward, or what the caller
+        wrote there."""
         dt, gt, dev, shape = self.tdtype, self.gdtype, self.device, self._shape
+        if not self._normed and self._rstd._version == self._rstd_at:
+            raise ValueError("no 1/rms to take the gradient with: call forward before")
         if h is not None:
             _need(h, "h", shape, dt, dev)
         elif self._summed:

@@ -256,3 +256,25 @@ def test_refused_norm_calls_change_nothing(host, monkeypatch):
         n.forward(torch.zeros(4, 12)[:, :8], w, residual=torch.zeros(4, 12)[:, :8])
     assert n.desc.x_stride == n.desc.res_stride == 8
     assert n._summed
+
+
+def test_norm_gradient_needs_a_forward(host):
+    """rstd is of a forward, or written by the caller: not uninitialised memory."""
+    x, w = torch.zeros(4, 8), torch.ones(8)
+    n = host.layer.AddRMSNorm(4, 8, "f32")
+    with pytest.raises(ValueError, match="forward"):
+        n.backward(x, w, h=x)
+    with pytest.raises(ValueError):
+        n.forward(x, w[:4])
+    with pytest.raises(ValueError, match="forward"):
+        n.backward(x, w, h=x)
+    n.rstd.fill_(1)
+    n.backward(x, w, h=x)
+    m = host.layer.AddRMSNorm(4, 8, "f32")
+    m.forward(x, w)
+    m.backward(x, w, h=x)
+    empty = host.layer.AddRMSNorm(0, 8, "f32")
+    empty.backward(x[:0], w, h=x[:0])
+    with torch.inference_mode():
+        host.layer.AddRMSNorm(4, 8, "f32").forward(x, w)
+    assert [name for name, _ in host.calls].count("_norm_bwd") == 3
