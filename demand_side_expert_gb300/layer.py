@@ -433,6 +433,9 @@ class AdamW:
     def load_state_dict(self, state: dict):
         """Copies a state of the same layout in; on torch's current stream. The
         parameters are left as they are."""
+        t, pairs = int(state["step"]), []
+        if t < 0:
+            raise ValueError(f"step: {t}")
         for name in ("master", "m", "v", "m_scale", "v_scale"):
             mine, other = getattr(self, name), state.get(name)
             if (mine is None) != (other is None):
@@ -441,5 +444,7 @@ class AdamW:
                 if other.shape != mine.shape or other.dtype is not mine.dtype:
                     raise ValueError(f"{name}: {mine.dtype} {tuple(mine.shape)} is needed, got "
                                      f"{other.dtype} {tuple(other.shape)}")
-                mine.copy_(other)
-        self.t = int(state["step"])
+                pairs.append((mine, other))
+        for mine, other in pairs:  # all of them checked
+            mine.copy_(other)
+        self.t = t

@@ -278,3 +278,32 @@ def test_norm_gradient_needs_a_forward(host):
     with torch.inference_mode():
         host.layer.AddRMSNorm(4, 8, "f32").forward(x, w)
     assert [name for name, _ in host.calls].count("_norm_bwd") == 3
+
+
+@pytest.mark.parametrize("state", ["f32", "f8"])
+def test_adamw_refused_state_changes_nothing(host, state):
+    def make():
+        opt = host.layer.AdamW([torch.ones(300, dtype=torch.bfloat16)], [torch.ones(300)],
+                               state=state, master=True)
+        return opt
+
+    opt = make()
+    kept = {k: v.clone() if torch.is_tensor(v) else v for k, v in opt.state_dict().items()}
+    good = {k: torch.ones_like(v.float()).to(v.dtype) if torch.is_tensor(v) else v
+            for k, v in kept.items()}
+    good["step"] = 7
+    last = "v" if state == "f32" else "v_scale"
+    for change in ({last: good[last][:-1]}, {last: None}, {last: good[last].double()},
+                   {"step": None}, {"step": "x"}, {"step": -1}):
+        with pytest.raises((ValueError, TypeError)):
+            opt.load_state_dict({**good, **change})
+        assert opt.t == 0
+        for k, v in opt.state_dict().items():
+            if torch.is_tensor(v):
+                assert torch.equal(v.view(torch.uint8), kept[k].view(torch.uint8)), (change, k)
+    with pytest.raises(KeyError):
+        opt.load_state_dict({k: v for k, v in good.items() if k != "step"})
+    assert torch.equal(opt.m.view(torch.uint8), kept["m"].view(torch.uint8))
+    opt.load_state_dict(good)
+    assert opt.t == 7
+    assert torch.equal(opt.v.view(torch.uint8), good["v"].view(torch.uint8))
