@@ -368,7 +368,7 @@ class AdamW:
         self._master = torch.zeros(total, device=dev) if master else None
         if master:
             for p, a in zip(self.params, self.starts):
-                self.master[a:a + p.numel()].copy_(p.reshape(-1))
+                self.master[a:a + p.numel()].copy_(p.detach().reshape(-1))
         self._hyper = lrm.lrm_adamw(lr, betas[0], betas[1], eps, 1, None)
         self._table = (lrm.lrm_adamw_tensor * n)()
         for i, (p, a) in enumerate(zip(self.params, self.starts)):
@@ -446,5 +446,5 @@ class AdamW:
                                      f"{other.dtype} {tuple(other.shape)}")
                 pairs.append((mine, other))
         for mine, other in pairs:  # all of them checked
-            mine.copy_(other)
+            mine.copy_(other.detach())
         self.t = t

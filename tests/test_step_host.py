@@ -307,3 +307,21 @@ def test_adamw_refused_state_changes_nothing(host, state):
     opt.load_state_dict(good)
     assert opt.t == 7
     assert torch.equal(opt.v.view(torch.uint8), good["v"].view(torch.uint8))
+
+
+def test_adamw_state_is_no_part_of_a_graph(host):
+    """Parameters that autograd tracks: their master copies are plain numbers, and a state
+    that is loaded from tracked tensors stays so."""
+    import copy
+
+    p = torch.nn.Parameter(torch.ones(300, dtype=torch.bfloat16))
+    opt = host.layer.AdamW([p], [torch.ones(300)], master=True)
+    assert (opt.master[:300] == 1).all()
+    other = host.layer.AdamW([p], [torch.ones(300)], master=True)
+    state = {**other.state_dict(), "m": other.m.clone().requires_grad_(True)}
+    opt.load_state_dict(state)
+    for k, v in opt.state_dict().items():
+        if torch.is_tensor(v):
+            assert not v.requires_grad and v.grad_fn is None, k
+    copy.deepcopy(opt.state_dict())
+    opt.step()
