@@ -502,11 +502,15 @@ static RowPlan plan_rows(int64_t rows, int D, int upt, int pieces) {
   return p;
 }
 
+// Lets a kernel have `smem` bytes of dynamic shared memory. The limit is the
+// kernel's, for all host threads, so it is only ever set to the most that any call
+// needs: a smaller call in another thread cannot lower it before this one's launch.
 template <typename K>
 static bool allow_smem(K kern, size_t smem) {
   if (smem <= 40 * 1024) return true;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) ==
-      cudaSuccess)
+  if (smem <= kNormRing &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormRing) ==
+          cudaSuccess)
     return true;
   (void)cudaGetLastError();
   return false;
@@ -531,15 +535,19 @@ static lrm_status launch_norm_bwd(const lrm_norm* n, const NormBwd& a, cudaStrea
   const int sums = p.threads / std::max(p.tpr, 32);
   if (sums > 1) p.smem = std::max(p.smem, (size_t)sums * n->D * 4);
   auto kern = rmsnorm_bwd_kernel<T, G, UPT>;
-  if (!allow_smem(kern, p.smem)) return LRM_ERR_CUDA;
-  launch_k(kern, dim3((unsigned)p.ctas), dim3(p.threads), p.smem, cs, (const G*)a.dy,
-           (const G*)a.dh, (const T*)a.h, (const T*)a.w, a.rstd, (G*)a.dx,
-           p.ctas == 1 ? a.dw : a.part, n->T, n->D, p.tpr, p.stages);
+  // both before the first launch: a refusal leaves dx and dw as they were
+  if (!allow_smem(kern, p.smem) || (p.ctas > 1 && !allow_smem(dw_sum_kernel, p.smem)))
+    return LRM_ERR_CUDA;
+  if (launch_k(kern, dim3((unsigned)p.ctas), dim3(p.threads), p.smem, cs, (const G*)a.dy,
+               (const G*)a.dh, (const T*)a.h, (const T*)a.w, a.rstd, (G*)a.dx,
+               p.ctas == 1 ? a.dw : a.part, n->T, n->D, p.tpr, p.stages) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return LRM_ERR_CUDA;
+  }
   if (p.ctas > 1) {
     // It asks for the same shared memory, which it does not use: an SM that had
     // to change its split of L1 would start it later (9.7 us instead of 8.6 for
     // both kernels at T 1021 D 2048).
-    if (!allow_smem(dw_sum_kernel, p.smem)) return LRM_ERR_CUDA;
     launch_k(dw_sum_kernel, dim3((n->D + 31) / 32), dim3(kColThreads), p.smem, cs,
              (const float*)a.part, (int)p.ctas, n->D, a.dw);
   }

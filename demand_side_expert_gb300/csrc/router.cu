@@ -827,10 +827,16 @@ static lrm_status launch_route(const lrm_router* r, const void* logits, const ui
   float* part_z = reinterpret_cast<float*>(part + (size_t)kRouterMaxCtas * r->E);
   auto kern = stats ? route_kernel<T, NI, G, KC, true> : route_kernel<T, NI, G, KC, false>;
   const size_t smem = stats ? ((size_t)nwarp + 1) * r->E * 4 : 0;
+  // The limit is the kernel's, for all host threads, so it is only ever set to the
+  // most that any call needs: a smaller call in another thread cannot lower it
+  // before this one's launch.
+  constexpr int kMostSmem = (kMaxWarps + 1) * NI * G * 4;
   if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
-          cudaSuccess)
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) !=
+          cudaSuccess) {
+    (void)cudaGetLastError();
     return LRM_ERR_CUDA;
+  }
   if (launch_k(kern, dim3((unsigned)grid), dim3(nwarp * 32), smem, cs, (const T*)logits, mask,
                r->T, r->E, r->K, r->stride, (int)chunks_aligned<T, NI, G>(r->stride), r->renorm,
                r->balance_coef, r->z_coef, topk_idx, alpha, counts, prob_sum, loss, part, part_z) != cudaSuccess) {

@@ -100,3 +100,67 @@ def test_first_expert_calls_on_another_stream(dev, other_stream):
     got = first_call(other_stream, (T, K), torch.float32,
                      lambda st: p.gate_grad(x, stream=st), lambda: p.dalpha)
     assert torch.equal(got, want)
+
+
+# -- several host threads -------------------------------------------------------
+def in_threads(jobs, times):
+    """Every job in a thread and on a stream of its own; the errors that came up."""
+    import threading
+
+    errors = []
+
+    def work(job):
+        stream = torch.cuda.Stream()
+        try:
+            for _ in range(times):
+                job(stream)
+        except Exception as e:
+            errors.append(repr(e))
+        stream.synchronize()
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(job,)) for job in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    return errors
+
+
+@pytest.mark.parametrize("copies", [1, 2])
+def test_norm_gradients_in_threads(dev, copies):
+    """Calls with different needs of shared memory on the same kernels (f32, two units a
+    thread, 96 bytes a unit: 49 KB for a row of 4096 a CTA, 98 KB for two) at the same
+    time."""
+    from demand_side_expert_gb300 import AddRMSNorm
+
+    jobs, want = [], []
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    for T, D in ((2 * sms, 4096), (sms, 4096)) * copies:
+        x, w = torch.randn(T, D, device=dev), torch.ones(D, device=dev)
+        n = AddRMSNorm(T, D, "f32")
+        n.forward(x, w)
+        n.backward(x, w, dh=x, h=x)
+        want.append((n, n.dx.clone(), n.dw.clone()))
+        jobs.append(lambda st, n=n, x=x, w=w: n.backward(x, w, dh=x, h=x, stream=st))
+    assert in_threads(jobs, 5000) == []
+    for n, dx, dw in want:
+        assert torch.equal(n.dx, dx) and torch.equal(n.dw, dw)
+
+
+def test_routers_in_threads(dev):
+    """The same of the router's statistics: 64 KB for 512 experts, 50 KB for 400."""
+    from demand_side_expert_gb300 import Router
+
+    jobs, want = [], []
+    for E in (400, 512, 400, 512):
+        x = torch.randn(9000, E, device=dev).bfloat16()
+        r = Router(9000, E, 4, "bf16")
+        r.route(x)
+        want.append((r, r.alpha.clone(), r.prob_sum.clone(), r.loss.clone()))
+        jobs.append(lambda st, r=r, x=x: r.route(x, stream=st))
+    assert in_threads(jobs, 5000) == []
+    for r, alpha, prob_sum, loss in want:
+        assert torch.equal(r.alpha, alpha) and torch.equal(r.prob_sum, prob_sum)
+        assert torch.equal(r.loss, loss)
