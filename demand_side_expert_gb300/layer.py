@@ -97,7 +97,7 @@ class Router:
             self._loss = empty(2)
         self._dlogits = None
         # what backward may read: ids and counts of a route, or written by the caller since
-        self._routed = self._counted = False
+        self._routed = self._counted = T == 0  # no token, nothing to read
         self._idx_at, self._counts_at = self._topk_idx._version, self._counts._version
         self._ref = ctypes.byref(self.desc)
         self._at = tuple(t.data_ptr() for t in (self._topk_idx, self._alpha, self._counts,
@@ -132,7 +132,7 @@ class Router:
             counts = prob_sum = loss = None
         _route(self._ref, logits.data_ptr(), _address(mask), topk_idx, alpha, counts, prob_sum,
                loss, ws, self.ws_bytes, at)
-        self._routed, self._counted = True, stats
+        self._routed, self._counted = True, stats or self.T == 0
         if not stats:
             self._counts_at = self._counts._version
 

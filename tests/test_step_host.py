@@ -325,3 +325,12 @@ def test_adamw_state_is_no_part_of_a_graph(host):
             assert not v.requires_grad and v.grad_fn is None, k
     copy.deepcopy(opt.state_dict())
     opt.step()
+
+
+def test_router_without_tokens_needs_no_counts(host):
+    x = torch.zeros(0, 8)
+    r = host.layer.Router(0, 8, 2)
+    r.backward(x)
+    r.route(x, stats=False)
+    r.backward(x)
+    assert [name for name, _ in host.calls].count("_route_bwd") == 2
