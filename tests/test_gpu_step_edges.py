@@ -164,3 +164,41 @@ def test_routers_in_threads(dev):
     for r, alpha, prob_sum, loss in want:
         assert torch.equal(r.alpha, alpha) and torch.equal(r.prob_sum, prob_sum)
         assert torch.equal(r.loss, loss)
+
+
+# -- routing weights' gradient ----------------------------------------------------
+def gate_grad_of(g, y, inv, K, dev):
+    """dalpha and the device error word; g, y, inv on the device."""
+    from demand_side_expert_gb300 import lrm
+
+    T, D = g.shape
+    shape = lrm.make_shape(T, D, 8, max(K, 4), K,
+                           lrm.LRM_BF16 if g.dtype is torch.bfloat16 else lrm.LRM_F32)
+    n = lrm.lrm_workspace_bytes(shape)
+    ws = torch.zeros(n, dtype=torch.uint8, device=dev)
+    out = torch.full((T, K), float("nan"), device=dev)
+    lrm.lrm_gate_grad(shape, g, y, inv, out, ws, n)
+    return out, lrm.lrm_get_device_error(ws, n)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [1, 2, 4, 8, 9])
+@pytest.mark.parametrize("tokens_per_sm", [0, 3])
+def test_gate_grad_bad_entries_beside_infinities(dev, tokens_per_sm, K, dtype):
+    """A bad entry of inv gives 0 also where the token's cotangent is infinite or NaN; a
+    warp a token (3 tokens an SM) and a CTA a token (4 tokens)."""
+    from demand_side_expert_gb300 import lrm
+
+    T = tokens_per_sm * torch.cuda.get_device_properties(dev).multi_processor_count or 4
+    D = 72
+    gen = torch.Generator().manual_seed(K)
+    g = torch.randn(T, D, generator=gen)
+    g[0, 3], g[T - 1, 71] = float("inf"), float("nan")
+    y = torch.randn(T * K, D, generator=gen)
+    inv = torch.randperm(T * K, generator=gen).to(torch.int32)
+    inv[0], inv[T * K - 1] = T * K, -1
+    out, err = gate_grad_of(g.to(DT[dtype]).to(dev), y.to(DT[dtype]).to(dev), inv.to(dev), K, dev)
+    assert out[0, 0].item() == 0 and out[T - 1, K - 1].item() == 0
+    assert not torch.isfinite(out[0, 1:]).any() and not torch.isfinite(out[T - 1, :K - 1]).any()
+    assert torch.isfinite(out[1:T - 1]).all()
+    assert err == lrm.LRM_DEVERR_INDEX
