@@ -80,9 +80,9 @@ gate_grad_kernel(const T* __restrict__ g, const T* __restrict__ y,
   const int64_t dt = (int64_t)gridDim.x * kTokens;
   const uint32_t mine = (uint32_t)__cvta_generic_to_shared(ring + threadIdx.x);
 
-  // copies: token, first row of the pass, step, the rows' positions
+  // copies: token, step, the rows' positions
   int64_t ct = t0;
-  int ck = 0, cs = 0;
+  int cs = 0;
   int row[R];
   // lane r: position of row r of a pass; a bad entry reads nothing
   bool bad = false;
@@ -127,7 +127,6 @@ gate_grad_kernel(const T* __restrict__ g, const T* __restrict__ y,
       if (++cs == steps) {
         cs = 0;
         ct = nt;
-        ck = nk;
         spread(next_pos);
         nk += R;
         if (nk >= K) {
