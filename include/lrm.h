@@ -469,8 +469,11 @@ lrm_status lrm_select_rate(const lrm_shape* shape, const float* score, const int
  *   loss[1] = z_coef / n * sum_t lse_t^2
  * Tokens that take no part get alpha = 0 and K valid, distinct ids (of their
  * logits, by the same rule); they count nowhere. In a token that takes part,
- * NaN and +inf logits make its weights and the statistics NaN. FP32 arithmetic; the
- * statistics are added in a fixed order (same inputs, same bits).
+ * NaN and +inf logits make its weights and the statistics NaN. FP32 arithmetic: alpha,
+ * the losses and float32 gradients keep its accuracy at any distance from the row's
+ * largest logit; prob_sum is off by up to 7e-8 of an expert's share for each unit that
+ * it stands below the largest (shares under 2^-126 count as 0). The statistics are
+ * added in a fixed order (same inputs, same bits).
  *   logits [T,E] dtype (read), rows `stride` elements apart (stride >= E).
  *   mask [T] uint8 (read) or NULL, any alignment.
  *   topk_idx [T,K] int32, alpha [T,K] float (written).

@@ -202,3 +202,52 @@ def test_gate_grad_bad_entries_beside_infinities(dev, tokens_per_sm, K, dtype):
     assert not torch.isfinite(out[0, 1:]).any() and not torch.isfinite(out[T - 1, :K - 1]).any()
     assert torch.isfinite(out[1:T - 1]).all()
     assert err == lrm.LRM_DEVERR_INDEX
+
+
+# -- router: far tails ------------------------------------------------------------
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T,E", [(64, 8), (64, 300), (5000, 8), (5000, 200)])
+def test_route_weights_far_below_the_largest(dev, T, E, dtype, renorm):
+    """Weights of 1e-13 down to the smallest number keep float32's relative accuracy, and so
+    do float32 gradients. The logits are whole numbers and the largest is 0, so differences
+    are exact; every other weight is below 2^-43, so sums of up to 300 round to 1 in float32
+    and are 1 + 4e-11 at most. What is left is the exponential (2 ulp) and one product."""
+    from demand_side_expert_gb300 import Router
+
+    K, low = 8, 103
+    t, e = torch.arange(T)[:, None], torch.arange(E)[None]
+    x = -(30 + (t * 7 + e * 11) % (low - 29)).float()
+    x[:, 3] = 0
+    r = Router(T, E, K, dtype, renorm=renorm, balance_coef=0.0, z_coef=0.0)
+    xd = x.to(DT[dtype]).to(dev)
+    r.route(xd)
+    idx = r.topk_idx.cpu().long()
+    p = torch.exp(x.double())
+    want = p.gather(1, idx)
+    err = (r.alpha.cpu().double() - want).abs()
+    assert (err <= 6 * U * want + 2.0 ** -149).all(), (err / want).max().item() / U
+
+    # dalpha 1 at the choices but the first: dx = a there, to the rest's share of 1e-12,
+    # and minus their sum at the first
+    r.backward(xd, (idx != 3).float().to(dev))
+    got = r.dlogits.cpu().double().gather(1, idx)[:, 1:]
+    # two exponentials' roundings and four products; the gradient's own type
+    lim = (12 * U + (0 if dtype == "f32" else 2.0 ** -8)) * want[:, 1:]
+    # below 2^-126 a product may be rounded twice to a multiple of 2^-149 (2^-133)
+    lim = lim + (2.0 ** -148 if dtype == "f32" else 2.0 ** -126)
+    assert ((got - want[:, 1:]).abs() <= lim).all()
+
+
+def test_route_z_loss_of_even_logits(dev):
+    """log 2 and log 3 to float32's accuracy: a token's lse is a logarithm and one sum."""
+    import math
+
+    from demand_side_expert_gb300 import Router
+
+    for E in (2, 3):
+        r = Router(1, E, 1, "f32", balance_coef=0.0, z_coef=1.0)
+        r.route(torch.zeros(1, E, device=dev))
+        want = math.log(E) ** 2
+        # the logarithm 2 ulp = 4 u, squared twice that, and one product
+        assert abs(r.loss[1].item() - want) <= 10 * U * want
