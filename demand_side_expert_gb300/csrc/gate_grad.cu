@@ -192,20 +192,24 @@ gate_grad_kernel(const T* __restrict__ g, const T* __restrict__ y,
   }
 }
 
+// Bytes of a CTA's ring, and CTAs that fit an SM's shared memory with theirs.
+constexpr size_t gate_smem(int R) {
+  return (size_t)kGateSteps * gate_pieces(R) * (R + 1) * kGateThreads * 16;
+}
+constexpr int64_t gate_per_sm(int R) { return 227 * 1024 / (gate_smem(R) + 2048); }
+
 template <typename T, int TPT, int R>
 static lrm_status launch_gate(const lrm_shape* s, const void* g, const void* y,
                               const int32_t* inv, float* dalpha, int32_t* err,
                               cudaStream_t cs) {
-  constexpr size_t kSmem =
-      (size_t)kGateSteps * gate_pieces(R) * (R + 1) * kGateThreads * 16;
-  constexpr int64_t kPerSm = 227 * 1024 / (kSmem + 2048);  // CTAs that fit an SM's shared memory
+  constexpr size_t kSmem = gate_smem(R);
   const int64_t need = ((int64_t)s->T * TPT + kGateThreads - 1) / kGateThreads;
   // More CTAs than fit at once, so that an SM which starts late or reads slowly
   // gets fewer tokens. Behind lrm_route_bwd (T 16384 D 4096, both, us): 210, 187,
   // 181 and 177 for 1, 4, 8 and 16 times as many as fit; a warp a token
   // (D 256): 27.4, 24.0 and 24.5 for 1, 3 and 4.
   constexpr int64_t kTimes = TPT == 32 ? 3 : 16;
-  const int blocks = (int)std::min<int64_t>(need, num_sms() * kPerSm * kTimes);
+  const int blocks = (int)std::min<int64_t>(need, num_sms() * gate_per_sm(R) * kTimes);
   auto kern = gate_grad_kernel<T, TPT, R>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
       cudaSuccess) {
@@ -217,28 +221,39 @@ static lrm_status launch_gate(const lrm_shape* s, const void* g, const void* y,
   return launch_status();
 }
 
-template <typename T, int TPT>
-static lrm_status pick_rows(const lrm_shape* s, const void* g, const void* y, const int32_t* inv,
-                            float* dalpha, int32_t* err, cudaStream_t cs) {
-  if (s->K == 1) return launch_gate<T, TPT, 1>(s, g, y, inv, dalpha, err, cs);
-  if (s->K == 2) return launch_gate<T, TPT, 2>(s, g, y, inv, dalpha, err, cs);
-  if (s->K <= 4) return launch_gate<T, TPT, 4>(s, g, y, inv, dalpha, err, cs);
-  return launch_gate<T, TPT, kGateRows>(s, g, y, inv, dalpha, err, cs);
+// A CTA a token where every token's CTA is resident at once and a token has 8 KB or
+// more (a warp a token would leave SMs with a few warps each), and for any number of
+// tokens of 35 KB or more where four CTAs fit an SM (not so with R = 4); a warp a token
+// else. Measured (warp | CTA, us), bf16:
+//   K 8        T 305        600        900        1500       6000       16384
+//   D  512     3.2 |  3.2   3.9 | 4.0  4.4 | 5.6  5.5 | 7.5  12.2|20.8  27.6| 47.2
+//   D 1000     4.4 |  4.0   5.4 | 5.2  6.3 | 6.7  8.8 | 8.8  21.6|25.9  51.1| 56.6
+//   D 2040     6.5 |  5.4   7.5 | 7.3  9.1 | 9.1  13.6|12.4  38.3|37.8  97.6| 94.7
+//   D 4096     9.0 |  7.1  11.2 |10.4 13.9 |14.4  22.0|21.2  68.9|67.0 178.7|169.5
+//   K 4 D 4096 6.3 |  5.2   7.5 | 7.7  9.1 | 9.7  13.0|13.2  39.2|42.3 100.1|100.9
+//   K 2 D 4096 4.7 |  4.4   5.8 | 5.8  7.1 | 7.5   9.8| 9.9  26.3|29.7  62.2| 68.1
+//   K 1 D  512 2.6 |  2.8   2.8 | 3.0  2.8 | 4.2   3.2| 5.8   7.0|16.9  10.8| 34.5
+// and float32: K 8 D 1000 (36 KB) 12.4 | 11.9 at T 1500, 92.3 | 90.2 at 16384; K 2
+// D 4096 (48 KB) 15.3 | 14.7, 115.2 | 115.6; bf16 K 16 D 1000 (34 KB) 13.4 | 12.8,
+// 93.5 | 95.8.
+template <typename T, int R>
+static lrm_status pick_threads(const lrm_shape* s, const void* g, const void* y,
+                               const int32_t* inv, float* dalpha, int32_t* err,
+                               cudaStream_t cs) {
+  const int64_t token = ((int64_t)s->K + 1) * s->D * (int64_t)sizeof(T);
+  if ((token >= 8 * 1024 && s->T <= num_sms() * gate_per_sm(R)) ||
+      (token >= 35 * 1024 && gate_per_sm(R) >= 4))
+    return launch_gate<T, kGateThreads, R>(s, g, y, inv, dalpha, err, cs);
+  return launch_gate<T, 32, R>(s, g, y, inv, dalpha, err, cs);
 }
 
-// A CTA a token where a token's rows are 36 KB or more, or where there are at
-// most two tokens an SM; a warp a token else. Measured (bf16, warp | CTA, us):
-// T 16384: D 4096 K 8 (72 KB) 178.6 | 169.2, D 4096 K 4 (40 KB) 99.4 | 101.1,
-// D 2048 K 8 (36 KB) 92.1 | 91.2, D 4096 K 2 (24 KB) 61.8 | 69.1, D 1024 K 8 48.9 |
-// 55.8, D 2048 K 1 23.7 | 42.8; T 200: D 4096 K 8 6.9 | 4.3, D 1024 K 8 3.2 | 2.7,
-// D 512 K 8 2.6 | 2.6.
 template <typename T>
 static lrm_status pick_gate(const lrm_shape* s, const void* g, const void* y, const int32_t* inv,
                             float* dalpha, int32_t* err, cudaStream_t cs) {
-  const int64_t token = ((int64_t)s->K + 1) * s->D * (int64_t)sizeof(T);
-  if (token >= 36 * 1024 || s->T <= 2 * num_sms())
-    return pick_rows<T, kGateThreads>(s, g, y, inv, dalpha, err, cs);
-  return pick_rows<T, 32>(s, g, y, inv, dalpha, err, cs);
+  if (s->K == 1) return pick_threads<T, 1>(s, g, y, inv, dalpha, err, cs);
+  if (s->K == 2) return pick_threads<T, 2>(s, g, y, inv, dalpha, err, cs);
+  if (s->K <= 4) return pick_threads<T, 4>(s, g, y, inv, dalpha, err, cs);
+  return pick_threads<T, kGateRows>(s, g, y, inv, dalpha, err, cs);
 }
 
 }  // namespace lrm

@@ -251,3 +251,51 @@ def test_route_z_loss_of_even_logits(dev):
         want = math.log(E) ** 2
         # the logarithm 2 ulp = 4 u, squared twice that, and one product
         assert abs(r.loss[1].item() - want) <= 10 * U * want
+
+
+def check_gate_grad(T, D, K, dtype, dev, bad=True):
+    """All of dalpha against float64 sums; with a bad entry of inv in the middle."""
+    from demand_side_expert_gb300 import lrm
+
+    gen = torch.Generator(device=dev).manual_seed(T + D + K)
+    g = torch.empty(T, D, dtype=DT[dtype], device=dev).normal_(generator=gen)
+    y = torch.empty(T * K, D, dtype=DT[dtype], device=dev).normal_(generator=gen)
+    inv = torch.randperm(T * K, generator=gen, device=dev).to(torch.int32)
+    spot = (T // 2) * K + K - 1
+    if bad:
+        inv[spot] = T * K
+    out, err = gate_grad_of(g, y, inv, K, dev)
+    assert err == (lrm.LRM_DEVERR_INDEX if bad else 0)
+    for t in range(0, T, 1024):
+        rows = y[inv[t * K:(t + 1024) * K].long().clamp(max=T * K - 1)].double()
+        rows = rows.view(-1, K, D)
+        prod = rows * g[t:t + 1024, None].double()
+        want, mag = prod.sum(2), prod.abs().sum(2)
+        if bad and t <= T // 2 < t + 1024:
+            want.view(-1)[spot - t * K] = 0
+            assert out.view(-1)[spot].item() == 0
+        # D terms, each product's and each sum's rounding
+        off = (out[t:t + 1024].double() - want).abs() > (D + 1) * U * mag
+        assert not off.any(), (t, int(off.sum()))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("K", [1, 2, 3, 8, 9, 32])
+@pytest.mark.parametrize("D", [8, 72, 1000])
+def test_gate_grad_by_warps(dev, D, K, dtype):
+    """A warp a token, past the number of warps a grid has (at most 4 a CTA, 3 rounds of 4
+    CTAs an SM): tokens follow one another in a warp, in several passes for K > 8."""
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    if (K + 1) * D * torch.finfo(DT[dtype]).bits // 8 >= 35 * 1024:
+        pytest.skip("a CTA a token")
+    check_gate_grad(sms * 48 + 1203, D, K, dtype, dev)
+
+
+@pytest.mark.parametrize("T,D,K,dtype", [
+    (64, 2040, 8, "bf16"), (64, 1000, 8, "f32"), (64, 1000, 20, "bf16"), (64, 504, 32, "f32"),
+    (2, 1000, 9, "f32"), (2, 4104, 1, "bf16"), (2, 2056, 2, "f32"), (2, 4088, 4, "bf16"),
+    (2, 2056, 3, "f32")])
+def test_gate_grad_by_ctas(dev, T, D, K, dtype):
+    """A CTA a token, T tokens an SM and some: 64 is past the number of CTAs a grid has."""
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    check_gate_grad(sms * T + 101, D, K, dtype, dev, bad=K > 1)
