@@ -299,3 +299,235 @@ def test_gate_grad_by_ctas(dev, T, D, K, dtype):
     """A CTA a token, T tokens an SM and some: 64 is past the number of CTAs a grid has."""
     sms = torch.cuda.get_device_properties(dev).multi_processor_count
     check_gate_grad(sms * T + 101, D, K, dtype, dev, bad=K > 1)
+
+
+# -- norm: the forms of large blocks -----------------------------------------------
+def norm_of(x, res, w, eps):
+    """h, rstd and y in 64 bits."""
+    h = x.double() if res is None else x.double() + res.double()
+    rstd = (h.square().mean(1) + eps).rsqrt()
+    return h, rstd, h * rstd[:, None] * w.double()
+
+
+def within(got, want, lim, name):
+    off = (got.double() - want).abs() > lim
+    assert not off.any(), (name, int(off.sum()), (got.double() - want).abs().max().item())
+
+
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D", [264, 1000, 1032, 2040, 4088, 8184, 8200])
+def test_norm_forward_of_large_blocks(dev, D, dtype, residual):
+    """More than 16384 values an SM, where several units a thread (and for bfloat16 rows
+    without a residual other threads a row) take over: every output, each width of the
+    8-bit groups."""
+    from demand_side_expert_gb300 import AddRMSNorm
+
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    T, eps = sms * 16384 // D + 3, 1e-5
+    gen = torch.Generator(device=dev).manual_seed(D)
+    dt = DT[dtype]
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=gen, device=dev)
+
+    x, w = randn(T, D).to(dt), (1 + 0.2 * randn(D)).to(dt)
+    res = (3 * randn(T, D)).to(dt) if residual else None
+    h, rstd, y = norm_of(x, res, w, eps)
+    out = 2.0 ** -8 if dtype == "bf16" else 0.0  # the rounding of a stored value
+    rs = (D + 8) * U  # D squares and sums, a division, a root
+    mag = y.abs()
+    h_lim = U * (x.double().abs() + (0 if res is None else res.double().abs()))
+    if residual:  # the rounding of the sum reaches y times rstd w
+        mag = mag + h_lim / U * rstd[:, None] * w.double().abs()
+    y_lim = (rs + 4 * U) * mag
+    for q_cols in (None, 0, 32, 64, 128, 256):
+        n = AddRMSNorm(T, D, dtype, eps=eps, q_cols=q_cols, store_y=q_cols in (None, 64))
+        n.forward(x, w, residual=res)
+        within(n.rstd, rstd, rs * rstd, "rstd")
+        if residual:
+            within(n.h, h, out * h.abs() + 2 * h_lim, "h")
+        if n.y is not None:
+            within(n.y, y, out * y.abs() + y_lim, "y")
+        if q_cols is None:
+            continue
+        cols = q_cols or D
+        groups = -(-D // cols)
+        pad = (0, groups * cols - D)
+        top = torch.nn.functional.pad(y.abs(), pad).view(T, groups, cols).amax(2) / 448
+        slack = torch.nn.functional.pad(y_lim, pad).view(T, groups, cols).amax(2) / 448
+        within(n.q_scale, top, slack + 4 * U * top, "q_scale")
+        scale = n.q_scale.double().repeat_interleave(cols, 1)[:, :D]
+        # half a step of the code: 2^-4 of a normal value, 2^-10 below
+        half = torch.maximum(y.abs() * 2.0 ** -4, scale * 2.0 ** -10)
+        within(n.q.double() * scale, y, half * (1 + 1e-3) + 4 * y_lim, "q")
+
+
+@pytest.mark.parametrize("grad", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("D,rows_per_sm", [(16384, 4), (8200, 7), (8192, 9), (1032, 40), (72, 300)])
+def test_norm_backward_of_many_rows(dev, D, rows_per_sm, dtype, grad):
+    """More rows a CTA than its ring has places, at every depth of the ring: the places are
+    used again and again. With the residual stream's gradient."""
+    from demand_side_expert_gb300 import AddRMSNorm
+
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    T = rows_per_sm * sms + 5
+    gen = torch.Generator(device=dev).manual_seed(D)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=gen, device=dev)
+
+    x, w = randn(T, D).to(DT[dtype]), (1 + 0.2 * randn(D)).to(DT[dtype])
+    dy, dh = randn(T, D).to(DT[grad]), randn(T, D).to(DT[grad])
+    n = AddRMSNorm(T, D, dtype, eps=1e-5, grad_dtype=grad)
+    n.forward(x, w)
+    n.backward(dy, w, dh=dh, h=x)
+    rstd, d64, w64 = n.rstd.double()[:, None], dy.double(), w.double()
+    xhat, wdy = x.double() * rstd, dy.double() * w64
+    dx = rstd * (wdy - xhat * (wdy * xhat).mean(1, keepdim=True)) + dh.double()
+    # D products and sums of the row's mean, and 8 roundings of what it is taken from
+    mag = rstd * (wdy.abs() * 8 + xhat.abs() * (wdy * xhat).abs().mean(1, keepdim=True) * (D + 8))
+    lim = U * (mag + 2 * dh.double().abs())
+    if grad == "bf16":
+        lim = lim + 2.0 ** -8 * dx.abs()
+    within(n.dx, dx, lim, "dx")
+    within(n.dw, (d64 * xhat).sum(0), (T + 3) * U * (d64 * xhat).abs().sum(0), "dw")
+
+
+# -- router: rounds and shared memory of many tokens ----------------------------------
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,K,dtype", [(20, 3, "f32"), (32, 12, "bf16"), (64, 8, "bf16"),
+                                       (100, 8, "f32"), (128, 16, "bf16"), (250, 8, "bf16"),
+                                       (250, 20, "f32")])
+def test_route_gradient_of_many_tokens(dev, E, K, dtype, renorm):
+    """More tokens than a grid takes at once (8 CTAs an SM of 8 warps, up to 4 tokens each):
+    the choices of the second round are read during the first."""
+    from demand_side_expert_gb300 import Router
+
+    sms = torch.cuda.get_device_properties(dev).multi_processor_count
+    T = sms * 8 * 32 + 2003
+    gen = torch.Generator(device=dev).manual_seed(E)
+    x = (2 * torch.randn(T, E, generator=gen, device=dev)).to(DT[dtype])
+    mask = torch.rand(T, generator=gen, device=dev) < 0.9
+    da = torch.randn(T, K, generator=gen, device=dev)
+    dl = torch.tensor([1.5, -0.5], device=dev)
+    c_b, c_z = 50.0, 200.0
+    r = Router(T, E, K, dtype, renorm=renorm, balance_coef=c_b, z_coef=c_z)
+    r.route(x, mask=mask)
+    r.backward(x, da, mask=mask, dloss=dl)
+    x64 = x.double()
+    idx = x64.sort(dim=1, descending=True, stable=True).indices[:, :K]
+    assert torch.equal(r.topk_idx.long(), idx)
+    lse = x64.logsumexp(1)
+    p = (x64 - lse[:, None]).exp()
+    n = int(mask.sum())
+    counts = torch.zeros(E, dtype=torch.int64, device=dev)
+    counts.scatter_add_(0, idx[mask].reshape(-1), torch.ones(n * K, dtype=torch.int64, device=dev))
+    assert torch.equal(r.counts.long(), counts)
+    cost = 1.5 * c_b * E * counts.double() / (n * n * K)
+    chosen, d64 = p.gather(1, idx), da.double()
+    want = p * (cost - (p * cost).sum(1, keepdim=True)) - (p * c_z * lse[:, None] / n)
+    a = torch.zeros_like(p)
+    if renorm:
+        w = chosen / chosen.sum(1, keepdim=True)
+        own = w * (d64 - (w * d64).sum(1, keepdim=True))
+        a.scatter_(1, idx, w)
+    else:
+        dp = torch.zeros_like(p).scatter_(1, idx, d64)
+        want, own = want + p * (dp - (p * dp).sum(1, keepdim=True)), torch.zeros_like(d64)
+    want = want.scatter_add(1, idx, own) * mask[:, None]
+    # p and the weights: their exponential at a distance of up to `span` (2 span u), E terms
+    # of the sum; they multiply dalpha, its mean, the cost, its mean and lse
+    span = (x64.max() - x64.min()).item()
+    tol = (2 * span + E + 16) * U
+    scale = 2 * d64.abs().amax(1) + 2 * cost.max() + c_z / n * (lse.abs() + 1)
+    lim = (3 * tol + (K + E + 16) * U) * torch.maximum(a, p) * scale[:, None]
+    if dtype == "bf16":
+        lim = lim + 2.0 ** -8 * want.abs()
+    within(r.dlogits, want, lim + 1e-37, "dlogits")
+
+
+@pytest.mark.parametrize("T,E,K,dtype", [(9001, 400, 6, "bf16"), (9001, 512, 4, "bf16"),
+                                         (5003, 320, 8, "bf16"), (9001, 512, 4, "f32"),
+                                         (9001, 1000, 8, "bf16")])
+def test_route_statistics_in_much_shared_memory(dev, T, E, K, dtype):
+    """Statistics of 311 to 512 experts and thousands of bfloat16 tokens are the ones whose
+    sums take more shared memory than a kernel has unasked; and those beside them."""
+    from demand_side_expert_gb300 import Router
+
+    gen = torch.Generator(device=dev).manual_seed(E)
+    x = torch.randn(T, E, generator=gen, device=dev).to(DT[dtype])
+    r = Router(T, E, K, dtype, balance_coef=0.3, z_coef=0.2)
+    r.route(x)
+    x64 = x.double()
+    idx = x64.sort(dim=1, descending=True, stable=True).indices[:, :K]
+    assert torch.equal(r.topk_idx.long(), idx)
+    counts = torch.bincount(idx.reshape(-1), minlength=E)
+    assert torch.equal(r.counts.long(), counts)
+    lse = x64.logsumexp(1)
+    p = (x64 - lse[:, None]).exp()
+    tol = (2 * (x64.max() - x64.min()).item() + E + 16) * U
+    within(r.alpha, p.gather(1, idx), 2 * tol * p.gather(1, idx), "alpha")
+    prob = p.sum(0)
+    within(r.prob_sum, prob, (tol + (T + 8) * U) * prob, "prob_sum")
+    loss = torch.stack([0.3 * E / (T * T * K) * (counts * prob).sum(), 0.2 * lse.square().mean()])
+    within(r.loss, loss, (2 * tol + (T + E + 16) * U) * loss, "loss")
+
+
+def test_router_through_the_c_names(dev):
+    """lrm_route and lrm_route_bwd of the binding on the caller's buffers give Router's."""
+    from demand_side_expert_gb300 import Router, lrm
+
+    T, E, K = 300, 24, 3
+    x = torch.randn(T, E, device=dev)
+    mask = (torch.arange(T, device=dev) % 5 != 0).to(torch.uint8)
+    da = torch.randn(T, K, device=dev)
+    r = Router(T, E, K, "f32", renorm=True, balance_coef=0.5, z_coef=0.25)
+    r.route(x, mask=mask)
+    r.backward(x, da, mask=mask)
+    desc = lrm.lrm_router(T, E, K, lrm.LRM_F32, E, 1, 0.5, 0.25)
+    size = lrm.lrm_router_workspace_bytes(desc)
+    ws = torch.zeros(size, dtype=torch.uint8, device=dev)
+    idx, counts = (torch.empty(n, dtype=torch.int32, device=dev) for n in ((T, K), (E,)))
+    alpha, prob, loss, dx = (torch.empty(n, device=dev) for n in ((T, K), (E,), (2,), (T, E)))
+    lrm.lrm_route(desc, x, mask, idx, alpha, counts, prob, loss, ws, size)
+    lrm.lrm_route_bwd(desc, x, mask, idx, counts, da, None, dx, ws, size)
+    for got, name in ((idx, "topk_idx"), (alpha, "alpha"), (counts, "counts"),
+                      (prob, "prob_sum"), (loss, "loss"), (dx, "dlogits")):
+        assert torch.equal(got, getattr(r, name)), name
+    assert lrm.lrm_get_device_error(ws, size) == 0
+
+
+# -- AdamW: more tensors than a launch describes ---------------------------------------
+@pytest.mark.parametrize("state", ["f32", "f8"])
+def test_adamw_of_many_tensors_of_mixed_kinds(dev, state):
+    """600 tensors of one kind are three launches; with another 40 of other types between
+    them each is stepped once, from its own place, like the same tensor alone."""
+    from demand_side_expert_gb300 import AdamW
+
+    gen = torch.Generator(device=dev).manual_seed(0)
+    params, grads = [], []
+    for i in range(640):
+        n = int(torch.randint(1, 700, (1,), generator=gen, device=dev))
+        p = torch.randn(n, generator=gen, device=dev)
+        g = torch.randn(n, generator=gen, device=dev)
+        if i % 16 == 7:
+            p, g = p.to(torch.bfloat16), (g if i % 32 == 7 else g.to(torch.bfloat16))
+        params.append(p)
+        grads.append(g)
+    alone = [p.clone() for p in params]
+    decay = [0.1 * (i % 3) for i in range(640)]
+    kw = dict(lr=1e-2, betas=(0.9, 0.95), state=state, master=True)
+    opt = AdamW(params, grads, weight_decay=decay, **kw)
+    for _ in range(2):
+        opt.step()
+    for i, (p, g) in enumerate(zip(alone, grads)):
+        one = AdamW([p], [g], weight_decay=decay[i], **kw)
+        for _ in range(2):
+            one.step()
+        assert torch.equal(p, params[i]), i
+        for name in ("m", "v"):
+            got, want = getattr(opt, name), getattr(one, name)[:p.numel()]
+            got = got[opt.starts[i]:opt.starts[i] + p.numel()]
+            assert torch.equal(got.view(torch.uint8), want.view(torch.uint8)), (i, name)
