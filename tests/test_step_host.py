@@ -155,17 +155,20 @@ def test_gate_grad_needs_expert_outputs(host):
 def test_other_devices_are_refused(monkeypatch):
     """The kernels launch on the current device: an object on another one's memory is
     refused where it is made, and its calls are while another device is current."""
-    from demand_side_expert_gb300 import layer, lrm
+    from demand_side_expert_gb300 import layer, lrm, pipeline
 
     monkeypatch.setattr(lrm, "current_device", lambda: 0)
     assert layer._device("cuda") == torch.device("cuda", 0) == layer._device("cuda:0")
     for other in ("cuda:1", torch.device("cuda", 7)):
         with pytest.raises(ValueError, match="current device"):
             layer._device(other)
-    monkeypatch.setattr(lrm, "stream_address", lambda stream=None: 5)
-    assert layer._stream(torch.device("cuda", 0), None) == 5
-    with pytest.raises(ValueError, match="current device"):
-        layer._stream(torch.device("cuda", 1), None)
+    monkeypatch.setattr(pipeline, "_device_now", lambda: 0)
+    monkeypatch.setattr(pipeline, "_stream_now", lambda index: 5 + index)
+    here = torch.device("cuda", 0)
+    assert layer._stream(here, None) == 5 and layer._stream(here, 9) == 9
+    for stream in (None, 9):
+        with pytest.raises(ValueError, match="current device"):
+            layer._stream(torch.device("cuda", 1), stream)
 
 
 def test_calls_run_on_the_device_of_their_buffers(host, monkeypatch):
