@@ -9,7 +9,8 @@
 // loads into registers got to 0.70-0.90 of the copy bandwidth (257-198 us at
 // T 16384 D 4096 K 8, bf16, by how many were unrolled), a ring of asynchronous
 // copies in shared memory gets to 1.05 (169 us, 7.1 TB/s); with its step made for
-// 8 rows whatever K, K 2 took 99 us where it takes 62.
+// 8 rows whatever K, K 2 took 99 us where it takes 62. Bad entries of inv cost only
+// where there are any.
 #include <algorithm>
 
 #include "common.cuh"

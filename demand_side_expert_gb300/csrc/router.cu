@@ -13,11 +13,11 @@
 // G lanes of a warp hold a token's row in registers, NI experts a lane, so a
 // row is read once and no shared memory is touched before the statistics. The
 // bytes are few (T 32768 E 128 bfloat16: 10.5 MB, 1.5 us); what bounds the
-// kernels is the minima, maxima and selections of a token (60% of the integer
-// pipe while a CTA runs) and, for few tokens, latency. So many tokens share a
-// warp (G = 8 or 16) and few get a whole one. Measured at T 32768 E 128 K 8:
-// choices and weights 7.3 us (bfloat16) and 9.5 us (float32), with the
-// statistics 11.8 and 15.2 us, the gradient 6.8 and 7.4 us.
+// kernels is the minima, maxima and selections of a token (at that size 60% of the
+// integer pipe's cycles with statistics and 66% without, 47% and 51% for float32) and,
+// for few tokens, latency. So many tokens share a warp (G = 8 or 16) and few get a
+// whole one. Measured at T 32768 E 128 K 8: choices and weights 7.2 us (bfloat16) and
+// 9.6 us (float32), with the statistics 11.9 and 15.3 us, the gradient 6.7 and 7.7 us.
 #include <math_constants.h>
 
 #include <algorithm>
@@ -41,8 +41,8 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 // A choice's key: the logit's order first, then the lower expert id, so that
-// keys are unique (a lane's places past E hold -inf and rank behind the row's). A bfloat16 leaves the low half of its 32 bits free for the
-// id; a float32 needs 64 bits.
+// keys are unique (a lane's places past E hold -inf and rank behind the row's). A
+// bfloat16 leaves the low half of its 32 bits free for the id; a float32 needs 64 bits.
 template <typename T>
 struct ChoiceKey;
 template <>
@@ -109,15 +109,15 @@ __device__ __forceinline__ float group_fmax(float v) {
 // that cannot be seen: in sums over a row (|x| e^x stays below 0.37), in prob_sum
 // (an expert's share of which is as small as it is far down) and in gradients that
 // are rounded to bfloat16. Weights and float32 gradients take expf. With expf for
-// the whole row too T 32768 E 128 K 8 bfloat16 takes 13.4 us with statistics instead
-// of 12.8, and its gradient 8.7 instead of 8.1.
+// the whole row too T 32768 E 128 K 8 bfloat16, ten inputs in turn, takes 13.4 us with
+// statistics instead of 12.9, and its gradient 8.7 instead of 8.1.
 __device__ __forceinline__ float exp_neg(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
   return y;
 }
-// The functions of a gradient in T. float32 pays for them: T 32768 E 128 K 8 takes
-// 9.3 us, 8.4 with the approximate ones.
+// The functions of a gradient in T. float32 pays for them: T 32768 E 128 K 8, ten
+// inputs in turn, takes 9.3 us, 8.4 with the approximate ones.
 template <typename T>
 __device__ __forceinline__ float exp_grad(float x) {
   if constexpr (sizeof(T) == 4) return expf(x);

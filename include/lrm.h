@@ -520,7 +520,7 @@ lrm_status lrm_route_bwd(const lrm_router* router, const void* logits, const uin
  *   g [T,D] dtype (cotangent at the MoE output), y [N,D] dtype (expert outputs
  *   in dispatch order, as lrm_expert_fc2_fwd leaves them), inv [N] int32 (read);
  *   dalpha [T,K] float (written).
- * inv entries outside [0,N) give 0 and flag LRM_DEVERR_INDEX.
+ * inv entries outside [0,N) give 0, whatever g holds, and flag LRM_DEVERR_INDEX.
  */
 lrm_status lrm_gate_grad(const lrm_shape* shape, const void* g, const void* y,
                          const int32_t* inv, float* dalpha, void* ws, size_t ws_bytes,
