@@ -10,100 +10,14 @@
 // (T 32768 D 2048 bfloat16, residual and 8-bit rows: 472 MB in 71 us, 0.97 of the
 // copy bandwidth; T 16384 D 4096 backward, float32 gradients: 940 MB in 138 us,
 // 1.00), and bound by latency and launches below.
-#include <cuda_fp8.h>
-
 #include <algorithm>
 
-#include "common.cuh"
+#include "rows.cuh"
 
 namespace lrm {
 
 constexpr int kNormMaxD = 16384;
 constexpr int kNormMaxCtas = 160;  // partial dw rows in the workspace
-constexpr float kF8Max = 448.f;    // largest e4m3 value
-constexpr float kF8MaxInv = 1.f / kF8Max;
-constexpr float kAmaxMin = 7.888609052210118e-31f;  // 2^-100
-
-// A unit is 8 consecutive elements: what one thread loads at a time.
-constexpr int kUnit = 8;
-
-// 16 bytes, or zeros: a predicated load, which no branch keeps apart from the
-// loads before and after it.
-__device__ __forceinline__ uint4 load_if(const void* p, bool ok) {
-  uint4 v;
-  asm volatile(
-      "{\n\t.reg .pred ok;\n\tsetp.ne.b32 ok, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@ok ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
-      : "l"(p), "r"((int)ok)
-      : "memory");
-  return v;
-}
-
-template <typename T>
-struct Unit8 {
-  uint4 v[sizeof(T) / 2];
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ void load(const T* p, bool ok) {
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-      v[i] = load_if(reinterpret_cast<const uint4*>(p) + i, ok);
-  }
-  __device__ __forceinline__ void load_cached(const T* p) {
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
-  }
-  __device__ __forceinline__ void get(float (&f)[kUnit]) const {
-    constexpr int V = Vec16<T>::kElems;
-#pragma unroll
-    for (int i = 0; i < (int)(sizeof(T) / 2); ++i) Vec16<T>::unpack(v[i], f + i * V);
-  }
-};
-
-template <typename T>
-__device__ __forceinline__ void store8(T* p, const float (&f)[kUnit]) {
-  constexpr int V = Vec16<T>::kElems;
-#pragma unroll
-  for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
-    reinterpret_cast<uint4*>(p)[i] = Vec16<T>::pack(f + i * V);
-}
-
-__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
-  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
-  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
-  return lo | hi << 16;
-}
-
-__device__ __forceinline__ void store_e4m3(uint8_t* p, const float (&f)[kUnit], float k) {
-  uint2 c;
-  c.x = pack_e4m3(f[0] * k, f[1] * k, f[2] * k, f[3] * k);
-  c.y = pack_e4m3(f[4] * k, f[5] * k, f[6] * k, f[7] * k);
-  *reinterpret_cast<uint2*>(p) = c;
-}
-
-// Sum (or maximum) over the TPR threads of a row in the forward kernel; `slot`
-// is a shared buffer of its own for each of the two.
-template <int TPR, bool MAX>
-__device__ __forceinline__ float row_reduce(float v, float (*red)[32], int slot) {
-#pragma unroll
-  for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1) {
-    const float u = __shfl_xor_sync(0xffffffffu, v, o);
-    v = MAX ? fmaxf(v, u) : v + u;
-  }
-  if constexpr (TPR > 32) {
-    const int warp = threadIdx.x >> 5;
-    if ((threadIdx.x & 31) == 0) red[slot][warp] = v;
-    __syncthreads();
-    v = red[slot][0];
-#pragma unroll
-    for (int w = 1; w < TPR / 32; ++w) v = MAX ? fmaxf(v, red[slot][w]) : v + red[slot][w];
-  }
-  return v;
-}
 
 // Forward: TPR threads a row (lanes of a warp, or a CTA), UPT units a thread,
 // TPR * UPT * 8 >= D, one row (of a warp: 32 / TPR rows) a thread and CTA. The
@@ -216,12 +130,6 @@ add_rmsnorm_kernel(const T* x, const T* res, const T* __restrict__ w, T* h, T* y
 constexpr int kNormThreads = 512;
 constexpr int kNormRing = 200 * 1024;  // bytes of a CTA's copies in flight, at most
 
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copies_commit() {
-  asm volatile("cp.async.commit_group;" ::: "memory");
-}
 // One group of copies a row: all but the newest `stages` - 1 have landed.
 constexpr int kNormStages = 6;
 __device__ __forceinline__ void copies_wait(int stages) {
