@@ -12,11 +12,14 @@ _LAZY = {
     "lrm": ("lrm", None),
     "pipeline": ("pipeline", None),
     "RecalibratedExpertBackward": ("pipeline", "RecalibratedExpertBackward"),
+    "PackedState": ("pipeline", "PackedState"),
     "dtype_code": ("pipeline", "dtype_code"),
     "layer": ("layer", None),
     "Router": ("layer", "Router"),
     "AddRMSNorm": ("layer", "AddRMSNorm"),
     "AdamW": ("layer", "AdamW"),
+    "GroupRouter": ("layer", "GroupRouter"),
+    "BlockNorm": ("layer", "BlockNorm"),
 }
 
 

@@ -136,3 +136,23 @@ extern "C" lrm_status lrm_expert_bwd_gathered(
     return launch_dx_gather(s, dx_c, inv, row_of_pos, dx, error_word(ws), (cudaStream_t)stream);
   return LRM_OK;
 }
+
+extern "C" lrm_status lrm_expert_bwd_compacted(
+    const lrm_shape* s, const int32_t* sel_off, const int32_t* tok_c, const void* w_gate,
+    const void* w_up, const void* w_down, const void* dy_c, const void* x, const void* ab_c,
+    const void* phi_c, const int32_t* inv, const int32_t* row_of_pos, void* dab_c, float* dx_c,
+    float* dw_gate, float* dw_up, float* dw_down, float* dx, void* ws, size_t ws_bytes,
+    void* stream) {
+  LRM_NVTX("lrm_expert_bwd_compacted");
+  lrm_status st = check_common(s, ws, ws_bytes, sel_off);
+  if (st != LRM_OK) return st;
+  if (s->K > 32) return LRM_ERR_UNSUPPORTED;
+  if ((st = check_ptrs(s, {w_gate, w_up, w_down, dw_gate, dw_up, dw_down},
+                       {tok_c, dy_c, x, ab_c, phi_c, inv, row_of_pos, dab_c, dx_c, dx})) != LRM_OK)
+    return st;
+  BwdArgs a{s, sel_off, w_gate, w_up, w_down, dy_c, x, ab_c, phi_c, dab_c,
+            dx_c, dw_gate, dw_up, dw_down, error_word(ws), (cudaStream_t)stream};
+  a.tok_c = tok_c;
+  if ((st = run_parts(a, kPartAll)) != LRM_OK) return st;
+  return launch_dx_gather(s, dx_c, inv, row_of_pos, dx, error_word(ws), (cudaStream_t)stream);
+}

@@ -1627,6 +1627,7 @@ lrm_status launch_bwd_tc(const BwdArgs& a, unsigned parts) {
   lrm_status st = LRM_OK;
   const bool gathered = a.sel_pos != nullptr;
   if (gathered && !a.tok_c) return LRM_ERR_INVALID_ARG;
+  const bool x_in_place = a.tok_c != nullptr;  // also beside compacted [a | b] and phi
   const uint64_t tok_rows = std::max<uint64_t>(s->T, 1);
   // upper bounds of the tile counts (the exact ones depend on device-side sizes)
   auto dg_tiles = [&](int tm, int ncols) {
@@ -1684,7 +1685,7 @@ lrm_status launch_bwd_tc(const BwdArgs& a, unsigned parts) {
     Maps m, mp;  // single CTAs (B: 256 columns) and CTA pairs (B: 128 per CTA)
     if (!make_map(&m.o1, a.dw_gate, true, 3, E, D, H, 32, 32) ||
         !make_map(&m.o2, a.dw_up, true, 3, E, D, H, 32, 32) ||
-        !make_chunked_map(&m.a, a.x_c, gathered ? tok_rows : rows, D, BM / 64) ||
+        !make_chunked_map(&m.a, a.x_c, x_in_place ? tok_rows : rows, D, BM / 64) ||
         !make_chunked_map(&m.b, a.dab_c, rows, 2 * H, BN / 64) ||
         !make_chunked_map(&mp.b, a.dab_c, rows, 2 * H, BN / 128))
       return LRM_ERR_CUDA;
@@ -1695,7 +1696,7 @@ lrm_status launch_bwd_tc(const BwdArgs& a, unsigned parts) {
     mp.o2 = m.o2;
     p.out0 = a.dw_gate;
     p.out1 = a.dw_up;
-    p.a_rows = gathered ? a.tok_c : nullptr;
+    p.a_rows = x_in_place ? a.tok_c : nullptr;
     p.a_src = reinterpret_cast<const __nv_bfloat16*>(a.x_c);
     p.a_src_rows = s->T;
     p.a_src_cols = D;

@@ -1,0 +1,734 @@
+// Router over groups of experts: sigmoid or softmax scores, a bias that only the
+// choices see, the best groups of a token, its top-K in them, and the gradient.
+//   s = sigmoid(x) or softmax(x),  key = s + bias (without one: x)
+//   a group's score: the sum of its group_top largest s + bias; top_groups are kept
+//   I = the K largest keys in them, ties to the lower expert id
+//   alpha = scale s at I (renorm: over its sum),  share = s / sum_e s
+//   balance = c_b E / (n^2 K) sum_e counts_e sum_t share_te
+//   d alpha -> ds,  dx = ds s (1 - s)  or  s (ds - sum s ds)
+//
+// Choices are whole numbers: two keys nearer than 32-bit arithmetic can tell may stand
+// in the other order. Every key's error has a bound, so the kernel knows which tokens
+// it cannot decide, and does those again in 64 bits. Keys of equal logits and equal
+// biases are equal in any arithmetic and go by their ids.
+#include <algorithm>
+
+#include "router.cuh"
+
+namespace lrm {
+
+constexpr int kMaxGroups = 32;
+
+// A lane holds NI consecutive experts, so that groups are runs of lanes. -inf past E.
+template <typename T, int NI>
+__device__ __forceinline__ void load_run(const T* row, int e0, int E, bool vec, float (&x)[NI]) {
+  constexpr int kVec = NI * (int)sizeof(T) < 16 ? NI : 16 / (int)sizeof(T);
+#pragma unroll
+  for (int c = 0; c < NI; c += kVec) {
+    alignas(16) T v[kVec];
+    if (vec && e0 + c + kVec <= E) {
+      copy_bytes<kVec * (int)sizeof(T)>(v, row + e0 + c);
+#pragma unroll
+      for (int i = 0; i < kVec; ++i) x[c + i] = (float)v[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < kVec; ++i)
+        x[c + i] = e0 + c + i < E ? (float)row[e0 + c + i] : -CUDART_INF_F;
+    }
+  }
+}
+
+__device__ __forceinline__ uint64_t order_key(double x) {
+  const uint64_t u = (uint64_t)__double_as_longlong(fmax(x, -CUDART_INF) + 0.0);
+  return u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+
+__device__ __forceinline__ float rcp_fast(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Keeps the larger two of (a, b) and (c, d), a >= b, c >= d.
+template <typename F>
+__device__ __forceinline__ void merge_two(F& a, F& b, F c, F d) {
+  const F lo = a < c ? a : c;
+  b = b < d ? d : b;
+  b = b < lo ? lo : b;
+  a = a < c ? c : a;
+}
+
+// The groups that a token keeps, of its warp: bit g of the result. v: s + bias, -inf
+// where closed or past E. gap: how far the kept groups' scores stand above the others'.
+template <typename F, int NI>
+__device__ __forceinline__ uint32_t keep_groups(const F (&v)[NI], int lane, int size, int groups,
+                                                int top_groups, int group_top, F& gap) {
+  const F kLow = -(F)CUDART_INF;
+  F mine = kLow;
+  const int e0 = lane * NI;
+  for (int g = 0; g < groups; ++g) {
+    F a = kLow, b = kLow;
+    const int lo = g * size - e0, hi = lo + size;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const F f = i >= lo && i < hi ? v[i] : kLow;
+      merge_two(a, b, f, kLow);
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const F c = __shfl_xor_sync(0xffffffffu, a, o), d = __shfl_xor_sync(0xffffffffu, b, o);
+      merge_two(a, b, c, d);
+    }
+    const F sum = group_top == 2 && b > kLow ? a + b : a;
+    if (lane == g) mine = sum;
+  }
+  int before = 0;
+  for (int g = 0; g < groups; ++g) {
+    const F other = __shfl_sync(0xffffffffu, mine, g);
+    before += other > mine || (other == mine && g < lane);
+  }
+  const bool kept = lane < groups && before < top_groups;
+  F least = kept ? mine : (F)CUDART_INF, most = kept || lane >= groups ? kLow : mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const F c = __shfl_xor_sync(0xffffffffu, least, o), d = __shfl_xor_sync(0xffffffffu, most, o);
+    least = c < least ? c : least;
+    most = d > most ? d : most;
+  }
+  gap = most == kLow ? (F)CUDART_INF : least - most;
+  return __ballot_sync(0xffffffffu, kept);
+}
+
+// Takes the places of the groups that are not kept out of the keys.
+template <typename U, int NI>
+__device__ __forceinline__ void drop_groups(U (&key)[NI], int lane, int size, uint32_t kept) {
+  int g = lane * NI / size, at = lane * NI - g * size;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    if (!(g < 32 && (kept >> g & 1))) key[i] = 0;
+    if (++at == size) { at = 0; ++g; }
+  }
+}
+
+__device__ __forceinline__ uint32_t warp_max(uint32_t v) {
+  return __reduce_max_sync(0xffffffffu, v);
+}
+__device__ __forceinline__ uint64_t warp_max(uint64_t v) { return group_max<32>(v); }
+
+// The K largest keys in order, equal ones by the lower id (0: a place that was taken,
+// which the key becomes): lane k gets the k-th's expert and key.
+template <typename U, int NI>
+__device__ __forceinline__ void choose(U (&key)[NI], int lane, int K, int& my_idx, U& my_key) {
+  for (int k = 0; k < K; ++k) {
+    U best = key[0];
+    int at = 0;
+#pragma unroll
+    for (int i = 1; i < NI; ++i)
+      if (key[i] > best) { best = key[i]; at = i; }
+    const U top = warp_max(best);
+    const int who = __ffs(__ballot_sync(0xffffffffu, best == top)) - 1;
+    const int e = __shfl_sync(0xffffffffu, lane * NI + at, who);
+    if (lane == k) { my_idx = e; my_key = top; }
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (lane == who && i == at) key[i] = 0;
+  }
+}
+
+struct RouteArgs {
+  const float* bias;
+  const uint8_t* mask;
+  int32_t* topk_idx;
+  float* alpha;
+  int32_t* counts;
+  float *prob_sum, *loss;
+  float2* part;
+  int64_t stride;
+  int ntok, E, K, vec, softmax, groups, size, top_groups, group_top, renorm;
+  float scale, balance_coef;
+};
+
+// A token's choices with keys and group scores in 64 bits: by the whole warp.
+template <int NI>
+__device__ __noinline__ int choose_exact(const float (&x)[NI], int lane, const RouteArgs& a) {
+  const int e0 = lane * NI;
+  double v[NI];
+  if (a.softmax) {
+    float top = -CUDART_INF_F;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) top = fmaxf(top, x[i]);
+    top = group_fmax<32>(top);
+    double total = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < NI; ++i) {
+      v[i] = x[i] > -CUDART_INF_F ? exp((double)x[i] - (double)top) : 0.0;
+      total += v[i];
+    }
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+#pragma unroll 1
+    for (int i = 0; i < NI; ++i) v[i] /= total;
+  } else {
+#pragma unroll 1
+    for (int i = 0; i < NI; ++i) {
+      // rows of equal logits (a router before its first step) are computed once
+      const bool again = i == 0 || x[i] != x[i > 0 ? i - 1 : 0];
+      if (__any_sync(0xffffffffu, again)) v[i] = 1.0 / (1.0 + exp(-(double)x[i]));
+      else v[i] = v[i > 0 ? i - 1 : 0];
+    }
+  }
+  uint64_t key[NI];
+#pragma unroll 1
+  for (int i = 0; i < NI; ++i) {
+    if (a.bias && e0 + i < a.E) v[i] += (double)a.bias[e0 + i];
+    if (!(x[i] > -CUDART_INF_F)) v[i] = -CUDART_INF;  // closed, NaN, past E
+    key[i] = e0 + i < a.E ? order_key(a.bias ? v[i] : (double)x[i]) : 0;
+  }
+  if (a.groups > 1) {
+    double gap;
+    drop_groups(key, lane, a.size,
+                keep_groups(v, lane, a.size, a.groups, a.top_groups, a.group_top, gap));
+  }
+  int idx = 0;
+  uint64_t last;
+  choose(key, lane, a.K, idx, last);
+  return idx;
+}
+
+template <int NI>
+constexpr int group_route_threads() { return NI <= 4 ? 1024 : NI <= 8 ? 512 : 256; }
+
+// A warp a token.
+template <typename T, int NI, bool STATS>
+__global__ void __launch_bounds__(group_route_threads<NI>(), 1)
+group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
+  pdl_begin();  // predecessor complete before any global access
+  extern __shared__ float sm_p[];  // STATS: sums of the shares [warps][E], then counts [E]
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
+  const int E = a.E, K = a.K, e0 = lane * NI;
+  int32_t* sm_c = reinterpret_cast<int32_t*>(sm_p + nwarp * E);
+  float acc[NI], b[NI];
+  if constexpr (STATS) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) sm_c[e] = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) acc[i] = 0.f;
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) b[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.f;
+  for (int64_t t = (int64_t)blockIdx.x * nwarp + warp; t < a.ntok; t += (int64_t)gridDim.x * nwarp) {
+    const T* row = logits + t * a.stride;
+    float x[NI], s[NI];
+    load_run<T, NI>(row, e0, E, a.vec, x);
+    const bool masked = a.mask && a.mask[t] == 0;
+    float top = -CUDART_INF_F;
+    bool some = false;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      top = fmaxf(top, x[i]);
+      some |= x[i] != -CUDART_INF_F;
+    }
+    top = group_fmax<32>(top);
+    const bool use = __any_sync(0xffffffffu, some) && !masked;
+    // s = f c: softmax f = exp(x - top), c its inverse sum; sigmoid f = exp(-m) s with
+    // m = min(top, 0), so that rows of very low logits keep their shares, and c = exp(m)
+    float total = 0.f, c, ptop;
+    if (a.softmax) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) total += s[i] = top > -CUDART_INF_F ? exp_neg(x[i] - top) : 0.f;
+      total = group_sum<32>(total);
+      c = ptop = __frcp_rn(total == 0.f ? 1.f : total);
+    } else {
+      const float m = top > -CUDART_INF_F ? fminf(top, 0.f) : 0.f;
+      c = exp_neg(m);
+      ptop = 1.f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const float u = exp_neg(-fabsf(x[i]) - m), r = rcp_fast(1.f + u * c);
+        total += s[i] = x[i] >= 0.f ? r : u * r;
+      }
+      total = group_sum<32>(total);
+    }
+    // keys in 32 bits and what they may be off by: |s| error below 5 2^-24 (sigmoid) or
+    // (43 p + 1) 2^-24 (softmax, p at most the row's largest), the sum's own rounding
+    float v[NI];
+    uint32_t key[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const bool open = x[i] > -CUDART_INF_F;
+      v[i] = open ? fmaf(s[i], c, b[i]) : -CUDART_INF_F;
+      key[i] = e0 + i < E ? order_key(a.bias ? v[i] : x[i]) : 0u;
+    }
+    const float unit = a.softmax ? fmaf(96.f, ptop, 4.f) : 12.f;  // of two keys, 2^-24
+    bool sure = true;
+    if (a.groups > 1) {
+      float gap, most = 0.f;
+      const uint32_t kept =
+          keep_groups(v, lane, a.size, a.groups, a.top_groups, a.group_top, gap);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) most = fmaxf(most, x[i] > -CUDART_INF_F ? fabsf(v[i]) : 0.f);
+      most = group_fmax<32>(most);
+      sure = gap > (2.f * unit + 8.f * most) * 5.9604645e-8f;
+      drop_groups(key, lane, a.size, kept);
+    }
+    int idx = 0;
+    uint32_t kk = 0;
+    choose(key, lane, K, idx, kk);
+    const bool choice = lane < K;
+    float xk = choice ? (float)row[idx] : -CUDART_INF_F;
+    if (a.bias) {
+      const float f = key_value(kk), bk = choice ? a.bias[idx] : 0.f;
+      const float first = __shfl_sync(0xffffffffu, f, 0), last = __shfl_sync(0xffffffffu, f, K - 1);
+      const float size = fmaxf(fabsf(first), last > -CUDART_INF_F ? fabsf(last) : 0.f);
+      const float tol = (unit + 4.f * size) * 5.9604645e-8f;
+      const float fn = __shfl_down_sync(0xffffffffu, f, 1), xn = __shfl_down_sync(0xffffffffu, xk, 1),
+                  bn = __shfl_down_sync(0xffffffffu, bk, 1);
+      bool near = lane + 1 < K && f - fn <= tol && !(xk == xn && bk == bn);
+      const float xl = __shfl_sync(0xffffffffu, xk, K - 1), bl = __shfl_sync(0xffffffffu, bk, K - 1);
+      const uint32_t floor_key = last > -CUDART_INF_F ? order_key(last - tol) : 0xffffffffu;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) near |= key[i] >= floor_key && !(x[i] == xl && b[i] == bl);
+      sure = sure && !__any_sync(0xffffffffu, near);
+    }
+    if (!sure) {
+      idx = choose_exact<NI>(x, lane, a);
+      xk = choice ? (float)row[idx] : -CUDART_INF_F;
+    }
+    // weights, with float32's accuracy at any logit
+    float w;
+    if (a.softmax) {
+      const float m = a.renorm ? group_fmax<32>(xk) : top;
+      w = choice && m > -CUDART_INF_F ? expf(xk - m) : 0.f;
+      if (!a.renorm) w *= c;
+      if (total != total) w = total;
+    } else {
+      const float most = group_fmax<32>(xk);
+      const float m = a.renorm && most > -CUDART_INF_F ? fminf(most, 0.f) : 0.f;
+      w = xk >= 0.f ? __frcp_rn(1.f + expf(-xk)) : expf(xk - m) / (1.f + expf(xk));
+      if (!choice) w = 0.f;
+    }
+    if (a.renorm) {
+      const float sum = group_sum<32>(w);
+      w = sum == 0.f ? 0.f : w / sum;
+    }
+    if (choice) {
+      a.topk_idx[t * K + lane] = idx;
+      a.alpha[t * K + lane] = use ? w * a.scale : 0.f;
+    }
+    if constexpr (STATS) {
+      if (use) {
+        const float inv = total == 0.f ? 0.f : __frcp_rn(total);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
+        if (choice) atomicAdd(&sm_c[idx], 1);
+      }
+    }
+  }
+  if constexpr (STATS) {
+    // the CTA's sums, in a fixed order; a single CTA finishes by itself, the sums of
+    // several are added by route_sums_kernel
+    __shared__ float red[2][32];
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      if (e0 + i < E) sm_p[warp * E + e0 + i] = acc[i];
+    __syncthreads();
+    const bool alone = gridDim.x == 1;
+    float dot = 0.f, cnt = 0.f;
+    for (int e = threadIdx.x; e < E; e += blockDim.x) {
+      float sum = 0.f;
+#pragma unroll 8
+      for (int w = 0; w < nwarp; ++w) sum += sm_p[w * E + e];
+      const int n = sm_c[e];
+      if (alone) {
+        a.prob_sum[e] = sum;
+        a.counts[e] = n;
+        dot = fmaf((float)n, sum, dot);
+        cnt += (float)n;
+      } else {
+        a.part[(int64_t)blockIdx.x * E + e] = make_float2(sum, __int_as_float(n));
+      }
+    }
+    if (!alone) return;
+    dot = warp_sum(dot);
+    cnt = warp_sum(cnt);
+    if (lane == 0) { red[0][warp] = dot; red[1][warp] = cnt; }
+    __syncthreads();
+    if (warp == 0) {
+      const float d = warp_sum(lane < nwarp ? red[0][lane] : 0.f);
+      // tokens that took part: every one chose K experts
+      const float n = fmaxf(warp_sum(lane < nwarp ? red[1][lane] : 0.f) / (float)K, 1.f);
+      if (lane == 0) a.loss[0] = a.balance_coef * (float)E * (d / (n * n * (float)K));
+    }
+  }
+}
+
+struct RouteBwdArgs {
+  const uint8_t* mask;
+  const int32_t *topk_idx, *counts;
+  const float *dalpha, *dloss;
+  int64_t stride;
+  int ntok, E, K, vec, out_vec, softmax, renorm;
+  float scale, balance_coef;
+  int32_t* err;
+};
+
+// Gradient: the G lanes of a token write what every expert has (the balance loss), then
+// lane k adds what choice k has on top and writes that element again. kPer: choices a lane.
+constexpr int kGroupBwdThreads = 256;
+template <typename T, int NI, int G, int kPer>
+__global__ void __launch_bounds__(kGroupBwdThreads)
+group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dlogits) {
+  pdl_begin();  // predecessor complete before any global access
+  using S = RowShape<T, NI, G>;
+  constexpr int kTokens = 32 / G, nwarp = kGroupBwdThreads / 32;
+  const int lane = threadIdx.x & 31, gl = lane % G, E = a.E, K = a.K;
+  const int64_t step = (int64_t)gridDim.x * nwarp * kTokens;
+  int64_t first = ((int64_t)blockIdx.x * nwarp + (threadIdx.x >> 5)) * kTokens;
+  // the lane's own choices of token t: read a round ahead, because their logits are
+  // read by them
+  int next[kPer];
+  auto read_choices = [&](int64_t t) {
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int k = j * G + gl;
+      next[j] = t < a.ntok && k < K ? a.topk_idx[t * K + k] : 0;
+    }
+  };
+  read_choices(first + lane / G);
+  float cost[NI];
+  int pairs = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int e = S::expert(i, gl), n = e < E ? a.counts[e] : 0;
+    cost[i] = (float)n;
+    pairs += n;
+  }
+#pragma unroll
+  for (int o = 1; o < G; o <<= 1) pairs += __shfl_xor_sync(0xffffffffu, pairs, o);
+  // tokens that took part: every one chose K experts
+  const float inv_n = 1.f / fmaxf((float)pairs / (float)K, 1.f);
+  const float kb = (a.dloss ? a.dloss[0] : 1.f) * a.balance_coef * (float)E * inv_n *
+                   (inv_n / (float)K);
+#pragma unroll
+  for (int i = 0; i < NI; ++i) cost[i] *= kb;
+  for (; first < a.ntok; first += step) {
+    const bool real = first + lane / G < a.ntok;
+    const int64_t t = real ? first + lane / G : first;
+    const T* row = logits + t * a.stride;
+    float x[NI];
+    load_row<T, NI, G>(row, gl, E, a.vec, x);
+    const bool masked = a.mask && a.mask[t] == 0;
+    int idx[kPer];
+    float da[kPer], xc[kPer];
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const int k = j * G + gl;
+      idx[j] = -1;
+      da[j] = 0.f;
+      xc[j] = -CUDART_INF_F;
+      if (k < K && real) {
+        const int q = next[j];
+        if (q >= 0 && q < E) {
+          idx[j] = q;
+          xc[j] = (float)row[q];
+          if (a.dalpha) da[j] = a.dalpha[t * K + k] * a.scale;
+        } else {
+          flag_error(a.err, LRM_DEVERR_EXPERT_ID);
+        }
+      }
+    }
+    read_choices(first + step + lane / G);
+    float top = -CUDART_INF_F;
+    bool some = false;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      top = fmaxf(top, x[i]);
+      some |= x[i] != -CUDART_INF_F;
+    }
+    top = group_fmax<G>(top);
+    const uint32_t who = __ballot_sync(0xffffffffu, some);
+    const bool use =
+        (G == 32 ? who : who >> (lane & ~(G - 1)) & ((1u << (G & 31)) - 1)) != 0 && !masked;
+    // f: the score over exp(m), less: 1 - s of the sigmoid
+    float less[NI], total = 0.f, cdot = 0.f;
+    const float m = a.softmax ? top : top > -CUDART_INF_F ? fminf(top, 0.f) : 0.f;
+    const float c = exp_grad<T>(a.softmax ? 0.f : m);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const float xi = x[i];
+      if (a.softmax) {
+        x[i] = top > -CUDART_INF_F ? exp_grad<T>(xi - m) : 0.f;
+        less[i] = 1.f;
+      } else {
+        const float u = exp_grad<T>(-fabsf(xi) - m), z = u * c, r = inverse_grad<T>(1.f + z);
+        x[i] = xi >= 0.f ? r : u * r;
+        less[i] = xi >= 0.f ? z * r : r;
+      }
+      total += x[i];
+      cdot = fmaf(x[i], cost[i], cdot);
+    }
+    total = group_sum<G>(total);
+    const float inv = total == 0.f ? 0.f : inverse_grad<T>(total);
+    const float cmean = group_sum<G>(cdot) * inv;
+    // the choices' scores over exp(mc): their ratios are right however low they are
+    float most = -CUDART_INF_F;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) most = fmaxf(most, xc[j]);
+    most = group_fmax<G>(most);
+    float mc = m;  // at most m, so that exp(mc - m) does not overflow
+    if (most > -CUDART_INF_F) mc = a.softmax ? most : fminf(most, 0.f);
+    float sc[kPer], lc[kPer], chosen = 0.f, adot = 0.f;
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      const float xj = xc[j];
+      if (a.softmax) {
+        sc[j] = idx[j] >= 0 && xj > -CUDART_INF_F ? exp_grad<T>(xj - mc) : 0.f;
+        if (xj != xj) sc[j] = xj;
+        lc[j] = 1.f;
+      } else {
+        const float z = exp_grad<T>(-fabsf(xj)), r = inverse_grad<T>(1.f + z);
+        sc[j] = xj >= 0.f ? r : exp_grad<T>(xj - mc) * r;
+        lc[j] = xj >= 0.f ? z * r : r;
+        if (idx[j] < 0) sc[j] = 0.f;
+      }
+      chosen += sc[j];
+      adot = fmaf(sc[j], da[j], adot);
+    }
+    chosen = group_sum<G>(chosen);
+    adot = group_sum<G>(adot);
+    const float back = a.softmax ? exp_grad<T>(mc - m) * inv : exp_grad<T>(mc);  // s = sc back
+    const float inv_c = chosen == 0.f ? 0.f : inverse_grad<T>(chosen);
+    const float mean = a.renorm ? adot * inv_c : a.softmax ? adot * back : 0.f;
+    const float common = -cmean - (a.softmax && !a.renorm ? mean : 0.f);
+    T* out = dlogits + t * E;
+#pragma unroll
+    for (int q = 0; q < NI / S::kVec; ++q) {
+      const int e = S::expert(q * S::kVec, gl);
+      alignas(16) T v[S::kVec];
+#pragma unroll
+      for (int i = 0; i < S::kVec; ++i) {
+        const int s = q * S::kVec + i;
+        v[i] = (T)(use ? x[s] * inv * (cost[s] + common) * less[s] : 0.f);
+      }
+      if (real) {
+        if (a.out_vec && e + S::kVec <= E) {
+          copy_bytes<S::kVec * (int)sizeof(T)>(out + e, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < S::kVec; ++i)
+            if (e + i < E) out[e + i] = v[i];
+        }
+      }
+    }
+    __syncwarp();  // the choices' elements are written after the row's
+#pragma unroll
+    for (int j = 0; j < kPer; ++j) {
+      if (idx[j] >= 0 && use && real) {
+        // share of the whole row: sc exp(mc - m) / total
+        const float share = sc[j] * exp_grad<T>(mc - m) * inv;
+        const float base = share * (kb * (float)a.counts[idx[j]] + common);
+        const float own = a.renorm ? sc[j] * inv_c * (da[j] - mean) : sc[j] * back * da[j];
+        out[idx[j]] = (T)((base + own) * lc[j]);
+      }
+    }
+  }
+}
+
+__global__ void bias_step_kernel(const int32_t* __restrict__ counts, const float* bias, float* out,
+                                 int E, float rate) {
+  pdl_begin();  // predecessor complete before any global access
+  __shared__ long long red[32];
+  long long sum = 0;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) sum += counts[e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
+  __syncthreads();
+  sum = 0;
+  for (int w = 0; w < (int)blockDim.x / 32; ++w) sum += red[w];
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    const long long lack = sum - (long long)E * counts[e];
+    out[e] = bias[e] + (lack > 0 ? rate : lack < 0 ? -rate : 0.f);
+  }
+}
+
+static lrm_status check_group_router(const lrm_group_router* r) {
+  if (!r) return LRM_ERR_INVALID_ARG;
+  if (r->T < 0 || r->E <= 0 || r->K <= 0 || r->groups <= 0 || r->top_groups <= 0 ||
+      r->group_top <= 0)
+    return LRM_ERR_INVALID_ARG;
+  if (r->dtype != LRM_F32 && r->dtype != LRM_BF16) return LRM_ERR_INVALID_ARG;
+  if (r->score_fn != LRM_SIGMOID && r->score_fn != LRM_SOFTMAX) return LRM_ERR_INVALID_ARG;
+  if (r->stride < r->E) return LRM_ERR_INVALID_ARG;
+  if (r->E > kRouterMaxE || r->K > kRouterMaxK || r->groups > kMaxGroups || r->group_top > 2)
+    return LRM_ERR_UNSUPPORTED;
+  if (r->E % r->groups != 0 || r->top_groups > r->groups ||
+      r->K > r->top_groups * (r->E / r->groups))
+    return LRM_ERR_UNSUPPORTED;
+  if ((int64_t)r->T * r->K >= (int64_t)1 << 31) return LRM_ERR_UNSUPPORTED;
+  return LRM_OK;
+}
+
+static size_t group_router_bytes(const lrm_group_router* r) {
+  // header, then sums of the shares and counts of every CTA
+  return kWsHeaderBytes + ((size_t)kRouterMaxCtas * 8 * r->E + 255) / 256 * 256;
+}
+
+static lrm_status check_group_ws(const lrm_group_router* r, const void* ws, size_t ws_bytes) {
+  if (!ws) return LRM_ERR_WORKSPACE;
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) return LRM_ERR_UNSUPPORTED;
+  return ws_bytes < group_router_bytes(r) ? LRM_ERR_WORKSPACE : LRM_OK;
+}
+
+template <typename T, int NI>
+static lrm_status launch_group_route(const void* logits, RouteArgs a, cudaStream_t cs) {
+  const bool stats = a.counts != nullptr;
+  constexpr int kMaxWarps = group_route_threads<NI>() / 32;
+  constexpr int kVec = NI * (int)sizeof(T) < 16 ? NI : 16 / (int)sizeof(T);
+  a.vec = a.stride % kVec == 0;
+  const int64_t warps = std::max(1, a.ntok);
+  int nwarp;
+  int64_t grid;
+  if (stats) {
+    // one CTA an SM at most (each leaves a row for the last sums), its warps in even
+    // rounds; tokens that fit one CTA stay in one, without that second launch
+    const int64_t ctas = std::min(num_sms(), kRouterMaxCtas);
+    const int64_t rounds = (warps + ctas * kMaxWarps - 1) / (ctas * kMaxWarps);
+    const int64_t need = (warps + rounds - 1) / rounds;
+    nwarp = (int)(need <= kMaxWarps
+                      ? need
+                      : std::max<int64_t>(std::min(16, kMaxWarps), (need + ctas - 1) / ctas));
+    grid = (need + nwarp - 1) / nwarp;
+  } else {
+    nwarp = (int)std::min<int64_t>(4, warps);  // a warp for each scheduler of an SM
+    grid = std::min<int64_t>((warps + nwarp - 1) / nwarp, 1 << 30);
+  }
+  auto kern = stats ? group_route_kernel<T, NI, true> : group_route_kernel<T, NI, false>;
+  const size_t smem = stats ? ((size_t)nwarp + 1) * a.E * 4 : 0;
+  // the limit is the kernel's, for all host threads: only ever set to the most any call needs
+  constexpr int kMostSmem = (kMaxWarps + 1) * NI * 32 * 4;
+  if (smem > 40 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) !=
+          cudaSuccess) {
+    (void)cudaGetLastError();
+    return LRM_ERR_CUDA;
+  }
+  if (launch_k(kern, dim3((unsigned)grid), dim3(nwarp * 32), smem, cs, (const T*)logits, a) !=
+      cudaSuccess) {
+    (void)cudaGetLastError();
+    return LRM_ERR_CUDA;
+  }
+  if (stats && grid > 1)
+    launch_k(route_sums_kernel, dim3(kSumCtas), dim3(kSumThreads), 0, cs, (const float2*)a.part,
+             (const float*)nullptr, (int)grid, a.E, a.K, a.balance_coef, 0.f, a.counts,
+             a.prob_sum, a.loss);
+  return launch_status();
+}
+
+template <typename T>
+static lrm_status pick_group_route(const void* logits, const RouteArgs& a, cudaStream_t cs) {
+  if (a.E <= 32) return launch_group_route<T, 1>(logits, a, cs);
+  if (a.E <= 64) return launch_group_route<T, 2>(logits, a, cs);
+  if (a.E <= 128) return launch_group_route<T, 4>(logits, a, cs);
+  if (a.E <= 256) return launch_group_route<T, 8>(logits, a, cs);
+  if (a.E <= 512) return launch_group_route<T, 16>(logits, a, cs);
+  return launch_group_route<T, 32>(logits, a, cs);
+}
+
+template <typename T, int NI, int G, int kPer>
+static lrm_status launch_group_bwd(const void* logits, RouteBwdArgs a, void* dlogits,
+                                   cudaStream_t cs) {
+  constexpr int kTokens = 32 / G * (kGroupBwdThreads / 32);  // tokens a CTA and round
+  const int64_t blocks =
+      std::min<int64_t>(((int64_t)a.ntok + kTokens - 1) / kTokens, (int64_t)num_sms() * 8);
+  a.vec = a.stride % RowShape<T, NI, G>::kVec == 0;
+  a.out_vec = a.E % RowShape<T, NI, G>::kVec == 0;
+  launch_k(group_route_bwd_kernel<T, NI, G, kPer>, dim3((unsigned)blocks), dim3(kGroupBwdThreads),
+           0, cs, (const T*)logits, a, (T*)dlogits);
+  return launch_status();
+}
+
+template <typename T, int NI, int G>
+static lrm_status pick_group_choices(const void* logits, const RouteBwdArgs& a, void* dlogits,
+                                     cudaStream_t cs) {
+  if (a.K <= G) return launch_group_bwd<T, NI, G, 1>(logits, a, dlogits, cs);
+  return launch_group_bwd<T, NI, G, kRouterMaxK / G>(logits, a, dlogits, cs);
+}
+
+template <typename T>
+static lrm_status pick_group_bwd(const void* logits, const RouteBwdArgs& a, void* dlogits,
+                                 cudaStream_t cs) {
+  if (a.E <= 32) return pick_group_choices<T, 4, 8>(logits, a, dlogits, cs);
+  if (a.E <= 64) return pick_group_choices<T, 8, 8>(logits, a, dlogits, cs);
+  if (a.E <= 128) return pick_group_choices<T, 16, 8>(logits, a, dlogits, cs);
+  if (a.E <= 256) return pick_group_choices<T, 16, 16>(logits, a, dlogits, cs);
+  if (a.E <= 512) return pick_group_choices<T, 16, 32>(logits, a, dlogits, cs);
+  return pick_group_choices<T, 32, 32>(logits, a, dlogits, cs);
+}
+
+}  // namespace lrm
+
+using namespace lrm;
+
+extern "C" size_t lrm_group_router_workspace_bytes(const lrm_group_router* r) {
+  return check_group_router(r) == LRM_OK ? group_router_bytes(r) : 0;
+}
+
+extern "C" lrm_status lrm_group_route(const lrm_group_router* r, const void* logits,
+                                      const float* bias, const uint8_t* mask, int32_t* topk_idx,
+                                      float* alpha, int32_t* counts, float* prob_sum, float* loss,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  LRM_NVTX("lrm_group_route");
+  lrm_status st = check_group_router(r);
+  if (st != LRM_OK) return st;
+  if ((st = check_group_ws(r, ws, ws_bytes)) != LRM_OK) return st;
+  const int given = !!counts + !!prob_sum + !!loss;
+  if (given != 0 && given != 3) return LRM_ERR_INVALID_ARG;
+  if (r->T > 0 && (!logits || !topk_idx || !alpha)) return LRM_ERR_INVALID_ARG;
+  if ((st = check_aligned({logits, topk_idx, alpha, counts, prob_sum})) != LRM_OK) return st;
+  if (((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(loss)) & 3) != 0)
+    return LRM_ERR_UNSUPPORTED;
+  if (r->T == 0 && !counts) return LRM_OK;
+  RouteArgs a{bias, mask, topk_idx, alpha, counts, prob_sum, loss,
+              reinterpret_cast<float2*>((char*)ws + kWsHeaderBytes), r->stride, r->T, r->E, r->K,
+              0, r->score_fn == LRM_SOFTMAX, r->top_groups == r->groups ? 1 : r->groups,
+              r->E / r->groups, r->top_groups, r->group_top, r->renorm, r->scale,
+              r->balance_coef};
+  cudaStream_t cs = (cudaStream_t)stream;
+  return r->dtype == LRM_BF16 ? pick_group_route<__nv_bfloat16>(logits, a, cs)
+                              : pick_group_route<float>(logits, a, cs);
+}
+
+extern "C" lrm_status lrm_group_route_bwd(const lrm_group_router* r, const void* logits,
+                                          const uint8_t* mask, const int32_t* topk_idx,
+                                          const int32_t* counts, const float* dalpha,
+                                          const float* dloss, void* dlogits, void* ws,
+                                          size_t ws_bytes, void* stream) {
+  LRM_NVTX("lrm_group_route_bwd");
+  lrm_status st = check_group_router(r);
+  if (st != LRM_OK) return st;
+  if ((st = check_group_ws(r, ws, ws_bytes)) != LRM_OK) return st;
+  if (r->T == 0) return LRM_OK;
+  if (!logits || !topk_idx || !counts || !dlogits) return LRM_ERR_INVALID_ARG;
+  if ((st = check_aligned({logits, topk_idx, counts, dalpha, dlogits})) != LRM_OK) return st;
+  if ((reinterpret_cast<uintptr_t>(dloss) & 3) != 0) return LRM_ERR_UNSUPPORTED;
+  const RouteBwdArgs a{mask, topk_idx, counts, dalpha, dloss, r->stride, r->T, r->E, r->K, 0, 0,
+                       r->score_fn == LRM_SOFTMAX, r->renorm, r->scale, r->balance_coef,
+                       error_word(ws)};
+  cudaStream_t cs = (cudaStream_t)stream;
+  return r->dtype == LRM_BF16 ? pick_group_bwd<__nv_bfloat16>(logits, a, dlogits, cs)
+                              : pick_group_bwd<float>(logits, a, dlogits, cs);
+}
+
+extern "C" lrm_status lrm_bias_step(const lrm_bias* b, const int32_t* counts, const float* bias,
+                                    float* out, void* stream) {
+  LRM_NVTX("lrm_bias_step");
+  if (!b || !counts || !bias || !out || b->E <= 0) return LRM_ERR_INVALID_ARG;
+  if (b->E > kRouterMaxE) return LRM_ERR_UNSUPPORTED;
+  if (((reinterpret_cast<uintptr_t>(counts) | reinterpret_cast<uintptr_t>(bias) |
+        reinterpret_cast<uintptr_t>(out)) & 3) != 0)
+    return LRM_ERR_UNSUPPORTED;
+  launch_k(bias_step_kernel, dim3(1), dim3((b->E + 31) / 32 * 32), 0, (cudaStream_t)stream, counts,
+           bias, out, b->E, b->rate);
+  return launch_status();
+}

@@ -18,7 +18,8 @@ struct BwdArgs {
   cudaStream_t stream;
   // Gathered operands: when set, ab_c / phi_c hold the uncompacted saved
   // state [N rows, dispatch order] read at row sel_pos[j], and x_c the token
-  // rows [T rows] read at row tok_c[j], for compacted row j.
+  // rows [T rows] read at row tok_c[j], for compacted row j. tok_c alone: only
+  // x is read in place.
   const int32_t* sel_pos = nullptr;
   const int32_t* tok_c = nullptr;
 };

@@ -1,0 +1,385 @@
+// The saved state [a | b] of the experts in 8 bits, and its use in the backward pass.
+//   pack:    s = max(amax, 2^-100) / 448 over each `cols` columns of a and of b,
+//            q = e4m3(v / s), phi_sq = sum (SiLU(a) b)^2 of the unquantised values
+//   score:   R_u = alpha_u^2 ||g_t||^2 phi_sq_u
+//   compact: dy = alpha g, (a, b) = q s, phi = SiLU(a) b for the retained rows, in
+//            their expert-major order
+#include <algorithm>
+
+#include "rows.cuh"
+
+namespace lrm {
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// a sigmoid(a) = a / (1 + 2^(-a log2 e)) on the hardware's power of two and reciprocal:
+// the product's rounding puts it off by up to 9e-8 |a| of itself for a below 0, where
+// SiLU falls as |a| e^a, and by 3e-7 elsewhere. -inf gives NaN, as the formula does.
+__device__ __forceinline__ float silu(float a) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-a * kLog2e));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return a * r;
+}
+
+// What a group's values are divided by: 448 v / amax, corrected by its own remainder
+// so that quotients which lie between two codes (bfloat16 values often do) round as
+// the exact ones. Both sides of the remainder are scaled by 2^-9, so that neither
+// overflows.
+struct Divisor {
+  float k, a, r;  // 448 / amax, amax / 512, 512 / amax
+  __device__ __forceinline__ explicit Divisor(float amax) {
+    const float inv = __frcp_rn(amax);
+    k = inv * kF8Max;
+    a = amax * 0.001953125f;
+    r = inv * 512.f;
+  }
+  __device__ __forceinline__ float of(float v) const {
+    const float t = v * k;
+    return fmaf(fmaf(-t, a, v * 0.875f), r, t);
+  }
+};
+
+__device__ __forceinline__ uint2 codes8(const float (&f)[kUnit], float amax) {
+  const Divisor d(amax);
+  float t[kUnit];
+#pragma unroll
+  for (int j = 0; j < kUnit; ++j) t[j] = d.of(f[j]);
+  return make_uint2(pack_e4m3(t[0], t[1], t[2], t[3]), pack_e4m3(t[4], t[5], t[6], t[7]));
+}
+
+__device__ __forceinline__ float amax8(const float (&f)[kUnit]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < kUnit; ++j) m = fmaxf(m, fabsf(f[j]));
+  return m;
+}
+
+// A warp a row; lane l holds the 8 columns l, l + 32, .. of both halves, so that a
+// scale's group is 2^shift neighbouring lanes. NI of them are loaded before any is used.
+constexpr int kPackThreads = 128;
+
+template <typename T, int NI>
+__global__ void __launch_bounds__(kPackThreads)
+pack_kernel(const T* __restrict__ ab, int64_t rows, int H, int shift, uint8_t* __restrict__ q,
+            float* __restrict__ scale, float* __restrict__ phi_sq) {
+  pdl_begin();  // predecessor complete before any global access
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (int64_t)blockIdx.x * (kPackThreads / 32) + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  const int units = H / kUnit, groups = ((units - 1) >> shift) + 1;
+  const T* row = ab + r * 2 * H;
+  uint8_t* out = q + r * 2 * H;
+  float* sc = scale + r * 2 * groups;
+  float sq = 0.f;
+  for (int u0 = lane; u0 - lane < units; u0 += 32 * NI) {
+    Unit8<T> va[NI], vb[NI];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int u = u0 + 32 * i;
+      va[i].load(row + u * kUnit, u < units);
+      vb[i].load(row + H + u * kUnit, u < units);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int u = u0 + 32 * i;
+      if (u - lane >= units) break;
+      float a[kUnit], b[kUnit];
+      va[i].get(a);
+      vb[i].get(b);
+      float ma = amax8(a), mb = amax8(b);
+      for (int o = 0; o < shift; ++o) {
+        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1 << o));
+        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1 << o));
+      }
+      ma = fmaxf(ma, kAmaxMin);
+      mb = fmaxf(mb, kAmaxMin);
+#pragma unroll
+      for (int j = 0; j < kUnit; ++j) {
+        const float p = silu(a[j]) * b[j];
+        sq = fmaf(p, p, sq);
+      }
+      if (u < units) {
+        *reinterpret_cast<uint2*>(out + u * kUnit) = codes8(a, ma);
+        *reinterpret_cast<uint2*>(out + H + u * kUnit) = codes8(b, mb);
+        if ((u & ((1 << shift) - 1)) == 0) {
+          sc[u >> shift] = ma * kF8MaxInv;
+          sc[groups + (u >> shift)] = mb * kF8MaxInv;
+        }
+      }
+    }
+  }
+  sq = warp_sum(sq);
+  if (lane == 0) phi_sq[r] = sq;
+}
+
+// A warp a token: lane k holds slot k's position, ||g_t||^2 is the warp's sum.
+constexpr int kScoreWarps = 4;
+
+template <typename T>
+__global__ void __launch_bounds__(32 * kScoreWarps)
+score_packed_kernel(const T* __restrict__ g, const float* __restrict__ phi_sq,
+                    const float* __restrict__ alpha, const int32_t* __restrict__ inv,
+                    float* __restrict__ score, int ntok, int D, int K, int32_t* err) {
+  pdl_begin();  // predecessor complete before any global access
+  constexpr int V = Vec16<T>::kElems, kAhead = 8;
+  const int lane = threadIdx.x & 31;
+  const int64_t t = (int64_t)blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
+  if (t >= ntok) return;
+  const int64_t N = (int64_t)ntok * K;
+  const int chunks = D / V;
+  const T* row = g + t * D;
+  float s = 0.f;
+  for (int c0 = lane; c0 - lane < chunks; c0 += 32 * kAhead) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) v[i] = load_if(row + (c0 + 32 * i) * V, c0 + 32 * i < chunks);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      float f[V];
+      Vec16<T>::unpack(v[i], f);
+#pragma unroll
+      for (int j = 0; j < V; ++j) s = fmaf(f[j], f[j], s);
+    }
+  }
+  s = warp_sum(s);
+  for (int k = lane; k < K; k += 32) {
+    const int pos = inv[t * K + k];
+    if (pos >= 0 && pos < N) {
+      const float a = alpha[t * K + k];
+      score[pos] = (a * a) * s * phi_sq[pos];
+    } else {
+      flag_error(err, LRM_DEVERR_INDEX);
+    }
+  }
+}
+
+// 8 values of e4m3 codes (a byte each) times their scale.
+__device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[kUnit]) {
+  const uint32_t w[2] = {c.x, c.y};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2(
+        (__nv_fp8x2_storage_t)(w[i / 2] >> (i % 2 * 16) & 0xffffu), __NV_E4M3);
+    const float2 v = __half22float2(__half2(h));
+    f[2 * i] = v.x * scale;
+    f[2 * i + 1] = v.y * scale;
+  }
+}
+
+// A warp a retained row, as the compaction of a 16-bit state; the row count
+// M = sel_off[E] is read on the device.
+constexpr int kUnpackThreads = 256;
+
+template <typename T>
+__global__ void __launch_bounds__(kUnpackThreads)
+compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale, int shift,
+                      const int32_t* __restrict__ perm, const uint8_t* __restrict__ keep,
+                      const int32_t* __restrict__ sel_off, const int32_t* __restrict__ sel_pos,
+                      const float* __restrict__ alpha, const void* __restrict__ x,
+                      const float* __restrict__ x_scale, int x_cols, const T* __restrict__ g,
+                      T* __restrict__ dy_c, T* __restrict__ x_c, T* __restrict__ ab_c,
+                      T* __restrict__ phi_c, int32_t* __restrict__ tok_c,
+                      int32_t* __restrict__ row_of_pos, int ntok, int D, int H, int K, int E,
+                      int32_t* err) {
+  pdl_begin();  // predecessor complete before any global access
+  constexpr int V = Vec16<T>::kElems;
+  const int64_t N = (int64_t)ntok * K;
+  const int64_t gtid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t nthr = (int64_t)gridDim.x * blockDim.x;
+  for (int64_t i = gtid; i < N; i += nthr)
+    if (!keep[i]) row_of_pos[i] = -1;
+
+  const int lane = threadIdx.x & 31;
+  int64_t M = sel_off[E];
+  if (M < 0 || M > N) {  // not of a selection: no row past the buffers is addressed
+    if (gtid == 0) flag_error(err, LRM_DEVERR_INDEX);
+    M = M < 0 ? 0 : N;
+  }
+  const int dv = D / V, units = H / kUnit, groups = ((units - 1) >> shift) + 1;
+  {  // the zero rows behind dy_c that the FC2 weight-gradient product reads
+    const int64_t zrows = M < N ? min((int64_t)64, N - M) : 0;
+    uint4* z = reinterpret_cast<uint4*>(dy_c + M * D);
+    for (int64_t i = gtid; i < zrows * dv; i += nthr) z[i] = make_uint4(0, 0, 0, 0);
+  }
+  const int x_groups = x_cols ? (D + x_cols - 1) / x_cols : 1;
+  for (int64_t j = gtid >> 5; j < M; j += nthr >> 5) {
+    const int i = sel_pos[j];
+    const int p = (i >= 0 && i < N) ? perm[i] : -1;
+    if (p < 0 || p >= N) {
+      if (lane == 0) flag_error(err, LRM_DEVERR_INDEX);
+      continue;
+    }
+    const int64_t t = p / K;
+    const float al = alpha[p];
+    const uint8_t* qr = q + (int64_t)i * 2 * H;
+    const float* sr = scale + (int64_t)i * 2 * groups;
+    const uint4* gs = reinterpret_cast<const uint4*>(g + t * D);
+    uint4* dyd = reinterpret_cast<uint4*>(dy_c + j * D);
+    for (int c0 = lane; c0 < dv; c0 += 32 * 8) {
+      uint4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        if (c0 + 32 * u < dv) v[u] = gs[c0 + 32 * u];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        if (c0 + 32 * u < dv) {
+          float f[V];
+          Vec16<T>::unpack(v[u], f);
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[e] *= al;
+          dyd[c0 + 32 * u] = Vec16<T>::pack(f);
+        }
+      }
+    }
+    if (x_c) {
+      if (x_scale) {
+        const uint8_t* xr = (const uint8_t*)x + t * D;
+        const float* xs = x_scale + t * x_groups;
+        for (int u = lane; u < D / kUnit; u += 32) {
+          float f[kUnit];
+          decode8(*reinterpret_cast<const uint2*>(xr + u * kUnit),
+                  xs[x_cols ? u * kUnit / x_cols : 0], f);
+          store8(x_c + j * D + u * kUnit, f);
+        }
+      } else {
+        const uint4* xr = reinterpret_cast<const uint4*>((const T*)x + t * D);
+        uint4* xd = reinterpret_cast<uint4*>(x_c + j * D);
+        for (int c = lane; c < dv; c += 32) xd[c] = xr[c];
+      }
+    }
+    T* abd = ab_c + j * 2 * H;
+    T* pd = phi_c + j * H;
+#pragma unroll 2
+    for (int u = lane; u < units; u += 32) {
+      const uint2 ca = *reinterpret_cast<const uint2*>(qr + u * kUnit);
+      const uint2 cb = *reinterpret_cast<const uint2*>(qr + H + u * kUnit);
+      float a[kUnit], b[kUnit], ph[kUnit];
+      decode8(ca, sr[u >> shift], a);
+      decode8(cb, sr[groups + (u >> shift)], b);
+#pragma unroll
+      for (int e = 0; e < kUnit; ++e) ph[e] = silu(a[e]) * b[e];
+      store8(abd + u * kUnit, a);
+      store8(abd + H + u * kUnit, b);
+      store8(pd + u * kUnit, ph);
+    }
+    if (lane == 0) {
+      tok_c[j] = (int32_t)t;
+      row_of_pos[i] = (int32_t)j;
+    }
+  }
+}
+
+static lrm_status check_packed(const lrm_packed* p) {
+  if (!p) return LRM_ERR_INVALID_ARG;
+  if (p->rows < 0 || p->H <= 0) return LRM_ERR_INVALID_ARG;
+  if (p->dtype != LRM_F32 && p->dtype != LRM_BF16) return LRM_ERR_INVALID_ARG;
+  if (p->H % 8 != 0 || p->rows >= (int64_t)1 << 31) return LRM_ERR_UNSUPPORTED;
+  if (p->cols != 32 && p->cols != 64 && p->cols != 128) return LRM_ERR_UNSUPPORTED;
+  if (p->rows > 0 && (!p->q || !p->scale || !p->phi_sq)) return LRM_ERR_INVALID_ARG;
+  for (const void* b : {(const void*)p->q, (const void*)p->scale, (const void*)p->phi_sq})
+    if (!aligned16(b)) return LRM_ERR_UNSUPPORTED;
+  return LRM_OK;
+}
+
+static int group_shift(int cols) { return cols == 32 ? 2 : cols == 64 ? 3 : 4; }
+
+// The state is the layer's: as many pairs, the same width and type.
+static lrm_status check_layer(const lrm_shape* s, const lrm_packed* p, const void* ws,
+                              size_t ws_bytes) {
+  lrm_status st = check_shape(s);
+  if (st != LRM_OK) return st;
+  if ((st = check_packed(p)) != LRM_OK) return st;
+  if (p->rows != (int64_t)s->T * s->K || p->H != s->H || p->dtype != s->dtype)
+    return LRM_ERR_INVALID_ARG;
+  return check_ws(s, ws, ws_bytes);
+}
+
+template <typename T>
+static lrm_status launch_pack(const lrm_packed* p, const void* ab, cudaStream_t cs) {
+  const int64_t grid = (p->rows + kPackThreads / 32 - 1) / (kPackThreads / 32);
+  const int per_lane = (p->H / kUnit + 31) / 32;
+  auto kern = per_lane <= 1   ? pack_kernel<T, 1>
+              : per_lane <= 2 ? pack_kernel<T, 2>
+              : per_lane <= 3 ? pack_kernel<T, 3>
+                              : pack_kernel<T, 4>;
+  launch_k(kern, dim3((unsigned)grid), dim3(kPackThreads), 0, cs, (const T*)ab, p->rows, p->H,
+           group_shift(p->cols), p->q, p->scale, p->phi_sq);
+  return launch_status();
+}
+
+}  // namespace lrm
+
+using namespace lrm;
+
+extern "C" lrm_status lrm_pack_state(const lrm_packed* p, const void* ab, void* stream) {
+  LRM_NVTX("lrm_pack_state");
+  lrm_status st = check_packed(p);
+  if (st != LRM_OK) return st;
+  if (p->rows == 0) return LRM_OK;
+  if (!ab) return LRM_ERR_INVALID_ARG;
+  if (!aligned16(ab)) return LRM_ERR_UNSUPPORTED;
+  return p->dtype == LRM_BF16 ? launch_pack<__nv_bfloat16>(p, ab, (cudaStream_t)stream)
+                              : launch_pack<float>(p, ab, (cudaStream_t)stream);
+}
+
+extern "C" lrm_status lrm_score_packed(const lrm_shape* s, const lrm_packed* p, const void* g,
+                                       const float* alpha, const int32_t* inv, float* score,
+                                       void* ws, size_t ws_bytes, void* stream) {
+  LRM_NVTX("lrm_score_packed");
+  lrm_status st = check_layer(s, p, ws, ws_bytes);
+  if (st != LRM_OK) return st;
+  if (s->T == 0) return LRM_OK;
+  if (!g || !alpha || !inv || !score) return LRM_ERR_INVALID_ARG;
+  if (!aligned16(g)) return LRM_ERR_UNSUPPORTED;
+  cudaStream_t cs = (cudaStream_t)stream;
+  const dim3 grid((unsigned)(((int64_t)s->T + kScoreWarps - 1) / kScoreWarps));
+  if (s->dtype == LRM_BF16)
+    launch_k(score_packed_kernel<__nv_bfloat16>, grid, dim3(32 * kScoreWarps), 0, cs,
+             (const __nv_bfloat16*)g, (const float*)p->phi_sq, alpha, inv, score, s->T, s->D, s->K,
+             error_word(ws));
+  else
+    launch_k(score_packed_kernel<float>, grid, dim3(32 * kScoreWarps), 0, cs, (const float*)g,
+             (const float*)p->phi_sq, alpha, inv, score, s->T, s->D, s->K, error_word(ws));
+  return launch_status();
+}
+
+extern "C" lrm_status lrm_compact_packed(
+    const lrm_shape* s, const lrm_packed* pk, const int32_t* perm, const uint8_t* keep,
+    const int32_t* sel_off, const int32_t* sel_pos, const float* alpha, const void* x,
+    const float* x_scale, int32_t x_cols, const void* g, void* dy_c, void* x_c, void* ab_c,
+    void* phi_c, int32_t* tok_c, int32_t* row_of_pos, void* ws, size_t ws_bytes, void* stream) {
+  LRM_NVTX("lrm_compact_packed");
+  lrm_status st = check_layer(s, pk, ws, ws_bytes);
+  if (st != LRM_OK) return st;
+  if (x_c && x_scale && x_cols != 0 && x_cols != 32 && x_cols != 64 && x_cols != 128 &&
+      x_cols != 256)
+    return LRM_ERR_UNSUPPORTED;
+  if (pk->rows == 0) return LRM_OK;
+  for (const void* p : {(const void*)perm, (const void*)keep, (const void*)sel_off,
+                        (const void*)sel_pos, (const void*)alpha, g, (const void*)dy_c,
+                        (const void*)ab_c, (const void*)phi_c, (const void*)tok_c,
+                        (const void*)row_of_pos})
+    if (!p) return LRM_ERR_INVALID_ARG;
+  if (x_c && !x) return LRM_ERR_INVALID_ARG;
+  for (const void* p : {x, g, (const void*)dy_c, (const void*)x_c, (const void*)ab_c,
+                        (const void*)phi_c})
+    if (!aligned16(p)) return LRM_ERR_UNSUPPORTED;
+  const dim3 grid(num_sms() * 8);
+  cudaStream_t cs = (cudaStream_t)stream;
+  const int shift = group_shift(pk->cols);
+  if (s->dtype == LRM_BF16) {
+    using T = __nv_bfloat16;
+    launch_k(compact_packed_kernel<T>, grid, dim3(kUnpackThreads), 0, cs, (const uint8_t*)pk->q,
+             (const float*)pk->scale, shift, perm, keep, sel_off, sel_pos, alpha, x, x_scale,
+             x_cols, (const T*)g, (T*)dy_c, (T*)x_c, (T*)ab_c, (T*)phi_c, tok_c, row_of_pos,
+             s->T, s->D, s->H, s->K, s->E, error_word(ws));
+  } else {
+    using T = float;
+    launch_k(compact_packed_kernel<T>, grid, dim3(kUnpackThreads), 0, cs, (const uint8_t*)pk->q,
+             (const float*)pk->scale, shift, perm, keep, sel_off, sel_pos, alpha, x, x_scale,
+             x_cols, (const T*)g, (T*)dy_c, (T*)x_c, (T*)ab_c, (T*)phi_c, tok_c, row_of_pos,
+             s->T, s->D, s->H, s->K, s->E, error_word(ws));
+  }
+  return launch_status();
+}

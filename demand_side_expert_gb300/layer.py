@@ -1,8 +1,10 @@
 """What stands around the expert passes in a training step, on one GPU.
 
-``Router``      logits -> experts, weights, counts, balance loss and z-loss; and back
-``AddRMSNorm``  residual addition, RMS norm, 8-bit rows with scales; and back
-``AdamW``       one optimizer step over many tensors, moments in 32 bits or in 8
+``Router``       logits -> experts, weights, counts, balance loss and z-loss; and back
+``GroupRouter``  the same with sigmoid or softmax scores, a selection bias and groups
+``AddRMSNorm``   residual addition, RMS norm, 8-bit rows with scales; and back
+``BlockNorm``    norm behind a block, gate, scaled residual, norm in front of the next; and back
+``AdamW``        one optimizer step over many tensors, moments in 32 bits or in 8
 
 Each owns its output buffers and workspace (allocated once through PyTorch on
 its current stream, some of them by the first call that writes them, whose own
@@ -23,10 +25,13 @@ from bisect import bisect_right
 import torch
 
 from . import lrm
-from .pipeline import _TORCH_DTYPE, _after_current, _need, _stream, dtype_code
+from .pipeline import _TORCH_DTYPE, _after_current, _device, _need, _stream, dtype_code
 
 _route, _route_bwd = lrm.entry("lrm_route"), lrm.entry("lrm_route_bwd")
 _norm, _norm_bwd = lrm.entry("lrm_add_rmsnorm"), lrm.entry("lrm_add_rmsnorm_bwd")
+_group_route, _group_route_bwd = lrm.entry("lrm_group_route"), lrm.entry("lrm_group_route_bwd")
+_bias_step = lrm.entry("lrm_bias_step")
+_block, _block_bwd = lrm.entry("lrm_block_norm"), lrm.entry("lrm_block_norm_bwd")
 
 
 def _owned(name: str) -> property:
@@ -51,16 +56,6 @@ def _need_rows(t, name: str, shape: tuple, dtype: torch.dtype, device: torch.dev
     raise ValueError(f"{name}: a {dtype} tensor {shape} with contiguous rows that do not overlap, "
                      f"on {device}, is needed, got {t.dtype} {tuple(t.shape)} strides "
                      f"{t.stride()} on {t.device}")
-
-
-def _device(device) -> torch.device:
-    dev = torch.device(device)
-    if dev.type != "cuda":
-        raise ValueError(f"a CUDA device is needed, got {dev}")
-    here = torch.device("cuda", lrm.current_device())
-    if dev.index is not None and dev != here:  # kernels launch on the current device
-        raise ValueError(f"{dev} is not the current device, {here}")
-    return here
 
 
 class Router:
@@ -287,6 +282,297 @@ class AddRMSNorm:
         self._backward_buffers()
         _norm_bwd(self._ref, dy.data_ptr(), _address(dh), h.data_ptr(), w.data_ptr(), self._at[3],
                   self._dx.data_ptr(), self._dw.data_ptr(), self._ws.data_ptr(), self.ws_bytes, at)
+
+
+_SCORE = {"sigmoid": lrm.LRM_SIGMOID, "softmax": lrm.LRM_SOFTMAX}
+
+
+class GroupRouter:
+    """Top-K router of T tokens over E experts in ``groups`` groups of neighbours.
+
+    ``score``: "sigmoid" or "softmax". A token keeps the ``top_groups`` groups whose
+    ``group_top`` (1 or 2) best experts score highest together and chooses its K experts
+    in them. A bias (``route``) is added to the scores for the choices only, not for the
+    weights. ``renorm``: the weights of a token add up to ``scale``.
+
+    After ``route``: ``topk_idx`` [T, K] int32 and ``alpha`` [T, K] float32 (what
+    ``RecalibratedExpertBackward`` takes); with statistics also ``counts`` [E] int32,
+    ``prob_sum`` [E] and ``loss`` [1], the balance loss. After ``backward``: ``dlogits``
+    [T, E] in the logits' type. See lrm_group_route and lrm_group_route_bwd in
+    include/lrm.h for the definitions.
+    """
+
+    def __init__(self, T: int, E: int, K: int, dtype: str = "f32", score: str = "sigmoid",
+                 groups: int = 1, top_groups: int | None = None, group_top: int = 2,
+                 renorm: bool = True, scale: float = 1.0, balance_coef: float = 0.0,
+                 device: str | torch.device = "cuda"):
+        if score not in _SCORE:
+            raise ValueError(f"score: 'sigmoid' or 'softmax', got {score!r}")
+        self.T, self.E, self.K = T, E, K
+        self._shape = (T, E)
+        self.tdtype = _TORCH_DTYPE[dtype_code(dtype)]
+        top_groups = groups if top_groups is None else top_groups
+        self.desc = lrm.lrm_group_router(T, E, K, dtype_code(dtype), E, _SCORE[score], groups,
+                                         top_groups, group_top, int(renorm), scale, balance_coef)
+        self.ws_bytes = lrm.lrm_group_router_workspace_bytes(self.desc)
+        if self.ws_bytes == 0:
+            raise ValueError(
+                f"unsupported router T={T} E={E} K={K} groups={groups} top_groups={top_groups} "
+                f"group_top={group_top}: E <= 1024 in up to 32 equal groups, K <= 32 experts of "
+                "the kept groups, group_top 1 or 2 and T*K < 2^31 are needed")
+        self.device = dev = _device(device)
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+        with torch.inference_mode(False):  # inference tensors do not count their writes
+            self._ws = empty(self.ws_bytes, dtype=torch.uint8)
+            self._topk_idx, self._alpha = empty(T, K, dtype=torch.int32), empty(T, K)
+            self._counts, self._prob_sum = empty(E, dtype=torch.int32), empty(E)
+            self._loss = empty(1)
+        self._dlogits = self._bias = None
+        # what backward may read: ids and counts of a route, or written by the caller since
+        self._routed = self._counted = T == 0  # no token, nothing to read
+        self._idx_at, self._counts_at = self._topk_idx._version, self._counts._version
+        self._ref = ctypes.byref(self.desc)
+        self._at = tuple(t.data_ptr() for t in (self._topk_idx, self._alpha, self._counts,
+                                                self._prob_sum, self._loss, self._ws))
+        lrm.lrm_clear_device_error(self._ws, self.ws_bytes)
+
+    topk_idx, alpha, counts = _owned("topk_idx"), _owned("alpha"), _owned("counts")
+    prob_sum, loss, ws = _owned("prob_sum"), _owned("loss"), _owned("ws")
+
+    @property
+    def dlogits(self) -> torch.Tensor:
+        if self._dlogits is None:  # a router that only serves has no gradient
+            self._dlogits = torch.empty(self.T, self.E, dtype=self.tdtype, device=self.device)
+        return self._dlogits
+
+    def _inputs(self, logits, mask):
+        self.desc.stride = _need_rows(logits, "logits", self._shape, self.tdtype, self.device)
+        if mask is not None:
+            if mask.dtype is torch.bool:
+                mask = mask.view(torch.uint8)
+            _need(mask, "mask", (self.T,), torch.uint8, self.device)
+        return mask
+
+    def _has_counts(self) -> bool:
+        return self._counted or self._counts._version != self._counts_at
+
+    def route(self, logits, bias=None, mask=None, stats: bool = True, stream=None):
+        """Routes the tokens of ``logits`` [T, E] (rows may be strided; -inf closes an
+        expert to a token). ``bias`` [E] float32: added to the scores for the choices.
+        ``mask`` [T] bool or uint8: tokens that are 0 there get weight 0 and count
+        nowhere. ``stats=False`` skips counts and loss (serving)."""
+        mask = self._inputs(logits, mask)
+        if bias is not None:
+            _need(bias, "bias", (self.E,), torch.float32, self.device)
+        at = _stream(self.device, stream)
+        topk_idx, alpha, counts, prob_sum, loss, ws = self._at
+        if not stats:
+            counts = prob_sum = loss = None
+        _group_route(self._ref, logits.data_ptr(), _address(bias), _address(mask), topk_idx, alpha,
+                     counts, prob_sum, loss, ws, self.ws_bytes, at)
+        self._routed, self._counted = True, stats or self.T == 0
+        if not stats:
+            self._counts_at = self._counts._version
+
+    def backward(self, logits, dalpha=None, mask=None, dloss=None, stream=None):
+        """The logits' gradient, from the choices and counts of the last ``route`` (with
+        statistics) on the same logits and mask. ``dalpha`` [T, K] float32
+        (``RecalibratedExpertBackward.gate_grad``), ``dloss`` [1] float32: what the
+        balance loss weighs in the total (1 by default). Choices and counts that the
+        caller wrote into ``topk_idx`` and ``counts`` serve as well; without either the
+        call is refused (counts are not needed where the loss's coefficient is 0)."""
+        mask = self._inputs(logits, mask)
+        if not self._routed and self._topk_idx._version == self._idx_at:
+            raise ValueError("no choices to take the gradient of: call route before")
+        if self.desc.balance_coef != 0 and not self._has_counts():
+            raise ValueError("the last route had no statistics, and the loss's gradient needs "
+                             "its counts")
+        if dalpha is not None:
+            _need(dalpha, "dalpha", (self.T, self.K), torch.float32, self.device)
+        if dloss is not None:
+            _need(dloss, "dloss", (1,), torch.float32, self.device)
+        at = _stream(self.device, stream)
+        topk_idx, _, counts, _, _, ws = self._at
+        if self._dlogits is None:
+            _after_current(stream)
+        _group_route_bwd(self._ref, logits.data_ptr(), _address(mask), topk_idx, counts,
+                         _address(dalpha), _address(dloss), self.dlogits.data_ptr(), ws,
+                         self.ws_bytes, at)
+
+    def next_bias(self, bias, rate: float, out=None, stream=None) -> torch.Tensor:
+        """One step of the selection bias towards even loads, from the last route's counts:
+        bias + rate * sign(mean count - count). Written to ``out`` (may be ``bias``; by
+        default a buffer of the router's own, which the next call overwrites)."""
+        if not self._has_counts():
+            raise ValueError("no counts to take the step from: call route with statistics before")
+        _need(bias, "bias", (self.E,), torch.float32, self.device)
+        if out is not None:
+            _need(out, "out", (self.E,), torch.float32, self.device)
+        at = _stream(self.device, stream)
+        if out is None:
+            if self._bias is None:
+                _after_current(stream)
+                self._bias = torch.empty(self.E, device=self.device)
+            out = self._bias
+        step = lrm.lrm_bias(self.E, rate)
+        _bias_step(ctypes.byref(step), self._at[2], bias.data_ptr(), out.data_ptr(), at)
+        return out
+
+    def device_error(self, stream=None) -> int:
+        return lrm.lrm_get_device_error(self._ws, self.ws_bytes, stream)
+
+
+_GATE = {None: lrm.LRM_GATE_NONE, "column": lrm.LRM_GATE_COLUMN, "token": lrm.LRM_GATE_TOKEN}
+
+
+class BlockNorm:
+    """What stands between one block and the next, for T rows of D columns:
+
+      h = residual_scale * residual + gate * (block * block_rstd * w_post)
+      y = h * rstd * w
+
+    ``post=False``: no norm behind the block (then there is no w_post). ``gate``: None, a
+    "column" gate [D] or a "token" gate [T]. ``block_dtype``: "f32" (the experts' ``out``)
+    or the layer's type. After ``forward``: ``h`` and ``y`` [T, D], ``rstd`` [T] and (with
+    ``post``) ``block_rstd`` [T] float32; ``q_cols`` and ``store_y`` as in ``AddRMSNorm``
+    (``q``, ``q_scale``). After ``backward``: ``dres`` [T, D] in ``grad_dtype``,
+    ``dblock`` [T, D] in the layer's type, ``dw`` and ``dw_post`` [D] and ``dgate`` [D] or
+    [T] float32. See lrm_block_norm and lrm_block_norm_bwd in include/lrm.h.
+    """
+
+    def __init__(self, T: int, D: int, dtype: str = "bf16", block_dtype: str = "f32",
+                 gate: str | None = None, post: bool = True, residual_scale: float = 1.0,
+                 eps: float = 1e-6, q_cols: int | None = None, store_y: bool | None = None,
+                 grad_dtype: str = "f32", device: str | torch.device = "cuda"):
+        if gate not in _GATE:
+            raise ValueError(f"gate: None, 'column' or 'token', got {gate!r}")
+        self.T, self.D, self.post, self.gate = T, D, post, gate
+        self._shape, self._columns = (T, D), (D,)
+        self._gate_shape = (D,) if gate == "column" else (T,)
+        self.tdtype = _TORCH_DTYPE[dtype_code(dtype)]
+        self.odtype = _TORCH_DTYPE[dtype_code(block_dtype)]
+        self.gdtype = _TORCH_DTYPE[dtype_code(grad_dtype)]
+        self.desc = lrm.lrm_block(T, D, dtype_code(dtype), dtype_code(block_dtype),
+                                  dtype_code(grad_dtype), _GATE[gate], q_cols or 0, eps,
+                                  residual_scale, D, D)
+        self.ws_bytes = lrm.lrm_block_workspace_bytes(self.desc)
+        if self.ws_bytes == 0:
+            raise ValueError(f"unsupported norm T={T} D={D} q_cols={q_cols} eps={eps} "
+                             f"block_dtype={block_dtype}: D a multiple of 8 up to 8192, q_cols "
+                             "one of 0, 32, 64, 128, 256, eps >= 0 and a block in float32 or "
+                             "the layer's type are needed")
+        store_y = q_cols is None if store_y is None else store_y
+        if q_cols is None and not store_y:
+            raise ValueError("store_y=False leaves no output without q_cols")
+        self.device = dev = _device(device)
+
+        def empty(*shape, dtype=torch.float32):
+            return torch.empty(*shape, dtype=dtype, device=dev)
+
+        with torch.inference_mode(False):  # inference tensors do not count their writes
+            self._rstd = empty(T)
+            self._block_rstd = empty(T) if post else None
+        # another version: the caller wrote it
+        self._rstd_at = self._rstd._version
+        self._block_rstd_at = self._block_rstd._version if post else 0
+        self._h = empty(T, D, dtype=self.tdtype)
+        self._y = empty(T, D, dtype=self.tdtype) if store_y else None
+        self._q = self._q_scale = None
+        if q_cols is not None:
+            self._q = empty(T, D, dtype=torch.float8_e4m3fn)
+            self._q_scale = empty(T, -(-D // q_cols) if q_cols else 1)
+        self._dres = self._dblock = self._dw = self._dw_post = self._dgate = self._ws = None
+        self._normed = T == 0  # there is a 1/rms to take the gradient with
+        self._ref = ctypes.byref(self.desc)
+        self._at = tuple(_address(t) for t in (self._h, self._y, self._q, self._q_scale,
+                                               self._rstd, self._block_rstd))
+
+    h, y, q, q_scale = _owned("h"), _owned("y"), _owned("q"), _owned("q_scale")
+    rstd, block_rstd = _owned("rstd"), _owned("block_rstd")
+
+    def _backward_buffers(self):
+        """Gradients and workspace, allocated on the first backward call only."""
+        if self._dres is None:
+            dev, D = self.device, self.D
+            self._dblock = torch.empty(self.T, D, dtype=self.tdtype, device=dev)
+            self._dw = torch.empty(D, device=dev)
+            self._dw_post = torch.empty(D, device=dev) if self.post else None
+            self._dgate = None if self.gate is None else torch.empty(self._gate_shape, device=dev)
+            self._ws = torch.empty(self.ws_bytes, dtype=torch.uint8, device=dev)
+            self._dres = torch.empty(self.T, D, dtype=self.gdtype, device=dev)
+            self._grads_at = tuple(_address(t) for t in (self._dres, self._dblock, self._dw,
+                                                         self._dw_post, self._dgate, self._ws))
+
+    def _grad(self, name):
+        self._backward_buffers()
+        return getattr(self, name)
+
+    dres = property(lambda self: self._grad("_dres"))
+    dblock = property(lambda self: self._grad("_dblock"))
+    dw = property(lambda self: self._grad("_dw"))
+    dw_post = property(lambda self: self._grad("_dw_post"))
+    dgate = property(lambda self: self._grad("_dgate"))
+
+    def _weights(self, w, w_post, gate):
+        dt, dev = self.tdtype, self.device
+        _need(w, "w", self._columns, dt, dev)
+        if (w_post is None) == self.post:
+            raise ValueError("w_post: " + ("is needed" if self.post else "post=False takes none"))
+        if w_post is not None:
+            _need(w_post, "w_post", self._columns, dt, dev)
+        if (gate is None) != (self.gate is None):
+            raise ValueError("gate: " + ("gate=None takes none" if self.gate is None
+                                         else f"a {self.gate} gate is needed"))
+        if gate is not None:
+            _need(gate, "gate", self._gate_shape, dt, dev)
+
+    def forward(self, block, residual, w, w_post=None, gate=None, stream=None):
+        """block [T, D] in the block's type, residual [T, D] in the layer's (rows of both may
+        be strided by a multiple of 8 elements), w and w_post [D], gate [D] or [T]."""
+        dev, desc = self.device, self.desc
+        block_stride = _need_rows(block, "block", self._shape, self.odtype, dev)
+        res_stride = _need_rows(residual, "residual", self._shape, self.tdtype, dev)
+        self._weights(w, w_post, gate)
+        at = _stream(dev, stream)
+        desc.block_stride, desc.res_stride = block_stride, res_stride
+        h, y, q, q_scale, rstd, block_rstd = self._at
+        try:
+            _block(self._ref, block.data_ptr(), residual.data_ptr(), w.data_ptr(),
+                   _address(w_post), _address(gate), h, y, q, q_scale, rstd, block_rstd, at)
+        except lrm.LrmError:
+            desc.block_stride = desc.res_stride = self.D  # backward is not refused for them
+            raise
+        self._normed = True
+
+    def backward(self, dy, block, w, w_post=None, gate=None, dh=None, h=None, stream=None):
+        """dy [T, D]: the cotangent of y; dh: of h (the residual stream), or None. ``block``
+        is the forward call's, contiguous; ``h`` self.h by default. Uses ``rstd`` and
+        ``block_rstd`` of the last forward, or what the caller wrote there."""
+        dev, shape, gt = self.device, self._shape, self.gdtype
+        if not self._normed and (self._rstd._version == self._rstd_at or self.post and
+                                 self._block_rstd._version == self._block_rstd_at):
+            raise ValueError("no 1/rms to take the gradient with: call forward before")
+        if h is None:
+            if not self._normed:
+                raise ValueError("h: there was no forward, so pass it")
+            h = self._h
+        _need(h, "h", shape, self.tdtype, dev)
+        _need(block, "block", shape, self.odtype, dev)
+        _need(dy, "dy", shape, gt, dev)
+        if dh is not None:
+            _need(dh, "dh", shape, gt, dev)
+        self._weights(w, w_post, gate)
+        at = _stream(dev, stream)
+        if self._dres is None:
+            _after_current(stream)
+        self._backward_buffers()
+        dres, dblock, dw, dw_post, dgate, ws = self._grads_at
+        _block_bwd(self._ref, dy.data_ptr(), _address(dh), h.data_ptr(), block.data_ptr(),
+                   w.data_ptr(), _address(w_post), _address(gate), self._at[4], self._at[5], dres,
+                   dblock, dw, dw_post, dgate, ws, self.ws_bytes, at)
 
 
 _STATE = {"f32": lrm.LRM_STATE_F32, "f8": lrm.LRM_STATE_F8}

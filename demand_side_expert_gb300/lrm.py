@@ -31,13 +31,18 @@ EXPORTS = (
     "lrm_expert_fwd_grouped", "lrm_expert_fc1_recompute", "lrm_expert_bwd_gathered",
     "lrm_select_rate", "lrm_router_workspace_bytes", "lrm_route", "lrm_route_bwd",
     "lrm_gate_grad", "lrm_norm_workspace_bytes", "lrm_add_rmsnorm", "lrm_add_rmsnorm_bwd",
-    "lrm_adamw_step",
+    "lrm_adamw_step", "lrm_group_router_workspace_bytes", "lrm_group_route",
+    "lrm_group_route_bwd", "lrm_bias_step", "lrm_pack_state", "lrm_score_packed",
+    "lrm_compact_packed", "lrm_expert_bwd_compacted", "lrm_block_workspace_bytes",
+    "lrm_block_norm", "lrm_block_norm_bwd",
 )
 LRM_BWD_FC2_DGRAD, LRM_BWD_FC2_WGRAD, LRM_BWD_FC1_WGRAD = 1, 2, 4
 LRM_BWD_FC1_DGRAD, LRM_BWD_SCATTER_DX, LRM_BWD_ALL = 8, 16, 31
 LRM_METRIC_LRM, LRM_METRIC_GRAD_SQ, LRM_METRIC_GRAD_ABS, LRM_METRIC_RANDOM = range(4)
 LRM_NOALLOC_MAX_CHUNK_ENTRIES = 65536
 LRM_STATE_F32, LRM_STATE_F8 = 0, 1
+LRM_SIGMOID, LRM_SOFTMAX = 0, 1
+LRM_GATE_NONE, LRM_GATE_COLUMN, LRM_GATE_TOKEN = range(3)
 
 
 class LrmError(RuntimeError):
@@ -80,6 +85,33 @@ class lrm_adamw(ctypes.Structure):
                 ("grad_scale", ctypes.c_void_p)]
 
 
+class lrm_group_router(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("stride", ctypes.c_int64),
+                ("score_fn", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("renorm", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("balance_coef", ctypes.c_float)]
+
+
+class lrm_bias(ctypes.Structure):
+    _fields_ = [("E", ctypes.c_int32), ("rate", ctypes.c_float)]
+
+
+class lrm_packed(ctypes.Structure):
+    _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("phi_sq", ctypes.c_void_p),
+                ("rows", ctypes.c_int64), ("H", ctypes.c_int32), ("cols", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class lrm_block(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("block_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
+                ("gate", ctypes.c_int32), ("q_cols", ctypes.c_int32), ("eps", ctypes.c_float),
+                ("residual_scale", ctypes.c_float), ("block_stride", ctypes.c_int64),
+                ("res_stride", ctypes.c_int64)]
+
+
 def _load():
     if not os.path.exists(_LIB_PATH):
         raise ImportError(
@@ -90,6 +122,8 @@ def _load():
     sp = ctypes.POINTER(lrm_shape)
     rp, np_ = ctypes.POINTER(lrm_router), ctypes.POINTER(lrm_norm)
     ap, tp = ctypes.POINTER(lrm_adamw), ctypes.POINTER(lrm_adamw_tensor)
+    gp, bp = ctypes.POINTER(lrm_group_router), ctypes.POINTER(lrm_bias)
+    kp, lp = ctypes.POINTER(lrm_packed), ctypes.POINTER(lrm_block)
     sig = {
         "lrm_workspace_bytes": (sz, [sp]),
         "lrm_clear_device_error": (i32, [vp, sz, vp]),
@@ -126,6 +160,17 @@ def _load():
         "lrm_add_rmsnorm": (i32, [np_] + [vp] * 9),
         "lrm_add_rmsnorm_bwd": (i32, [np_] + [vp] * 8 + [sz, vp]),
         "lrm_adamw_step": (i32, [ap, tp, i32, vp]),
+        "lrm_group_router_workspace_bytes": (sz, [gp]),
+        "lrm_group_route": (i32, [gp] + [vp] * 9 + [sz, vp]),
+        "lrm_group_route_bwd": (i32, [gp] + [vp] * 8 + [sz, vp]),
+        "lrm_bias_step": (i32, [bp] + [vp] * 4),
+        "lrm_pack_state": (i32, [kp, vp, vp]),
+        "lrm_score_packed": (i32, [sp, kp] + [vp] * 5 + [sz, vp]),
+        "lrm_compact_packed": (i32, [sp, kp] + [vp] * 7 + [i32] + [vp] * 8 + [sz, vp]),
+        "lrm_expert_bwd_compacted": (i32, [sp] + [vp] * 18 + [sz, vp]),
+        "lrm_block_workspace_bytes": (sz, [lp]),
+        "lrm_block_norm": (i32, [lp] + [vp] * 12),
+        "lrm_block_norm_bwd": (i32, [lp] + [vp] * 15 + [sz, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -439,3 +484,73 @@ def lrm_adamw_step(adamw, tensors, count: int, stream=None):
     """``tensors``: a ctypes array of lrm_adamw_tensor."""
     _check("lrm_adamw_step", _lib.lrm_adamw_step(
         ctypes.byref(adamw), tensors, count, _s(stream)))
+
+
+def lrm_group_router_workspace_bytes(router: lrm_group_router) -> int:
+    return int(_lib.lrm_group_router_workspace_bytes(ctypes.byref(router)))
+
+
+def lrm_group_route(router, logits, bias, mask, topk_idx, alpha, counts, prob_sum, loss, ws,
+                    ws_bytes, stream=None):
+    _check("lrm_group_route", _lib.lrm_group_route(
+        ctypes.byref(router), _p(logits), _p(bias), _p(mask), _p(topk_idx), _p(alpha), _p(counts),
+        _p(prob_sum), _p(loss), _p(ws), ws_bytes, _s(stream)))
+
+
+def lrm_group_route_bwd(router, logits, mask, topk_idx, counts, dalpha, dloss, dlogits, ws,
+                        ws_bytes, stream=None):
+    _check("lrm_group_route_bwd", _lib.lrm_group_route_bwd(
+        ctypes.byref(router), _p(logits), _p(mask), _p(topk_idx), _p(counts), _p(dalpha),
+        _p(dloss), _p(dlogits), _p(ws), ws_bytes, _s(stream)))
+
+
+def lrm_bias_step(step, counts, bias, out, stream=None):
+    _check("lrm_bias_step", _lib.lrm_bias_step(
+        ctypes.byref(step), _p(counts), _p(bias), _p(out), _s(stream)))
+
+
+def lrm_pack_state(packed, ab, stream=None):
+    _check("lrm_pack_state", _lib.lrm_pack_state(ctypes.byref(packed), _p(ab), _s(stream)))
+
+
+def lrm_score_packed(shape, packed, g, alpha, inv, score, ws, ws_bytes, stream=None):
+    _check("lrm_score_packed", _lib.lrm_score_packed(
+        ctypes.byref(shape), ctypes.byref(packed), _p(g), _p(alpha), _p(inv), _p(score), _p(ws),
+        ws_bytes, _s(stream)))
+
+
+def lrm_compact_packed(shape, packed, perm, keep, sel_off, sel_pos, alpha, x, x_scale,
+                       x_cols: int, g, dy_c, x_c, ab_c, phi_c, tok_c, row_of_pos, ws, ws_bytes,
+                       stream=None):
+    _check("lrm_compact_packed", _lib.lrm_compact_packed(
+        ctypes.byref(shape), ctypes.byref(packed), _p(perm), _p(keep), _p(sel_off), _p(sel_pos),
+        _p(alpha), _p(x), _p(x_scale), x_cols, _p(g), _p(dy_c), _p(x_c), _p(ab_c), _p(phi_c),
+        _p(tok_c), _p(row_of_pos), _p(ws), ws_bytes, _s(stream)))
+
+
+def lrm_expert_bwd_compacted(shape, sel_off, tok_c, w_gate, w_up, w_down, dy_c, x, ab_c, phi_c,
+                             inv, row_of_pos, dab_c, dx_c, dw_gate, dw_up, dw_down, dx, ws,
+                             ws_bytes, stream=None):
+    _check("lrm_expert_bwd_compacted", _lib.lrm_expert_bwd_compacted(
+        ctypes.byref(shape), _p(sel_off), _p(tok_c), _p(w_gate), _p(w_up), _p(w_down), _p(dy_c),
+        _p(x), _p(ab_c), _p(phi_c), _p(inv), _p(row_of_pos), _p(dab_c), _p(dx_c), _p(dw_gate),
+        _p(dw_up), _p(dw_down), _p(dx), _p(ws), ws_bytes, _s(stream)))
+
+
+def lrm_block_workspace_bytes(desc: lrm_block) -> int:
+    return int(_lib.lrm_block_workspace_bytes(ctypes.byref(desc)))
+
+
+def lrm_block_norm(desc, block, res, w, w_post, gate, h, y, q, q_scale, rstd, block_rstd,
+                   stream=None):
+    _check("lrm_block_norm", _lib.lrm_block_norm(
+        ctypes.byref(desc), _p(block), _p(res), _p(w), _p(w_post), _p(gate), _p(h), _p(y), _p(q),
+        _p(q_scale), _p(rstd), _p(block_rstd), _s(stream)))
+
+
+def lrm_block_norm_bwd(desc, dy, dh, h, block, w, w_post, gate, rstd, block_rstd, dres, dblock,
+                       dw, dw_post, dgate, ws, ws_bytes, stream=None):
+    _check("lrm_block_norm_bwd", _lib.lrm_block_norm_bwd(
+        ctypes.byref(desc), _p(dy), _p(dh), _p(h), _p(block), _p(w), _p(w_post), _p(gate),
+        _p(rstd), _p(block_rstd), _p(dres), _p(dblock), _p(dw), _p(dw_post), _p(dgate), _p(ws),
+        ws_bytes, _s(stream)))

@@ -16,6 +16,8 @@ and passes pointers.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import lrm
@@ -64,6 +66,73 @@ def _after_current(stream):
     # ExternalStream takes address 0 for a new stream
     other = torch.cuda.ExternalStream(address) if address else torch.cuda.default_stream()
     other.wait_stream(current)
+
+
+_pack = lrm.entry("lrm_pack_state")
+
+
+def _device(device) -> torch.device:
+    dev = torch.device(device)
+    if dev.type != "cuda":
+        raise ValueError(f"a CUDA device is needed, got {dev}")
+    here = torch.device("cuda", lrm.current_device())
+    if dev.index is not None and dev != here:  # kernels launch on the current device
+        raise ValueError(f"{dev} is not the current device, {here}")
+    return here
+
+
+class PackedState:
+    """The saved state of T * K routed pairs in 8 bits, in the place of [a | b] and phi.
+
+    After ``pack``: ``q`` [N, 2H] float8_e4m3fn, ``scale`` [N, 2 ceil(H / cols)]
+    float32 (the groups of a, then those of b) and ``phi_sq`` [N] float32, |phi|^2 of the
+    unquantised state. 2H + 8 ceil(H / cols) + 4 bytes a pair instead of 6H in bfloat16.
+    ``RecalibratedExpertBackward.forward`` packs into one, ``.step`` takes it in the place
+    of [a | b]. See lrm_pack_state in include/lrm.h for the definitions.
+    """
+
+    def __init__(self, T: int, K: int, H: int, dtype: str = "bf16", cols: int = 128,
+                 device: str | torch.device = "cuda"):
+        self.N, self.H, self.cols = T * K, H, cols
+        self.dtype_code = dtype_code(dtype)
+        self.tdtype = _TORCH_DTYPE[self.dtype_code]
+        if T < 0 or K <= 0 or H <= 0 or H % 8 or cols not in (32, 64, 128) or self.N >= 1 << 31:
+            raise ValueError(f"unsupported state T={T} K={K} H={H} cols={cols}: H a multiple of "
+                             "8, cols one of 32, 64, 128 and T*K < 2^31 are needed")
+        self.device = dev = _device(device)
+        with torch.inference_mode(False):  # inference tensors do not count their writes
+            self._q = torch.empty(self.N, 2 * H, dtype=torch.uint8, device=dev).view(
+                torch.float8_e4m3fn)
+            self._scale = torch.empty(self.N, 2 * -(-H // cols), device=dev)
+            self._phi_sq = torch.empty(self.N, device=dev)
+        self._filled = self.N == 0
+        self._q_at = self._q._version  # another one: the caller wrote it
+        self.desc = lrm.lrm_packed(self._q.data_ptr(), self._scale.data_ptr(),
+                                   self._phi_sq.data_ptr(), self.N, H, cols, self.dtype_code, 0)
+        self._ref = ctypes.byref(self.desc)
+
+    q = property(lambda self: self._q)
+    scale = property(lambda self: self._scale)
+    phi_sq = property(lambda self: self._phi_sq)
+
+    @property
+    def filled(self) -> bool:
+        """Whether there is a state: of ``pack``, or written by the caller."""
+        return self._filled or self._q._version != self._q_at
+
+    def pack(self, ab, stream=None):
+        """Quantises ab [N, 2H], in the layer's type."""
+        _need(ab, "ab", (self.N, 2 * self.H), self.tdtype, self.device)
+        _pack(self._ref, ab.data_ptr(), _stream(self.device, stream))
+        self._filled = True
+
+
+def _x_groups(D: int, groups: int) -> int:
+    """Columns under one scale of 8-bit rows with ``groups`` scales (0: a scale a row)."""
+    for cols in (0, 256, 128, 64, 32):
+        if groups == (-(-D // cols) if cols else 1):
+            return cols
+    raise ValueError(f"x: {groups} scales for {D} columns")
 
 
 class RecalibratedExpertBackward:
@@ -136,16 +205,31 @@ class RecalibratedExpertBackward:
     def y(self, rows):
         self._y = rows
 
-    def forward(self, topk_idx, alpha, x, w_gate, w_up, w_down, stream=None):
+    def forward(self, topk_idx, alpha, x, w_gate, w_up, w_down, stream=None,
+                packed: PackedState | None = None):
         """Forward expert pass: dispatch, gather, gate/up + SwiGLU, down,
         combine. Leaves the saved state in ``ab`` / ``phi`` (dispatch order)
-        and the layer output in ``out`` (float32 [T, D])."""
+        and the layer output in ``out`` (float32 [T, D]). ``packed`` gets the
+        state in 8 bits: ``ab`` and ``phi`` may then serve the next layer."""
+        if packed is not None:
+            self._check_packed(packed)
         self._forward_buffers(stream)
         self._expert_outputs(stream)
         self.dispatch(topk_idx, stream)
         lrm.lrm_expert_fwd_grouped(self.shape, self.perm, self.inv, self.off, alpha, x, w_gate,
                                    w_up, w_down, self.x_disp, self.ab, self.phi, self.y,
                                    self.out, self.ws, self.ws_bytes, stream)
+        if packed is not None:
+            packed.pack(self.ab[:self.N], stream)
+
+    def _check_packed(self, packed: PackedState, filled: bool = False):
+        if packed.N != self.N or packed.H != self.H or packed.tdtype is not self.tdtype:
+            raise ValueError(f"packed: a state of {self.N} pairs, H={self.H}, {self.tdtype} is "
+                             f"needed, got {packed.N}, {packed.H}, {packed.tdtype}")
+        if packed.device != self.ws.device:
+            raise ValueError(f"packed: on {packed.device}, the buffers are on {self.ws.device}")
+        if filled and not packed.filled:
+            raise ValueError("packed: nothing has been packed into it")
 
     def gather_tokens(self, x, stream=None):
         self._forward_buffers(stream)
@@ -194,7 +278,15 @@ class RecalibratedExpertBackward:
         lrm.lrm_quota_from_rate(self.counts, self.E, num, den, cap, self.quota, stream)
 
     def score_pairs(self, alpha, g, phi, stream=None, metric: int = 0, seed: int = 0):
-        """LRM scores (metric 0) or one of the ablation criteria (lrm.LRM_METRIC_*)."""
+        """LRM scores (metric 0) or one of the ablation criteria (lrm.LRM_METRIC_*).
+        phi may be a PackedState, which holds its rows' squares."""
+        if isinstance(phi, PackedState):
+            self._check_packed(phi, filled=True)
+            if metric == lrm.LRM_METRIC_LRM:
+                lrm.lrm_score_packed(self.shape, phi.desc, g, alpha, self.inv, self.score, self.ws,
+                                     self.ws_bytes, _stream(phi.device, stream))
+                return
+            phi = None  # the other criteria do not read it
         if metric == lrm.LRM_METRIC_LRM:
             lrm.lrm_score(self.shape, g, phi, alpha, self.inv, self.score, self.ws,
                           self.ws_bytes, stream)
@@ -214,13 +306,45 @@ class RecalibratedExpertBackward:
     def compact(self, alpha, x, g, ab, phi, stream=None, gathered: bool = False):
         """Gather the retained rows; ab=None copies no [a | b] (recompute);
         gathered=True writes only the gradient rows (the products then read
-        x, ab and phi in place)."""
+        x, ab and phi in place). With a PackedState as ab, [a | b] and phi are
+        rebuilt from it, gathered is about x alone, and x may be 8-bit rows with
+        their scales (see ``step``)."""
+        if isinstance(ab, PackedState):
+            self._compact_packed(alpha, x, g, ab, stream, gathered)
+            return
         x_c = None if gathered else self.x_c
         ab_c = None if (gathered or ab is None) else self.ab_c
         phi_c = None if gathered else self.phi_c
         lrm.lrm_compact(self.shape, self.perm, self.keep, self.sel_off, self.sel_pos, alpha, x,
                         g, ab, phi, self.dy_c, x_c, ab_c, phi_c, self.tok_c, self.row_of_pos,
                         self.ws, self.ws_bytes, stream)
+
+    def _compact_packed(self, alpha, x, g, packed, stream, gathered):
+        self._check_packed(packed, filled=True)
+        dev, x_scale, cols = self.ws.device, None, 0
+        if isinstance(x, (tuple, list)):
+            x, x_scale = x
+            _need(x, "x", (self.T, self.D), torch.float8_e4m3fn, dev)
+            cols = _x_groups(self.D, x_scale.shape[-1])
+            _need(x_scale, "x's scales", (self.T, x_scale.shape[-1]), torch.float32, dev)
+            if gathered:
+                raise ValueError("8-bit x is not read in place: gathered=False")
+        else:
+            _need(x, "x", (self.T, self.D), self.tdtype, dev)
+        _need(g, "g", (self.T, self.D), self.tdtype, dev)
+        _need(alpha, "alpha", (self.T, self.K), torch.float32, dev)
+        lrm.lrm_compact_packed(self.shape, packed.desc, self.perm, self.keep, self.sel_off,
+                               self.sel_pos, alpha, x, x_scale, cols, g, self.dy_c,
+                               None if gathered else self.x_c, self.ab_c, self.phi_c, self.tok_c,
+                               self.row_of_pos, self.ws, self.ws_bytes, _stream(dev, stream))
+
+    def expert_bwd_compacted(self, x, w_gate, w_up, w_down, stream=None):
+        """The expert backward over compacted [a | b] and phi, reading x rows in place
+        (after a gathered compaction of a PackedState)."""
+        lrm.lrm_expert_bwd_compacted(
+            self.shape, self.sel_off, self.tok_c, w_gate, w_up, w_down, self.dy_c, x, self.ab_c,
+            self.phi_c, self.inv, self.row_of_pos, self.dab_c, self.dx_c, self.dw_gate,
+            self.dw_up, self.dw_down, self.dx, self.ws, self.ws_bytes, stream)
 
     def fc1_recompute(self, w_gate, w_up, stream=None):
         """[a | b] of the retained rows rebuilt from x_c (no saved [a | b])."""
@@ -277,9 +401,19 @@ class RecalibratedExpertBackward:
         """One pass of the whole path. ab / phi are in dispatch order; `metric`
         picks the selection criterion (LRM by default). ab=None recomputes
         [a | b] of the retained rows instead of reading saved state;
-        gathered=True lets the products read x, ab and phi rows in place."""
+        gathered=True lets the products read x, ab and phi rows in place.
+        ab a PackedState (phi is then not needed): [a | b] and phi of the
+        retained rows come from its 8 bits; x may then be (q, q_scale), 8-bit
+        rows as AddRMSNorm and BlockNorm write them; gathered lets the product
+        read a 16- or 32-bit x in place."""
         if gathered and ab is None:
             raise ValueError("the gathered backward reads saved [a | b]")
+        packed = isinstance(ab, PackedState)
+        if packed:
+            self._check_packed(ab, filled=True)
+            phi = ab
+        if isinstance(x, (tuple, list)) and (gathered or not packed):
+            raise ValueError("8-bit x goes with a PackedState and gathered=False")
         self.dispatch(topk_idx, stream)
         self.score_pairs(alpha, g, phi, stream, metric, seed)
         if quota is None:
@@ -288,6 +422,9 @@ class RecalibratedExpertBackward:
             self.quota.copy_(quota)
             self.select(stream)
         self.compact(alpha, x, g, ab, phi, stream, gathered)
+        if packed and gathered:
+            self.expert_bwd_compacted(x, w_gate, w_up, w_down, stream)
+            return
         if gathered:
             self.expert_bwd_gathered(x, ab, phi, w_gate, w_up, w_down, stream=stream)
             return

@@ -614,6 +614,213 @@ typedef struct lrm_adamw {
 lrm_status lrm_adamw_step(const lrm_adamw* adamw, const lrm_adamw_tensor* tensors,
                           int32_t count, void* stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Training under tight memory: a router with groups, the saved state in 8 bits,
+ * the norms around a block. Descriptors are HOST structs, read during the call only.
+ * ---------------------------------------------------------------------------
+ */
+
+/*
+ * Router over groups of experts. The E experts stand in `groups` groups of E / groups
+ * consecutive ones. A logit of -inf closes its expert to the token. A token takes part
+ * if its mask byte is not 0 (mask NULL: all) and at least one of its logits is above
+ * -inf (NaN is). For every token:
+ *   s_te     = sigmoid(x_te) (LRM_SIGMOID) or softmax(x_t)_e (LRM_SOFTMAX)
+ *   key_te   = s_te + bias_e, compared with 64 bits; without a bias: x_te
+ *   a group's score = the sum of the group_top largest s + bias of its open experts
+ *     (fewer open ones: of those; none: below every other group)
+ *   the top_groups groups of the largest scores are kept, equal ones by the lower id
+ *   topk_idx = the K largest keys of the kept groups' experts, descending, equal ones by
+ *     the lower id; closed experts and NaN come last
+ *   alpha    = scale * s at the choices; renorm != 0: divided by their sum before (0
+ *     where that is 0). The bias is in the choices only, not in the weights.
+ * and over the n tokens that take part (at least 1 in the loss), share_te = s_te / sum_e s_te:
+ *   counts[e] = number of (t, k) with topk_idx[t,k] = e, prob_sum[e] = sum_t share_te
+ *   loss[0]   = balance_coef * E / (n^2 K) * sum_e counts[e] prob_sum[e]
+ * Tokens that take no part get alpha = 0 and K valid, distinct ids; they count nowhere.
+ * In a token that takes part a NaN makes the softmax's weights NaN and, where the
+ * sigmoid's choices hold it, its weight (renorm: all of the token's); both make its
+ * shares NaN. Rows of the softmax that hold NaN
+ * or +inf get some K valid, distinct ids of the kept groups. FP32 arithmetic; a choice
+ * that 32 bits cannot tell is looked at with 64. Statistics are added in a fixed order.
+ *   logits [T,E] dtype (read), rows `stride` elements apart (stride >= E).
+ *   bias [E] float (read) or NULL; finite. mask [T] uint8 (read) or NULL.
+ *   topk_idx [T,K] int32, alpha [T,K] float (written).
+ *   counts [E] int32, prob_sum [E] float, loss [1] float (written), or all three
+ *     NULL: no statistics (the serving form).
+ * Limits: E <= 1024, K <= 32, groups <= 32 dividing E, 1 <= top_groups <= groups,
+ * K <= top_groups * E / groups, group_top 1 or 2, T*K < 2^31, else
+ * LRM_ERR_UNSUPPORTED (LRM_ERR_INVALID_ARG for sizes below 1).
+ * ws: lrm_group_router_workspace_bytes, header as everywhere (zeroed once with
+ * lrm_clear_device_error).
+ */
+typedef enum lrm_score_fn { LRM_SIGMOID = 0, LRM_SOFTMAX = 1 } lrm_score_fn;
+typedef struct lrm_group_router {
+  int32_t T, E, K;
+  int32_t dtype;      /* lrm_dtype of logits and dlogits */
+  int64_t stride;     /* elements from one row of logits to the next */
+  int32_t score_fn;   /* lrm_score_fn */
+  int32_t groups, top_groups, group_top;
+  int32_t renorm;
+  float scale, balance_coef;
+} lrm_group_router;
+size_t lrm_group_router_workspace_bytes(const lrm_group_router* router);
+lrm_status lrm_group_route(const lrm_group_router* router, const void* logits,
+                           const float* bias, const uint8_t* mask, int32_t* topk_idx,
+                           float* alpha, int32_t* counts, float* prob_sum, float* loss,
+                           void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Its gradient with respect to the logits, of sum alpha dalpha + dloss[0] loss[0], the
+ * choices and counts taken as constants. With ds the gradient of the scores,
+ *   renorm: ds at the choices = scale (dalpha - sum_k a dalpha) / sum_k s, a = s / sum_k s
+ *   else:   ds at the choices = scale dalpha
+ *   balance: + (c_e - sum_e share c) / sum_e s,
+ *            c_e = dloss[0] balance_coef E counts[e] / (n^2 K), n = sum counts / K
+ *   sigmoid: dx = ds s (1 - s);  softmax: dx = s (ds - sum_e s ds)
+ * Tokens that take no part get zeros, whatever their dalpha.
+ *   logits, mask as lrm_group_route (read); topk_idx [T,K], counts [E] from it (read).
+ *   dalpha [T,K] float (read) or NULL (0); dloss [1] float (read) or NULL (1).
+ *   dlogits [T,E] dtype, contiguous (written).
+ * Ids outside [0,E) are skipped and flag LRM_DEVERR_EXPERT_ID.
+ */
+lrm_status lrm_group_route_bwd(const lrm_group_router* router, const void* logits,
+                               const uint8_t* mask, const int32_t* topk_idx,
+                               const int32_t* counts, const float* dalpha, const float* dloss,
+                               void* dlogits, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * One step of the selection bias towards even loads, without a gradient:
+ *   out[e] = bias[e] + rate * sign(sum counts - E counts[e])
+ * counts [E] int32, bias [E] float (read), out [E] float (written; may be bias).
+ */
+typedef struct lrm_bias {
+  int32_t E;
+  float rate;
+} lrm_bias;
+lrm_status lrm_bias_step(const lrm_bias* step, const int32_t* counts, const float* bias,
+                         float* out, void* stream);
+
+/*
+ * The saved state [a | b] of a forward expert pass in 8 bits (LRMoE Sec. 3.1 keeps it per
+ * routed pair in the layer's type; this is a memory-saving variant): 2H + 8 ceil(H / cols)
+ * + 4 bytes a pair in the place of 6H in bfloat16, phi = SiLU(a) * b being rebuilt from it.
+ *   q [rows,2H] e4m3 bytes: a row's a and b, each by groups of `cols` columns (the last
+ *     one may be shorter): q = e4m3(v / scale), scale = max(amax, 2^-100) / 448
+ *   scale [rows, 2 ceil(H / cols)] float: the groups of a, then those of b
+ *   phi_sq [rows] float: |phi|^2 of the unquantised a and b, for the pairs' scores: the
+ *     selection is that of the exact state
+ * NaN and infinities stay in their group (and their row's phi_sq).
+ * lrm_pack_state: q, scale, phi_sq (written) from ab [rows,2H] dtype (read), in any row
+ * order; lrm_score_packed and lrm_compact_packed take dispatch order.
+ * Limits: H a multiple of 8, cols 32, 64 or 128, else LRM_ERR_UNSUPPORTED.
+ */
+typedef struct lrm_packed {
+  uint8_t* q;
+  float* scale;
+  float* phi_sq;
+  int64_t rows; /* routed pairs */
+  int32_t H, cols;
+  int32_t dtype; /* lrm_dtype of ab */
+  int32_t reserved;
+} lrm_packed;
+lrm_status lrm_pack_state(const lrm_packed* packed, const void* ab, void* stream);
+
+/*
+ * lrm_score from a packed state: R_u = alpha_u^2 * ||g_t||^2 * phi_sq_u (no phi is read).
+ * packed->rows, H and dtype have to be the shape's T*K, H and dtype. Other arguments as
+ * lrm_score.
+ */
+lrm_status lrm_score_packed(const lrm_shape* shape, const lrm_packed* packed, const void* g,
+                            const float* alpha, const int32_t* inv, float* score, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * lrm_compact from a packed state: for retained row j < M, i = sel_pos[j], p = perm[i],
+ * t = p / K, with (a, b) = q * scale of row i in float32,
+ *   dy_c[j] = alpha[p] * g[t],  ab_c[j] = [a | b],  phi_c[j] = SiLU(a) * b,
+ *   x_c[j] = x[t],  tok_c[j] = t,  row_of_pos[i] = j (-1 where keep[i] == 0),
+ * each rounded once to dtype. The rows serve lrm_expert_bwd_grouped, or
+ * lrm_expert_bwd_compacted with x read in place (then x_c NULL: no copy).
+ *   x [T,D] dtype where x_scale is NULL; else e4m3 bytes [T,D] with x_scale
+ *     [T, ceil(D / x_cols)] float, x_cols one of 0 (a scale a row), 32, 64, 128, 256: what
+ *     lrm_add_rmsnorm and lrm_block_norm write (read where x_c is given).
+ * Other arguments, the 64 zero rows after dy_c's and the checks of indices as lrm_compact.
+ */
+lrm_status lrm_compact_packed(const lrm_shape* shape, const lrm_packed* packed,
+                              const int32_t* perm, const uint8_t* keep, const int32_t* sel_off,
+                              const int32_t* sel_pos, const float* alpha, const void* x,
+                              const float* x_scale, int32_t x_cols, const void* g, void* dy_c,
+                              void* x_c, void* ab_c, void* phi_c, int32_t* tok_c,
+                              int32_t* row_of_pos, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * lrm_expert_bwd_grouped over compacted dy_c, ab_c and phi_c, with the rows of x [T,D]
+ * read in place by tok_c in the FC1 weight gradient, as lrm_expert_bwd_gathered does.
+ */
+lrm_status lrm_expert_bwd_compacted(const lrm_shape* shape, const int32_t* sel_off,
+                                    const int32_t* tok_c, const void* w_gate, const void* w_up,
+                                    const void* w_down, const void* dy_c, const void* x,
+                                    const void* ab_c, const void* phi_c, const int32_t* inv,
+                                    const int32_t* row_of_pos, void* dab_c, float* dx_c,
+                                    float* dw_gate, float* dw_up, float* dw_down, float* dx,
+                                    void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * The norm behind a block, its gate, the scaled residual and the norm in front of the next:
+ *   u = block * block_rstd * w_post, block_rstd = 1 / sqrt(mean_d block^2 + eps)
+ *       (w_post NULL: u = block)
+ *   h = residual_scale * res + gate * u
+ *   y = h * rstd * w, rstd = 1 / sqrt(mean_d h^2 + eps); q, q_scale as lrm_add_rmsnorm
+ * gate: LRM_GATE_NONE (1), LRM_GATE_COLUMN (gate [D]) or LRM_GATE_TOKEN (gate [T]).
+ * FP32 arithmetic on unrounded values; h and y are rounded once to dtype.
+ *   block [T,D] block_dtype, rows block_stride apart: LRM_F32 (what lrm_combine writes)
+ *     or dtype; res [T,D] dtype, rows res_stride apart; w, w_post, gate dtype (read).
+ *   h [T,D] dtype, y [T,D] dtype or NULL, q and q_scale or both NULL, rstd [T] float or
+ *     NULL, block_rstd [T] float or NULL (written, contiguous). y or q is required.
+ * h may be res itself where that is contiguous; no other overlap is allowed.
+ * Limits: D a multiple of 8 up to 8192, strides multiples of 8, q_cols one of 0, 32, 64,
+ * 128, 256, else LRM_ERR_UNSUPPORTED.
+ */
+typedef enum lrm_gate { LRM_GATE_NONE = 0, LRM_GATE_COLUMN = 1, LRM_GATE_TOKEN = 2 } lrm_gate;
+typedef struct lrm_block {
+  int32_t T, D;
+  int32_t dtype;       /* of res, w, w_post, gate, h, y, dblock */
+  int32_t block_dtype; /* of block */
+  int32_t grad_dtype;  /* of dy, dh, dres */
+  int32_t gate;        /* lrm_gate */
+  int32_t q_cols;
+  float eps, residual_scale;
+  int64_t block_stride, res_stride;
+} lrm_block;
+size_t lrm_block_workspace_bytes(const lrm_block* block);
+lrm_status lrm_block_norm(const lrm_block* desc, const void* block, const void* res,
+                          const void* w, const void* w_post, const void* gate, void* h, void* y,
+                          void* q, float* q_scale, float* rstd, float* block_rstd,
+                          void* stream);
+
+/*
+ * Its gradients, with xhat = h * rstd, ohat = block * block_rstd:
+ *   dhs    = rstd * (w dy - xhat * mean_d(w dy xhat)) + dh
+ *   dres   = residual_scale * dhs,  dw = sum_t dy * xhat
+ *   du     = gate * dhs,  dgate = sum dhs * u (over t for a gate of columns, over d for
+ *            one of tokens),  dw_post = sum_t du * ohat
+ *   dblock = block_rstd * (w_post du - ohat * mean_d(w_post du ohat)); w_post NULL: du
+ *   dy, dh [T,D] grad_dtype (dh NULL: none), h [T,D] dtype, block [T,D] block_dtype, w,
+ *     w_post, gate as in the forward call, rstd, block_rstd [T] float (read).
+ *   dres [T,D] grad_dtype, dblock [T,D] dtype, dw [D], dw_post [D] (with w_post), dgate [D]
+ *     or [T] (with a gate) float (overwritten). All contiguous; dres may be dy or dh
+ *     itself, no other overlap. Strides and q_cols are not used.
+ * Rows are added in a fixed order (same inputs, same bits). ws: lrm_block_workspace_bytes.
+ */
+lrm_status lrm_block_norm_bwd(const lrm_block* desc, const void* dy, const void* dh,
+                              const void* h, const void* block, const void* w,
+                              const void* w_post, const void* gate, const float* rstd,
+                              const float* block_rstd, void* dres, void* dblock, float* dw,
+                              float* dw_post, float* dgate, void* ws, size_t ws_bytes,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif
