@@ -319,24 +319,31 @@ class RecalibratedExpertBackward:
                         g, ab, phi, self.dy_c, x_c, ab_c, phi_c, self.tok_c, self.row_of_pos,
                         self.ws, self.ws_bytes, stream)
 
-    def _compact_packed(self, alpha, x, g, packed, stream, gathered):
+    def _packed_rows(self, alpha, x, g, packed, gathered):
+        """Checks what a packed state is compacted with: x, its scales or None, and the
+        columns under one of them."""
         self._check_packed(packed, filled=True)
         dev, x_scale, cols = self.ws.device, None, 0
         if isinstance(x, (tuple, list)):
+            if gathered:
+                raise ValueError("8-bit x is not read in place: gathered=False")
             x, x_scale = x
             _need(x, "x", (self.T, self.D), torch.float8_e4m3fn, dev)
             cols = _x_groups(self.D, x_scale.shape[-1])
             _need(x_scale, "x's scales", (self.T, x_scale.shape[-1]), torch.float32, dev)
-            if gathered:
-                raise ValueError("8-bit x is not read in place: gathered=False")
         else:
             _need(x, "x", (self.T, self.D), self.tdtype, dev)
         _need(g, "g", (self.T, self.D), self.tdtype, dev)
         _need(alpha, "alpha", (self.T, self.K), torch.float32, dev)
+        return x, x_scale, cols
+
+    def _compact_packed(self, alpha, x, g, packed, stream, gathered):
+        x, x_scale, cols = self._packed_rows(alpha, x, g, packed, gathered)
         lrm.lrm_compact_packed(self.shape, packed.desc, self.perm, self.keep, self.sel_off,
                                self.sel_pos, alpha, x, x_scale, cols, g, self.dy_c,
                                None if gathered else self.x_c, self.ab_c, self.phi_c, self.tok_c,
-                               self.row_of_pos, self.ws, self.ws_bytes, _stream(dev, stream))
+                               self.row_of_pos, self.ws, self.ws_bytes,
+                               _stream(self.ws.device, stream))
 
     def expert_bwd_compacted(self, x, w_gate, w_up, w_down, stream=None):
         """The expert backward over compacted [a | b] and phi, reading x rows in place
@@ -410,10 +417,10 @@ class RecalibratedExpertBackward:
             raise ValueError("the gathered backward reads saved [a | b]")
         packed = isinstance(ab, PackedState)
         if packed:
-            self._check_packed(ab, filled=True)
+            self._packed_rows(alpha, x, g, ab, gathered)  # all of it, before anything runs
             phi = ab
-        if isinstance(x, (tuple, list)) and (gathered or not packed):
-            raise ValueError("8-bit x goes with a PackedState and gathered=False")
+        elif isinstance(x, (tuple, list)):
+            raise ValueError("8-bit x goes with a PackedState")
         self.dispatch(topk_idx, stream)
         self.score_pairs(alpha, g, phi, stream, metric, seed)
         if quota is None:
