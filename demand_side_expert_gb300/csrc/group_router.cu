@@ -229,13 +229,13 @@ group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
       some |= x[i] != -CUDART_INF_F;
     }
     top = group_fmax<32>(top);
-    const bool use = __any_sync(0xffffffffu, some) && !masked;
+    const bool row_open = __any_sync(0xffffffffu, some), use = row_open && !masked;
     // s = f c: softmax f = exp(x - top), c its inverse sum; sigmoid f = exp(-m) s with
     // m = min(top, 0), so that rows of very low logits keep their shares, and c = exp(m)
     float total = 0.f, c, ptop;
     if (a.softmax) {
 #pragma unroll
-      for (int i = 0; i < NI; ++i) total += s[i] = top > -CUDART_INF_F ? exp_neg(x[i] - top) : 0.f;
+      for (int i = 0; i < NI; ++i) total += s[i] = row_open ? exp_neg(x[i] - top) : 0.f;
       total = group_sum<32>(total);
       c = ptop = __frcp_rn(total == 0.f ? 1.f : total);
     } else {
@@ -447,8 +447,9 @@ group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dl
     }
     top = group_fmax<G>(top);
     const uint32_t who = __ballot_sync(0xffffffffu, some);
-    const bool use =
-        (G == 32 ? who : who >> (lane & ~(G - 1)) & ((1u << (G & 31)) - 1)) != 0 && !masked;
+    const bool row_open =
+        (G == 32 ? who : who >> (lane & ~(G - 1)) & ((1u << (G & 31)) - 1)) != 0;
+    const bool use = row_open && !masked;
     // f: the score over exp(m), less: 1 - s of the sigmoid
     float less[NI], total = 0.f, cdot = 0.f;
     const float m = a.softmax ? top : top > -CUDART_INF_F ? fminf(top, 0.f) : 0.f;
@@ -457,7 +458,7 @@ group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dl
     for (int i = 0; i < NI; ++i) {
       const float xi = x[i];
       if (a.softmax) {
-        x[i] = top > -CUDART_INF_F ? exp_grad<T>(xi - m) : 0.f;
+        x[i] = row_open ? exp_grad<T>(xi - m) : 0.f;
         less[i] = 1.f;
       } else {
         const float u = exp_grad<T>(-fabsf(xi) - m), z = u * c, r = inverse_grad<T>(1.f + z);

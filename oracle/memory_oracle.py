@@ -129,10 +129,12 @@ def quantise_rows(v, cols):
     v = np.asarray(v, dtype=np.float64)
     width = v.shape[1]
     cols = cols or width
-    scale = np.stack([np.fmax(np.fmax.reduce(np.abs(v[:, c:c + cols]), axis=1), AMAX_MIN) / F8_MAX
-                      for c in range(0, width, cols)], 1)
+    amax = np.stack([np.fmax(np.fmax.reduce(np.abs(v[:, c:c + cols]), axis=1), AMAX_MIN)
+                     for c in range(0, width, cols)], 1)
     with np.errstate(invalid="ignore"):
-        return e4m3(v / np.repeat(scale, cols, axis=1)[:, :width]), scale
+        # 448 v is exact: a quotient that lies between two codes is one, and goes to the even
+        # one, where v over a rounded scale would fall to either side
+        return e4m3(v * F8_MAX / np.repeat(amax, cols, axis=1)[:, :width]), amax / F8_MAX
 
 
 def phi(a, b):
