@@ -195,6 +195,42 @@ __device__ __noinline__ int choose_exact(const float (&x)[NI], int lane, const R
   return idx;
 }
 
+// The CTA's statistics from its warps' sums, in a fixed order; a single CTA finishes by
+// itself, the sums of several are added by route_sums_kernel.
+__device__ __forceinline__ void finish_stats(const RouteArgs& a, const float* sm_p,
+                                             const int32_t* sm_c) {
+  __shared__ float red[2][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
+  __syncthreads();
+  const bool alone = gridDim.x == 1;
+  float dot = 0.f, cnt = 0.f;
+  for (int e = threadIdx.x; e < a.E; e += blockDim.x) {
+    float sum = 0.f;
+#pragma unroll 8
+    for (int w = 0; w < nwarp; ++w) sum += sm_p[w * a.E + e];
+    const int n = sm_c[e];
+    if (alone) {
+      a.prob_sum[e] = sum;
+      a.counts[e] = n;
+      dot = fmaf((float)n, sum, dot);
+      cnt += (float)n;
+    } else {
+      a.part[(int64_t)blockIdx.x * a.E + e] = make_float2(sum, __int_as_float(n));
+    }
+  }
+  if (!alone) return;
+  dot = warp_sum(dot);
+  cnt = warp_sum(cnt);
+  if (lane == 0) { red[0][warp] = dot; red[1][warp] = cnt; }
+  __syncthreads();
+  if (warp == 0) {
+    const float d = warp_sum(lane < nwarp ? red[0][lane] : 0.f);
+    // tokens that took part: every one chose K experts
+    const float n = fmaxf(warp_sum(lane < nwarp ? red[1][lane] : 0.f) / (float)a.K, 1.f);
+    if (lane == 0) a.loss[0] = a.balance_coef * (float)a.E * (d / (n * n * (float)a.K));
+  }
+}
+
 template <int NI>
 constexpr int group_route_threads() { return NI <= 4 ? 1024 : NI <= 8 ? 512 : 256; }
 
@@ -325,40 +361,302 @@ group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
     }
   }
   if constexpr (STATS) {
-    // the CTA's sums, in a fixed order; a single CTA finishes by itself, the sums of
-    // several are added by route_sums_kernel
-    __shared__ float red[2][32];
 #pragma unroll
     for (int i = 0; i < NI; ++i)
       if (e0 + i < E) sm_p[warp * E + e0 + i] = acc[i];
-    __syncthreads();
-    const bool alone = gridDim.x == 1;
-    float dot = 0.f, cnt = 0.f;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-      float sum = 0.f;
-#pragma unroll 8
-      for (int w = 0; w < nwarp; ++w) sum += sm_p[w * E + e];
-      const int n = sm_c[e];
-      if (alone) {
-        a.prob_sum[e] = sum;
-        a.counts[e] = n;
-        dot = fmaf((float)n, sum, dot);
-        cnt += (float)n;
-      } else {
-        a.part[(int64_t)blockIdx.x * E + e] = make_float2(sum, __int_as_float(n));
+    finish_stats(a, sm_p, sm_c);
+  }
+}
+
+// The common shapes: groups that are whole lanes, up to 8 choices of up to 256 experts.
+// L lanes a token, NI consecutive experts a lane. A key is 23 bits of fixed point, the
+// range of s + bias cut into 2^23 units, over 8 bits of the expert's id (the lower id is
+// the larger key), so that sorting networks of 32-bit minima and maxima find the choices
+// and equal ones go by their ids. Every lane sorts its keys, the two largest of a group's
+// lanes rank the groups, the others' keys are dropped, and the token's lanes merge
+// their lists of 8 pairwise. A key is within 3.5 units of the real one (5 2^-24 of the
+// score's own, 1 of two roundings to the grid; the softmax 22 p + 2.5), so choices
+// that stand further apart than twice that are sure.
+constexpr int kTopK = 8;
+constexpr int fast_route_threads(int l) { return l == 32 ? 512 : 768; }
+constexpr uint32_t kOpenUnit = 128;  // of the smallest key of an open expert; 1: closed
+
+// Where the keys' grid lies: unit = (s + bias) size + zero.
+struct KeyGrid {
+  float size, zero;
+  __device__ __forceinline__ explicit KeyGrid(float most) {  // the largest |bias|
+    size = 8388000.f / fmaf(2.f, most, 1.f);  // 2^23 less kOpenUnit and what rounds up
+    zero = fmaf(most, size, (float)kOpenUnit);
+  }
+  // bits of the float 2^23 + unit for a score of 0
+  __device__ __forceinline__ float offset(float bias) const {
+    return fmaf(bias, size, zero) + 8388608.f;
+  }
+};
+
+template <int NI, int L>
+__device__ __forceinline__ uint32_t token_bits(uint32_t ballot, int lane) {
+  if constexpr (L == 32) return ballot;
+  else return ballot >> (lane & ~(L - 1)) & ((1u << L) - 1);
+}
+
+template <typename T, int NI, int L, bool SOFTMAX, bool STATS>
+__global__ void __launch_bounds__(fast_route_threads(L), 1)
+group_route_fast_kernel(const T* __restrict__ logits, const RouteArgs a) {
+  pdl_begin();  // predecessor complete before any global access
+  extern __shared__ float sm_p[];  // STATS: sums of the shares [warps][E], then counts [E]
+  __shared__ float sm_off[L < 32 ? NI * L : 1];
+  constexpr int kTokens = 32 / L, kFull = NI * L, kExact = (kFull + 31) / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
+  const int gl = lane % L, E = a.E, K = a.K, e0 = gl * NI;
+  int32_t* sm_c = reinterpret_cast<int32_t*>(sm_p + nwarp * E);
+  float acc[STATS ? NI : 1], off[L == 32 ? NI : 1];
+  float most = 0.f;
+  if (a.bias) {
+#pragma unroll
+    for (int i = 0; i < kExact; ++i) {
+      const int e = i * 32 + lane;
+      most = fmaxf(most, e < E ? fabsf(a.bias[e]) : 0.f);
+    }
+    most = group_fmax<32>(most);
+  }
+  const KeyGrid grid(most);
+  if constexpr (L == 32) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i) off[i] = grid.offset(a.bias && e0 + i < E ? a.bias[e0 + i] : 0.f);
+  } else {
+    for (int e = threadIdx.x; e < kFull; e += blockDim.x)
+      sm_off[e] = grid.offset(a.bias && e < E ? a.bias[e] : 0.f);
+  }
+  if constexpr (STATS) {
+    for (int e = threadIdx.x; e < E; e += blockDim.x) sm_c[e] = 0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) acc[i] = 0.f;
+  }
+  if (STATS || L < 32) __syncthreads();
+  const uint32_t zero = (uint32_t)grid.zero;
+  const int per = a.size / NI;  // lanes a group
+  const int64_t step = (int64_t)gridDim.x * nwarp * kTokens;
+  for (int64_t first = ((int64_t)blockIdx.x * nwarp + warp) * kTokens; first < a.ntok;
+       first += step) {
+    // lanes of a token past the end follow token `first` and write nothing
+    const bool real = first + lane / L < a.ntok;
+    const int64_t t = real ? first + lane / L : first;
+    const T* row = logits + t * a.stride;
+    float x[NI], s[NI];
+    load_run<T, NI>(row, e0, E, a.vec, x);
+    const bool masked = a.mask && a.mask[t] == 0;
+    float low = x[0], total = 0.f, c = 1.f, top = 0.f;
+#pragma unroll
+    for (int i = 1; i < NI; ++i) low = fminf(low, x[i]);
+    bool row_open = true;
+    float base = 0.f;
+    auto score_of = [&](float v) {
+      if constexpr (SOFTMAX) return exp_neg(v - base);
+      float e;
+      asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(v * -1.4426950408889634f));
+      return rcp_fast(1.f + e);
+    };
+    if constexpr (SOFTMAX) {
+      top = x[0];
+#pragma unroll
+      for (int i = 1; i < NI; ++i) top = fmaxf(top, x[i]);
+      top = group_fmax<L>(top);
+      base = top > -CUDART_INF_F ? top : 0.f;  // nothing open: exp(-inf) each
+#pragma unroll
+      for (int i = 0; i < NI; ++i) total += s[i] = score_of(x[i]);
+      total = group_sum<L>(total);
+      row_open = total != 0.f;
+      c = __frcp_rn(row_open ? total : 1.f);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) total += s[i] = score_of(x[i]);
+      total = group_sum<L>(total);
+      // scores below 32 bits (and rows of none): over exp(m), m the largest logit
+      const bool lost = !(total >= 1e-30f);
+      if (__any_sync(0xffffffffu, lost)) {
+        float m = x[0], sum = 0.f;
+#pragma unroll
+        for (int i = 1; i < NI; ++i) m = fmaxf(m, x[i]);
+        m = group_fmax<L>(m);
+        m = m > -CUDART_INF_F ? fminf(m, 0.f) : 0.f;
+        const float cm = exp_neg(m);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float u = exp_neg(-fabsf(x[i]) - m), r = rcp_fast(fmaf(u, cm, 1.f));
+          const float f = x[i] >= 0.f ? r : u * r;
+          sum += f;
+          s[i] = lost ? f : s[i];
+        }
+        sum = group_sum<L>(sum);
+        total = lost ? sum : total;
+        c = lost ? cm : 1.f;
+        row_open = total != 0.f;
       }
     }
-    if (!alone) return;
-    dot = warp_sum(dot);
-    cnt = warp_sum(cnt);
-    if (lane == 0) { red[0][warp] = dot; red[1][warp] = cnt; }
-    __syncthreads();
-    if (warp == 0) {
-      const float d = warp_sum(lane < nwarp ? red[0][lane] : 0.f);
-      // tokens that took part: every one chose K experts
-      const float n = fmaxf(warp_sum(lane < nwarp ? red[1][lane] : 0.f) / (float)K, 1.f);
-      if (lane == 0) a.loss[0] = a.balance_coef * (float)E * (d / (n * n * (float)K));
+    const bool use = row_open && !masked && real;
+    if constexpr (STATS) {
+      const float inv = use ? (SOFTMAX ? c : __frcp_rn(total)) : 0.f;
+      if (use) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) acc[i] = fmaf(s[i], inv, acc[i]);
+      }
     }
+    uint32_t key[NI];
+    const float size = c * grid.size;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const float o = L == 32 ? off[L == 32 ? i : 0] : sm_off[L == 32 ? 0 : e0 + i];
+      key[i] = (__float_as_uint(fmaf(s[i], size, o)) << 8) + (uint32_t)(255 - e0) - i;
+    }
+    if (__any_sync(0xffffffffu, low == -CUDART_INF_F || !(total == total))) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        if (!(x[i] > -CUDART_INF_F)) key[i] = e0 + i < E ? (1u << 8) + (255 - e0) - i : 0u;
+      }
+    }
+    // the lane's 8 largest, sorted
+    constexpr int N = NI < kTopK ? NI : kTopK;
+#pragma unroll
+    for (int i = 0; i < NI; i += N) sort_desc<N>(key + i);
+#pragma unroll
+    for (int i = N; i < NI; i += N) top_of<N>(key, key + i);
+    // units of two keys that may stand the other way round
+    const uint32_t tol = SOFTMAX ? 8u + (uint32_t)(48.f * fminf(c, 1.f)) : 8u;
+    bool sure = true;
+    if (a.groups > 1) {
+      uint32_t k1 = key[0], k2 = NI > 1 ? key[NI > 1 ? 1 : 0] : 0u;
+      for (int o = 1; o < per; o <<= 1) {
+        const uint32_t p = __shfl_xor_sync(0xffffffffu, k1, o), q = __shfl_xor_sync(0xffffffffu, k2, o);
+        k2 = max(max(k2, q), min(k1, p));
+        k1 = max(k1, p);
+      }
+      // a missing second expert adds a score of 0; no open expert: below all
+      k1 >>= 8;
+      k2 >>= 8;
+      uint32_t score = 0;
+      if (k1 >= kOpenUnit / 2) {
+        score = k1;
+        if (a.group_top == 2) score += k2 >= kOpenUnit / 2 ? k2 : zero;
+      }
+      const int g = gl / per, begin = lane & ~(L - 1);
+      int before = 0;
+      const uint32_t margin = 2 * tol + 2;
+      bool close = false;
+      for (int j = 0; j < a.groups; ++j) {
+        const uint32_t other = __shfl_sync(0xffffffffu, score, begin + j * per);
+        before += other > score || (other == score && j < g);
+      }
+      const bool kept = g < a.groups && before < a.top_groups;
+      // the kept groups' least score and the others' largest
+      const uint32_t least = ~group_max<L>(kept ? ~score : 0u);
+      const uint32_t next = group_max<L>(kept || g >= a.groups ? 0u : score);
+      close = next != 0 && least - next <= margin;
+      sure = !close;
+#pragma unroll
+      for (int i = 0; i < N; ++i) key[i] = kept ? key[i] : 0u;
+    }
+    uint32_t v[kTopK];
+#pragma unroll
+    for (int i = 0; i < kTopK; ++i) v[i] = i < N ? key[i] : 0u;
+    merge_lanes<L, kTopK, N, 1>(v);
+    uint32_t mine = 0, last = 0;  // lane k: the k-th choice; the last of all
+#pragma unroll
+    for (int i = 0; i < kTopK; ++i) {
+      mine = gl == i ? v[i] : mine;
+      last = i == K - 1 ? v[i] : last;
+    }
+    const bool choice = gl < K;
+    int idx = min(255 - (int)(mine & 255u), E - 1);
+    float xk = choice ? (float)row[idx] : -CUDART_INF_F;
+    const float bk = a.bias && choice ? a.bias[idx] : 0.f;
+    {
+      const uint32_t next = __shfl_down_sync(0xffffffffu, mine, 1, L);
+      const float xn = __shfl_down_sync(0xffffffffu, xk, 1, L),
+                  bn = __shfl_down_sync(0xffffffffu, bk, 1, L);
+      bool near = gl + 1 < K && (next >> 8) > 1 && (mine >> 8) - (next >> 8) <= tol &&
+                  !(xk == xn && bk == bn);
+      // others that may stand above the last choice: how many keys reach it
+      const uint32_t reach = (last >> 8) > 1 ? ((last >> 8) - min(tol, last >> 8)) << 8 : ~0u;
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < N; ++i) n += key[i] >= reach;
+      bool more = NI > N && key[N - 1] >= reach;  // the lane may hold others
+#pragma unroll
+      for (int o = 1; o < L; o <<= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+      more |= n > K && reach != ~0u;
+      if (__any_sync(0xffffffffu, more)) {
+        // those of the last choice's own logit and bias are below it by their ids
+        const int src = (lane & ~(L - 1)) + K - 1;
+        const float xl = __shfl_sync(0xffffffffu, xk, src), bl = __shfl_sync(0xffffffffu, bk, src);
+        const int il = __shfl_sync(0xffffffffu, idx, src);
+        load_run<T, NI>(row, e0, E, a.vec, x);
+        const bool in = a.groups == 1 || key[0] != 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float bi = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.f;
+          const float o = L == 32 ? off[L == 32 ? i : 0] : sm_off[L == 32 ? 0 : e0 + i];
+          // (scores below 32 bits are 0 in units either way)
+          const float unit = fmaf(score_of(x[i]), SOFTMAX ? size : grid.size, o);
+          const uint32_t k = (__float_as_uint(unit) << 8) + (255 - e0) - i;
+          near |= more && in && x[i] > -CUDART_INF_F && k >= reach && k < last && e0 + i != il &&
+                  !(x[i] == xl && bi == bl);
+        }
+      }
+      sure = sure && !near;
+    }
+    uint32_t again = __ballot_sync(0xffffffffu, !sure && real);
+    while (again) {  // a token at a time, by the whole warp
+      const int at = (__ffs(again) - 1) & ~(L - 1);
+      if constexpr (L == 32) again = 0;
+      else again &= ~(((1u << L) - 1) << at);
+      const int64_t tt = first + at / L;
+      float xe[kExact];
+      load_run<T, kExact>(logits + tt * a.stride, lane * kExact, E, false, xe);
+      const int e = choose_exact<kExact>(xe, lane, a);
+      const int got = __shfl_sync(0xffffffffu, e, gl);
+      if ((lane & ~(L - 1)) == at && choice) {
+        idx = got;
+        xk = (float)row[idx];
+      }
+    }
+    // weights, with float32's accuracy at any logit
+    float w;
+    if constexpr (SOFTMAX) {
+      const float m = a.renorm ? group_fmax<L>(xk) : top;
+      w = choice && m > -CUDART_INF_F ? expf(xk - m) : 0.f;
+      if (!a.renorm) w *= c;
+      if (total != total) w = total;
+    } else {
+      float m = 0.f;
+      if (a.renorm) {
+        const float most_x = group_fmax<L>(xk);
+        m = most_x > -CUDART_INF_F ? fminf(most_x, 0.f) : 0.f;
+      }
+      w = xk >= 0.f ? __frcp_rn(1.f + expf(-xk)) : expf(xk - m) / (1.f + expf(xk));
+      if (!choice) w = 0.f;
+    }
+    if (a.renorm) {
+      const float sum = group_sum<L>(choice ? w : 0.f);
+      w = sum == 0.f ? 0.f : w / sum;
+    }
+    if (choice && real) {
+      a.topk_idx[t * K + gl] = idx;
+      a.alpha[t * K + gl] = use ? w * a.scale : 0.f;
+      if (STATS && use) atomicAdd(&sm_c[idx], 1);
+    }
+  }
+  if constexpr (STATS) {
+#pragma unroll
+    for (int o = L; o < 32; o <<= 1)  // over the warp's tokens
+#pragma unroll
+      for (int i = 0; i < NI; ++i) acc[i] += __shfl_xor_sync(0xffffffffu, acc[i], o);
+    if (lane < L) {
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+        if (e0 + i < E) sm_p[warp * E + e0 + i] = acc[i];
+    }
+    finish_stats(a, sm_p, sm_c);
   }
 }
 
@@ -581,35 +879,34 @@ static lrm_status check_group_ws(const lrm_group_router* r, const void* ws, size
   return ws_bytes < group_router_bytes(r) ? LRM_ERR_WORKSPACE : LRM_OK;
 }
 
-template <typename T, int NI>
-static lrm_status launch_group_route(const void* logits, RouteArgs a, cudaStream_t cs) {
+// `warps` of them have work, `most` of a CTA's threads; the statistics want `capacity`
+// floats a warp.
+template <typename T>
+static lrm_status launch_route_kernel(void (*kern)(const T*, RouteArgs), const void* logits,
+                                      const RouteArgs& a, int64_t warps, int max_warps,
+                                      int capacity, cudaStream_t cs) {
   const bool stats = a.counts != nullptr;
-  constexpr int kMaxWarps = group_route_threads<NI>() / 32;
-  constexpr int kVec = NI * (int)sizeof(T) < 16 ? NI : 16 / (int)sizeof(T);
-  a.vec = a.stride % kVec == 0;
-  const int64_t warps = std::max(1, a.ntok);
   int nwarp;
   int64_t grid;
   if (stats) {
     // one CTA an SM at most (each leaves a row for the last sums), its warps in even
     // rounds; tokens that fit one CTA stay in one, without that second launch
     const int64_t ctas = std::min(num_sms(), kRouterMaxCtas);
-    const int64_t rounds = (warps + ctas * kMaxWarps - 1) / (ctas * kMaxWarps);
+    const int64_t rounds = (warps + ctas * max_warps - 1) / (ctas * max_warps);
     const int64_t need = (warps + rounds - 1) / rounds;
-    nwarp = (int)(need <= kMaxWarps
+    nwarp = (int)(need <= max_warps
                       ? need
-                      : std::max<int64_t>(std::min(16, kMaxWarps), (need + ctas - 1) / ctas));
+                      : std::max<int64_t>(std::min(16, max_warps), (need + ctas - 1) / ctas));
     grid = (need + nwarp - 1) / nwarp;
   } else {
     nwarp = (int)std::min<int64_t>(4, warps);  // a warp for each scheduler of an SM
     grid = std::min<int64_t>((warps + nwarp - 1) / nwarp, 1 << 30);
   }
-  auto kern = stats ? group_route_kernel<T, NI, true> : group_route_kernel<T, NI, false>;
   const size_t smem = stats ? ((size_t)nwarp + 1) * a.E * 4 : 0;
   // the limit is the kernel's, for all host threads: only ever set to the most any call needs
-  constexpr int kMostSmem = (kMaxWarps + 1) * NI * 32 * 4;
+  const int most_smem = (max_warps + 1) * capacity * 4;
   if (smem > 40 * 1024 &&
-      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMostSmem) !=
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most_smem) !=
           cudaSuccess) {
     (void)cudaGetLastError();
     return LRM_ERR_CUDA;
@@ -626,8 +923,60 @@ static lrm_status launch_group_route(const void* logits, RouteArgs a, cudaStream
   return launch_status();
 }
 
+template <typename T, int NI>
+static int run_vec(int64_t stride) {
+  constexpr int kVec = NI * (int)sizeof(T) < 16 ? NI : 16 / (int)sizeof(T);
+  return stride % kVec == 0;
+}
+
+template <typename T, int NI>
+static lrm_status launch_group_route(const void* logits, RouteArgs a, cudaStream_t cs) {
+  a.vec = run_vec<T, NI>(a.stride);
+  return launch_route_kernel<T>(
+      a.counts ? group_route_kernel<T, NI, true> : group_route_kernel<T, NI, false>, logits, a,
+      std::max(1, a.ntok), group_route_threads<NI>() / 32, NI * 32, cs);
+}
+
+template <typename T, int NI, int L>
+static lrm_status launch_fast_route(const void* logits, RouteArgs a, cudaStream_t cs) {
+  a.vec = run_vec<T, NI>(a.stride);
+  constexpr int kTokens = 32 / L;
+  const bool stats = a.counts != nullptr;
+  auto kern = a.softmax ? (stats ? group_route_fast_kernel<T, NI, L, true, true>
+                                 : group_route_fast_kernel<T, NI, L, true, false>)
+                        : (stats ? group_route_fast_kernel<T, NI, L, false, true>
+                                 : group_route_fast_kernel<T, NI, L, false, false>);
+  return launch_route_kernel<T>(kern, logits, a,
+                                std::max<int64_t>(1, ((int64_t)a.ntok + kTokens - 1) / kTokens),
+                                fast_route_threads(L) / 32, NI * L, cs);
+}
+
+// Whether groups are whole lanes of NI experts, a power of two of them.
+static bool whole_lanes(const RouteArgs& a, int ni) {
+  if (a.groups == 1) return true;
+  const int per = a.size / ni;
+  return a.size % ni == 0 && (per & (per - 1)) == 0;
+}
+
 template <typename T>
 static lrm_status pick_group_route(const void* logits, const RouteArgs& a, cudaStream_t cs) {
+  if (a.E <= 256 && a.K <= kTopK) {
+    const int cap = a.E <= 32 ? 32 : a.E <= 64 ? 64 : a.E <= 128 ? 128 : 256;
+    const bool many = (int64_t)a.ntok > (int64_t)num_sms() * 20;
+    const int shared_ni = cap == 32 ? 4 : cap == 64 ? 8 : 16;
+    if (many && whole_lanes(a, shared_ni)) {
+      if (cap == 32) return launch_fast_route<T, 4, 8>(logits, a, cs);
+      if (cap == 64) return launch_fast_route<T, 8, 8>(logits, a, cs);
+      if (cap == 128) return launch_fast_route<T, 16, 8>(logits, a, cs);
+      return launch_fast_route<T, 16, 16>(logits, a, cs);
+    }
+    if (whole_lanes(a, cap / 32)) {
+      if (cap == 32) return launch_fast_route<T, 1, 32>(logits, a, cs);
+      if (cap == 64) return launch_fast_route<T, 2, 32>(logits, a, cs);
+      if (cap == 128) return launch_fast_route<T, 4, 32>(logits, a, cs);
+      return launch_fast_route<T, 8, 32>(logits, a, cs);
+    }
+  }
   if (a.E <= 32) return launch_group_route<T, 1>(logits, a, cs);
   if (a.E <= 64) return launch_group_route<T, 2>(logits, a, cs);
   if (a.E <= 128) return launch_group_route<T, 4>(logits, a, cs);
