@@ -195,6 +195,25 @@ __device__ __noinline__ int choose_exact(const float (&x)[NI], int lane, const R
   return idx;
 }
 
+// Keys on a grid: the range of s + bias cut into 2^23 units, kOpenUnit and above for open
+// experts, 1 for closed ones (and NaN), 0 for what is no choice. A key is within 3.5 units
+// of the real one: 5 2^-24 of the sigmoid's own error and 1 of two roundings to the grid;
+// (22 p + 2.5) for the softmax, whose sum carries 43 2^-24 of p.
+constexpr uint32_t kOpenUnit = 128;
+
+// Where the keys' grid lies: unit = (s + bias) size + zero.
+struct KeyGrid {
+  float size, zero;
+  __device__ __forceinline__ explicit KeyGrid(float most) {  // the largest |bias|
+    size = 8388000.f / fmaf(2.f, most, 1.f);  // 2^23 less kOpenUnit and what rounds up
+    zero = fmaf(most, size, (float)kOpenUnit);
+  }
+  // bits of the float 2^23 + unit for a score of 0
+  __device__ __forceinline__ float offset(float bias) const {
+    return fmaf(bias, size, zero) + 8388608.f;
+  }
+};
+
 // The CTA's statistics from its warps' sums, in a fixed order; a single CTA finishes by
 // itself, the sums of several are added by route_sums_kernel.
 __device__ __forceinline__ void finish_stats(const RouteArgs& a, const float* sm_p,
@@ -231,6 +250,172 @@ __device__ __forceinline__ void finish_stats(const RouteArgs& a, const float* sm
   }
 }
 
+
+__device__ __forceinline__ uint32_t pair_tolerance(bool softmax, float ptop) {
+  return softmax ? 8u + (uint32_t)(48.f * fminf(ptop, 1.f)) : 8u;
+}
+
+// Puts the elements that `take` into the warp's list; their number.
+template <int NI, typename Take>
+__device__ __forceinline__ int gather(int lane, uint16_t* list, Take take) {
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const bool mine = take(i);
+    const uint32_t who = __ballot_sync(0xffffffffu, mine);
+    const int at = n + __popc(who & lanemask_lt());
+    if (mine && at < 32) list[at] = (uint16_t)(lane * NI + i);
+    n += __popc(who);
+  }
+  __syncwarp();
+  return n;
+}
+
+// A token's choices where keys of 32 bits leave some open: the few experts (and groups)
+// that stand nearer to one another than their keys can tell get keys of 64 bits, a lane
+// each; more than a warp of them, and all do. By the whole warp; `list`: its 64 entries.
+template <typename T, int NI>
+__device__ __noinline__ int resolve(const T* row, int lane, const RouteArgs& a, float grid_size,
+                                    float grid_zero, uint16_t* list) {
+  float x[NI];
+  load_run<T, NI>(row, lane * NI, a.E, false, x);
+  const int e0 = lane * NI;
+  float top = x[0];
+#pragma unroll
+  for (int i = 1; i < NI; ++i) top = fmaxf(top, x[i]);
+  top = group_fmax<32>(top);
+  float total = 0.f, c = 1.f, s[NI];
+  const float m = a.softmax ? (top > -CUDART_INF_F ? top : 0.f) : 0.f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+    total += s[i] = a.softmax ? exp_neg(x[i] - m) : rcp_fast(1.f + exp_neg(-x[i]));
+  if (a.softmax) {
+    total = group_sum<32>(total);
+    c = __frcp_rn(total);
+  }
+  const uint32_t tol = pair_tolerance(a.softmax, c);
+  uint32_t u[NI], w[NI];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const float b = a.bias && e0 + i < a.E ? a.bias[e0 + i] : 0.f;
+    const float o = fmaf(b, grid_size, grid_zero) + 8388608.f;
+    u[i] = __float_as_uint(fmaf(s[i], c * grid_size, o)) & 0x7fffffu;
+    if (!(x[i] > -CUDART_INF_F)) u[i] = e0 + i < a.E ? 1u : 0u;
+  }
+  // 64-bit scores; the softmax's over its row's sum only where a bias is added to it
+  double scale = 1.0;
+  if (a.softmax && a.bias) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+      sum += x[i] > -CUDART_INF_F ? exp((double)x[i] - (double)m) : 0.0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    scale = sum;
+  }
+  auto exact = [&](int e) {
+    const double v = (double)(float)row[e];
+    double k = a.softmax ? exp(v - (double)m) / scale : 1.0 / (1.0 + exp(-v));
+    if (a.bias) k += (double)a.bias[e];
+    return k == k ? k : -CUDART_INF;  // (a softmax with NaN or +inf: by the ids)
+  };
+  if (a.groups > 1) {
+    uint32_t score = 0, second = 0;  // lane g: of group g
+    for (int g = 0; g < a.groups; ++g) {
+      uint32_t k1 = 0, k2 = 0;
+      const int lo = g * a.size - e0, hi = lo + a.size;
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        const uint32_t f = i >= lo && i < hi ? u[i] : 0u;
+        k2 = max(k2, min(k1, f));
+        k1 = max(k1, f);
+      }
+      // the warp's largest, then the largest of what is left
+      const uint32_t best = __reduce_max_sync(0xffffffffu, k1);
+      const int who = __ffs(__ballot_sync(0xffffffffu, k1 == best)) - 1;
+      const uint32_t next = __reduce_max_sync(0xffffffffu, lane == who ? k2 : k1);
+      if (lane == g && best >= kOpenUnit / 2) {
+        const bool two = a.group_top == 2, has = next >= kOpenUnit / 2;
+        score = best + (two ? has ? next : (uint32_t)grid_zero : 0u);
+        second = two && has ? next : best;
+      }
+    }
+    const bool group = lane < a.groups;
+    int before = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      const uint32_t other = __shfl_sync(0xffffffffu, score, g);
+      before += other > score || (other == score && g < lane);
+    }
+    bool kept = group && before < a.top_groups;
+    const uint32_t least = __reduce_min_sync(0xffffffffu, kept ? score : ~0u);
+    const uint32_t next = __reduce_max_sync(0xffffffffu, group && !kept ? score : 0u);
+    const uint32_t margin = 2 * tol + 2;
+    if (next != 0 && least - next <= margin) {
+      // kept for sure: those above every other's reach; the rest by their exact scores
+      const bool open = group && score != 0 && score + margin >= least && score <= next + margin;
+      const uint32_t in_doubt = __ballot_sync(0xffffffffu, open);
+      const uint32_t sure = __ballot_sync(0xffffffffu, kept && !open);
+      const uint32_t floor_of = second > tol ? second - tol : 1u;
+      const int n = [&] {
+        int g = e0 / a.size, at = e0 - g * a.size, count = 0;
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const uint32_t f = __shfl_sync(0xffffffffu, floor_of, min(g, 31));
+          const bool mine = u[i] >= kOpenUnit / 2 && g < 32 && (in_doubt >> g & 1) && u[i] >= f;
+          const uint32_t who = __ballot_sync(0xffffffffu, mine);
+          const int place = count + __popc(who & lanemask_lt());
+          if (mine && place < 32) list[place] = (uint16_t)(e0 + i);
+          count += __popc(who);
+          if (++at == a.size) { at = 0; ++g; }
+        }
+        __syncwarp();
+        return count;
+      }();
+      if (n > 32) return choose_exact<NI>(x, lane, a);
+      const int e = lane < n ? list[lane] : 0;
+      const double v = lane < n ? exact(e) : 0.0;
+      double k1 = -CUDART_INF, k2 = -CUDART_INF;  // lane g: of group g
+      for (int j = 0; j < n; ++j) {
+        const double f = __shfl_sync(0xffffffffu, v, j);
+        const int g = __shfl_sync(0xffffffffu, e, j) / a.size;
+        if (g == lane) merge_two(k1, k2, f, -(double)CUDART_INF);
+      }
+      const double mine = a.group_top == 2 && k2 > -CUDART_INF ? k1 + k2 : k1;
+      before = 0;
+      for (int g = 0; g < a.groups; ++g) {
+        const double other = __shfl_sync(0xffffffffu, mine, g);
+        before += (in_doubt >> g & 1) && (other > mine || (other == mine && g < lane));
+      }
+      kept = (sure >> lane & 1) || (open && before < a.top_groups - __popc(sure));
+    }
+    drop_groups(u, lane, a.size, __ballot_sync(0xffffffffu, kept));
+    __syncwarp();
+  }
+#pragma unroll
+  for (int i = 0; i < NI; ++i) w[i] = u[i];
+  int idx = 0;
+  uint32_t key = 0;
+  choose(w, lane, a.K, idx, key);
+  const uint32_t last = __shfl_sync(0xffffffffu, key, a.K - 1);
+  const uint32_t reach = last >= kOpenUnit / 2 ? last - min(tol, last) : kOpenUnit / 2;
+  const int n = gather<NI>(lane, list, [&](int i) { return u[i] >= reach; });
+  if (n > 32) return choose_exact<NI>(x, lane, a);
+  // (closed experts, where too few are open, stand behind in the order of their ids)
+  const int e = lane < n ? list[lane] : 0;
+  const double v = lane < n ? (a.bias ? exact(e) : (double)(float)row[e]) : 0.0;
+  int place = 0;
+  for (int j = 0; j < n; ++j) {
+    const double other = __shfl_sync(0xffffffffu, v, j);
+    const int oe = __shfl_sync(0xffffffffu, e, j);
+    place += other > v || (other == v && oe < e);
+  }
+  if (lane < n) list[32 + place] = (uint16_t)e;
+  __syncwarp();
+  if (lane < min(n, a.K)) idx = list[32 + lane];
+  __syncwarp();
+  return idx;
+}
+
 template <int NI>
 constexpr int group_route_threads() { return NI <= 4 ? 1024 : NI <= 8 ? 512 : 256; }
 
@@ -240,6 +425,7 @@ __global__ void __launch_bounds__(group_route_threads<NI>(), 1)
 group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
   pdl_begin();  // predecessor complete before any global access
   extern __shared__ float sm_p[];  // STATS: sums of the shares [warps][E], then counts [E]
+  __shared__ uint16_t sm_list[group_route_threads<NI>() / 32][64];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
   const int E = a.E, K = a.K, e0 = lane * NI;
   int32_t* sm_c = reinterpret_cast<int32_t*>(sm_p + nwarp * E);
@@ -250,8 +436,13 @@ group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
     for (int i = 0; i < NI; ++i) acc[i] = 0.f;
     __syncthreads();
   }
+  float bias_most = 0.f;
 #pragma unroll
-  for (int i = 0; i < NI; ++i) b[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.f;
+  for (int i = 0; i < NI; ++i) {
+    b[i] = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.f;
+    bias_most = fmaxf(bias_most, fabsf(b[i]));
+  }
+  bias_most = group_fmax<32>(bias_most);
   for (int64_t t = (int64_t)blockIdx.x * nwarp + warp; t < a.ntok; t += (int64_t)gridDim.x * nwarp) {
     const T* row = logits + t * a.stride;
     float x[NI], s[NI];
@@ -327,7 +518,8 @@ group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
       sure = sure && !__any_sync(0xffffffffu, near);
     }
     if (!sure) {
-      idx = choose_exact<NI>(x, lane, a);
+      const KeyGrid grid(bias_most);
+      idx = resolve<T, NI>(row, lane, a, grid.size, grid.zero, sm_list[warp]);
       xk = choice ? (float)row[idx] : -CUDART_INF_F;
     }
     // weights, with float32's accuracy at any logit
@@ -369,36 +561,14 @@ group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
 }
 
 // The common shapes: groups that are whole lanes, up to 8 choices of up to 256 experts.
-// L lanes a token, NI consecutive experts a lane. A key is 23 bits of fixed point, the
-// range of s + bias cut into 2^23 units, over 8 bits of the expert's id (the lower id is
-// the larger key), so that sorting networks of 32-bit minima and maxima find the choices
-// and equal ones go by their ids. Every lane sorts its keys, the two largest of a group's
-// lanes rank the groups, the others' keys are dropped, and the token's lanes merge
-// their lists of 8 pairwise. A key is within 3.5 units of the real one (5 2^-24 of the
-// score's own, 1 of two roundings to the grid; the softmax 22 p + 2.5), so choices
-// that stand further apart than twice that are sure.
+// L lanes a token, NI consecutive experts a lane. A key is its unit on the grid over 8
+// bits of the expert's id (the lower id is the larger key), so that sorting networks of
+// 32-bit minima and maxima find the choices and equal ones go by their ids. Every lane
+// sorts its keys, the two largest of a group's lanes rank the groups, the others' keys
+// are dropped, and the token's lanes merge their lists of 8 pairwise. Choices that stand
+// further apart than both keys' errors are sure.
 constexpr int kTopK = 8;
 constexpr int fast_route_threads(int l) { return l == 32 ? 512 : 768; }
-constexpr uint32_t kOpenUnit = 128;  // of the smallest key of an open expert; 1: closed
-
-// Where the keys' grid lies: unit = (s + bias) size + zero.
-struct KeyGrid {
-  float size, zero;
-  __device__ __forceinline__ explicit KeyGrid(float most) {  // the largest |bias|
-    size = 8388000.f / fmaf(2.f, most, 1.f);  // 2^23 less kOpenUnit and what rounds up
-    zero = fmaf(most, size, (float)kOpenUnit);
-  }
-  // bits of the float 2^23 + unit for a score of 0
-  __device__ __forceinline__ float offset(float bias) const {
-    return fmaf(bias, size, zero) + 8388608.f;
-  }
-};
-
-template <int NI, int L>
-__device__ __forceinline__ uint32_t token_bits(uint32_t ballot, int lane) {
-  if constexpr (L == 32) return ballot;
-  else return ballot >> (lane & ~(L - 1)) & ((1u << L) - 1);
-}
 
 template <typename T, int NI, int L, bool SOFTMAX, bool STATS>
 __global__ void __launch_bounds__(fast_route_threads(L), 1)
@@ -406,6 +576,7 @@ group_route_fast_kernel(const T* __restrict__ logits, const RouteArgs a) {
   pdl_begin();  // predecessor complete before any global access
   extern __shared__ float sm_p[];  // STATS: sums of the shares [warps][E], then counts [E]
   __shared__ float sm_off[L < 32 ? NI * L : 1];
+  __shared__ uint16_t sm_list[fast_route_threads(L) / 32][64];
   constexpr int kTokens = 32 / L, kFull = NI * L, kExact = (kFull + 31) / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarp = blockDim.x >> 5;
   const int gl = lane % L, E = a.E, K = a.K, e0 = gl * NI;
@@ -522,7 +693,7 @@ group_route_fast_kernel(const T* __restrict__ logits, const RouteArgs a) {
 #pragma unroll
     for (int i = N; i < NI; i += N) top_of<N>(key, key + i);
     // units of two keys that may stand the other way round
-    const uint32_t tol = SOFTMAX ? 8u + (uint32_t)(48.f * fminf(c, 1.f)) : 8u;
+    const uint32_t tol = pair_tolerance(SOFTMAX, c);
     bool sure = true;
     if (a.groups > 1) {
       uint32_t k1 = key[0], k2 = NI > 1 ? key[NI > 1 ? 1 : 0] : 0u;
@@ -611,9 +782,8 @@ group_route_fast_kernel(const T* __restrict__ logits, const RouteArgs a) {
       if constexpr (L == 32) again = 0;
       else again &= ~(((1u << L) - 1) << at);
       const int64_t tt = first + at / L;
-      float xe[kExact];
-      load_run<T, kExact>(logits + tt * a.stride, lane * kExact, E, false, xe);
-      const int e = choose_exact<kExact>(xe, lane, a);
+      const int e = resolve<T, kExact>(logits + tt * a.stride, lane, a, grid.size, grid.zero,
+                                       sm_list[warp]);
       const int got = __shfl_sync(0xffffffffu, e, gl);
       if ((lane & ~(L - 1)) == at && choice) {
         idx = got;
