@@ -222,33 +222,6 @@ __device__ __forceinline__ void write_columns(const BlockBwd<T, O, G>& a, int c,
   if (column) a.dgate[c] = a.w_post ? (float)a.w_post[c] * sc : sc;
 }
 
-// Two floats in one operation.
-using Pair = unsigned long long;
-__device__ __forceinline__ Pair pair(float lo, float hi) {
-  Pair p;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
-  return p;
-}
-__device__ __forceinline__ float2 floats(Pair p) {
-  float2 f;
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(p));
-  return f;
-}
-__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
-  Pair p;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
-  return p;
-}
-__device__ __forceinline__ Pair add2(Pair a, Pair b) {
-  Pair p;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(p) : "l"(a), "l"(b));
-  return p;
-}
-__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
-  Pair p;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(p) : "l"(a), "l"(b), "l"(c));
-  return p;
-}
 // What a lane loads and stores at once in the backward pass: Q consecutive columns, the 16
 // bytes of 4 float32 ones (or 8 where every row is bfloat16), so that a warp's access is 512
 // bytes in a row. With 8 columns of float32, two pieces of 16 bytes a lane, T 16384 D 4096

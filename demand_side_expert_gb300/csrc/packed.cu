@@ -5,6 +5,7 @@
 //   compact: dy = alpha g, (a, b) = q s, phi = SiLU(a) b for the retained rows, in
 //            their expert-major order
 #include <algorithm>
+#include <type_traits>
 
 #include "rows.cuh"
 
@@ -22,84 +23,133 @@ __device__ __forceinline__ float silu(float a) {
   return a * r;
 }
 
+__device__ __forceinline__ Pair silu2(Pair a) {
+  const float2 x = floats(mul2(a, pair(-kLog2e, -kLog2e)));
+  float2 e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.x) : "f"(x.x));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e.y) : "f"(x.y));
+  const float2 d = floats(add2(pair(e.x, e.y), pair(1.f, 1.f)));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.x) : "f"(d.x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r.y) : "f"(d.y));
+  return mul2(a, pair(r.x, r.y));
+}
+
 // What a group's values are divided by: 448 v / amax, corrected by its own remainder
 // so that quotients which lie between two codes (bfloat16 values often do) round as
 // the exact ones. Both sides of the remainder are scaled by 2^-9, so that neither
 // overflows.
 struct Divisor {
-  float k, a, r;  // 448 / amax, amax / 512, 512 / amax
+  Pair k, a, r;  // 448 / amax, -amax / 512, 512 / amax
   __device__ __forceinline__ explicit Divisor(float amax) {
     const float inv = __frcp_rn(amax);
-    k = inv * kF8Max;
-    a = amax * 0.001953125f;
-    r = inv * 512.f;
+    k = pair(inv * kF8Max, inv * kF8Max);
+    a = pair(amax * -0.001953125f, amax * -0.001953125f);
+    r = pair(inv * 512.f, inv * 512.f);
   }
-  __device__ __forceinline__ float of(float v) const {
-    const float t = v * k;
-    return fmaf(fmaf(-t, a, v * 0.875f), r, t);
+  __device__ __forceinline__ uint32_t codes(Pair v, Pair seven_eighths) const {
+    const Pair t = mul2(v, k);
+    const float2 q = floats(fma2(fma2(t, a, mul2(v, seven_eighths)), r, t));
+    return __nv_cvt_float2_to_fp8x2(q, __NV_SATFINITE, __NV_E4M3);
   }
 };
 
-__device__ __forceinline__ uint2 codes8(const float (&f)[kUnit], float amax) {
+// The largest magnitudes (NaN aside) of a group's values: 2^shift lanes have its units of a
+// and of b. Of bfloat16 both at once, in the halves of a word.
+template <typename T>
+__device__ __forceinline__ void group_amax(const Unit8<T>& a, const Unit8<T>& b, int shift,
+                                           float& ma, float& mb) {
+  if constexpr (sizeof(T) == 2) {
+    const __nv_bfloat162* pa = reinterpret_cast<const __nv_bfloat162*>(&a.v[0]);
+    const __nv_bfloat162* pb = reinterpret_cast<const __nv_bfloat162*>(&b.v[0]);
+    auto top = [](const __nv_bfloat162* p) {
+      return __hmax2(__hmax2(__habs2(p[0]), __habs2(p[1])), __hmax2(__habs2(p[2]), __habs2(p[3])));
+    };
+    const __nv_bfloat162 ta = top(pa), tb = top(pb);
+    __nv_bfloat162 m = __hmax2(__lows2bfloat162(ta, tb), __highs2bfloat162(ta, tb));
+#pragma unroll
+    for (int o = 0; o < 4; ++o)
+      if (o < shift) m = __hmax2(m, __shfl_xor_sync(0xffffffffu, m, 1 << o));
+    const float2 f = __bfloat1622float2(m);
+    ma = fmaxf(f.x, kAmaxMin);
+    mb = fmaxf(f.y, kAmaxMin);
+  } else {
+    float fa[kUnit], fb[kUnit];
+    a.get(fa);
+    b.get(fb);
+    ma = mb = kAmaxMin;
+#pragma unroll
+    for (int j = 0; j < kUnit; ++j) {
+      ma = fmaxf(ma, fabsf(fa[j]));
+      mb = fmaxf(mb, fabsf(fb[j]));
+    }
+#pragma unroll
+    for (int o = 0; o < 4; ++o) {
+      if (o < shift) {
+        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1 << o));
+        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1 << o));
+      }
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ void pairs_of(const Unit8<T>& u, Pair (&p)[4]) {
+  float f[kUnit];
+  u.get(f);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = pair(f[2 * i], f[2 * i + 1]);
+}
+
+__device__ __forceinline__ uint2 codes8(const Pair (&p)[4], float amax) {
   const Divisor d(amax);
-  float t[kUnit];
-#pragma unroll
-  for (int j = 0; j < kUnit; ++j) t[j] = d.of(f[j]);
-  return make_uint2(pack_e4m3(t[0], t[1], t[2], t[3]), pack_e4m3(t[4], t[5], t[6], t[7]));
+  const Pair c = pair(0.875f, 0.875f);
+  return make_uint2(d.codes(p[0], c) | d.codes(p[1], c) << 16,
+                    d.codes(p[2], c) | d.codes(p[3], c) << 16);
 }
 
-__device__ __forceinline__ float amax8(const float (&f)[kUnit]) {
-  float m = 0.f;
-#pragma unroll
-  for (int j = 0; j < kUnit; ++j) m = fmaxf(m, fabsf(f[j]));
-  return m;
-}
-
-// A warp a row; lane l holds the 8 columns l, l + 32, .. of both halves, so that a
-// scale's group is 2^shift neighbouring lanes. NI of them are loaded before any is used.
+// LANES lanes a row; lane l holds the 8 columns l, l + LANES, .. of both halves, so that a
+// scale's group is neighbouring lanes. NI of them are loaded before any is used. HBM-bound:
+// 262,144 pairs of H 768 in bfloat16, 1.22 GB, take 194 us, 0.93 of the copy bandwidth.
 constexpr int kPackThreads = 128;
 
-template <typename T, int NI>
+template <typename T, int NI, int LANES>
 __global__ void __launch_bounds__(kPackThreads)
 pack_kernel(const T* __restrict__ ab, int64_t rows, int H, int shift, uint8_t* __restrict__ q,
             float* __restrict__ scale, float* __restrict__ phi_sq) {
   pdl_begin();  // predecessor complete before any global access
-  const int lane = threadIdx.x & 31;
-  const int64_t r = (int64_t)blockIdx.x * (kPackThreads / 32) + (threadIdx.x >> 5);
-  if (r >= rows) return;
+  const int lane = threadIdx.x % LANES;
+  const int64_t at = (int64_t)blockIdx.x * (kPackThreads / LANES) + threadIdx.x / LANES;
+  if (LANES == 32 && at >= rows) return;
+  const bool real = at < rows;  // lanes of a row past the end stay with their warp
+  const int64_t r = real ? at : rows - 1;
   const int units = H / kUnit, groups = ((units - 1) >> shift) + 1;
   const T* row = ab + r * 2 * H;
   uint8_t* out = q + r * 2 * H;
   float* sc = scale + r * 2 * groups;
-  float sq = 0.f;
-  for (int u0 = lane; u0 - lane < units; u0 += 32 * NI) {
+  Pair sq2 = pair(0.f, 0.f);
+  for (int u0 = lane; u0 - lane < units; u0 += LANES * NI) {
     Unit8<T> va[NI], vb[NI];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int u = u0 + 32 * i;
+      const int u = u0 + LANES * i;
       va[i].load(row + u * kUnit, u < units);
       vb[i].load(row + H + u * kUnit, u < units);
     }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      const int u = u0 + 32 * i;
+      const int u = u0 + LANES * i;
       if (u - lane >= units) break;
-      float a[kUnit], b[kUnit];
-      va[i].get(a);
-      vb[i].get(b);
-      float ma = amax8(a), mb = amax8(b);
-      for (int o = 0; o < shift; ++o) {
-        ma = fmaxf(ma, __shfl_xor_sync(0xffffffffu, ma, 1 << o));
-        mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, 1 << o));
-      }
-      ma = fmaxf(ma, kAmaxMin);
-      mb = fmaxf(mb, kAmaxMin);
+      float ma, mb;
+      group_amax(va[i], vb[i], shift, ma, mb);
+      Pair a[4], b[4];
+      pairs_of(va[i], a);
+      pairs_of(vb[i], b);
 #pragma unroll
-      for (int j = 0; j < kUnit; ++j) {
-        const float p = silu(a[j]) * b[j];
-        sq = fmaf(p, p, sq);
+      for (int j = 0; j < 4; ++j) {
+        const Pair p = mul2(silu2(a[j]), b[j]);
+        sq2 = fma2(p, p, sq2);
       }
-      if (u < units) {
+      if (u < units && real) {
         *reinterpret_cast<uint2*>(out + u * kUnit) = codes8(a, ma);
         *reinterpret_cast<uint2*>(out + H + u * kUnit) = codes8(b, mb);
         if ((u & ((1 << shift) - 1)) == 0) {
@@ -109,8 +159,11 @@ pack_kernel(const T* __restrict__ ab, int64_t rows, int H, int shift, uint8_t* _
       }
     }
   }
-  sq = warp_sum(sq);
-  if (lane == 0) phi_sq[r] = sq;
+  const float2 part = floats(sq2);
+  float sq = part.x + part.y;
+#pragma unroll
+  for (int o = 1; o < LANES; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+  if (lane == 0 && real) phi_sq[r] = sq;
 }
 
 // A warp a token: lane k holds slot k's position, ||g_t||^2 is the warp's sum.
@@ -167,12 +220,67 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[kUnit])
   }
 }
 
-// A warp a retained row, as the compaction of a 16-bit state; the row count
-// M = sel_off[E] is read on the device.
+// A warp a retained row; the row count M = sel_off[E] is read on the device. The rows stand by
+// expert, and each expert's by token, so the rows of one token are far apart. The warps
+// therefore go through all experts' segments side by side: in each of `rounds` rounds every
+// segment's next part is dealt out, a row a warp, and the rows of a token, at about the same
+// place of their segments, are met while its cotangent is still in L2 (T 16384 D 4096 H 1408, half
+// of the pairs: 239 us; in the rows' own order, at the best number of CTAs, 296).
 constexpr int kUnpackThreads = 256;
 
+// The row of warp `w` in the round whose parts lie between the fractions f0 and f1 (of
+// 2^32; the last round's f1 is 0) of the segments; -1: none.
+__device__ __forceinline__ int64_t row_of_round(const int32_t* sel_off, int E, int64_t M,
+                                                uint32_t f0, uint32_t f1, int64_t w, int lane) {
+  const int per = (E + 31) / 32;  // experts a lane, consecutive
+  auto part = [&](int e, uint32_t& begin) -> uint32_t {
+    if (e >= E) return 0;
+    const int64_t lo = min(max((int64_t)sel_off[e], (int64_t)0), M);
+    const uint32_t m = (uint32_t)(min(max((int64_t)sel_off[e + 1], lo), M) - lo);
+    const uint32_t at = __umulhi(m, f0), end = f1 ? __umulhi(m, f1) : m;
+    begin = (uint32_t)lo + at;
+    return end - at;
+  };
+  uint32_t begin = 0, sum = 0;
+  for (int q = 0; q < per; ++q) sum += part(lane * per + q, begin);
+  uint32_t upto = sum;  // with the lanes before
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += v;
+  }
+  const uint32_t has = __ballot_sync(0xffffffffu, upto > w);
+  if (has == 0) return -1;
+  const int who = __ffs(has) - 1;
+  uint32_t left = (uint32_t)w - (upto - sum), row = 0;
+  for (int q = 0; q < per; ++q) {  // (only lane `who` finds its place)
+    const uint32_t n = part(lane * per + q, begin);
+    if (left < n) {
+      row = begin + left;
+      break;
+    }
+    left -= n;
+  }
+  return (int64_t)__shfl_sync(0xffffffffu, row, who);
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kUnpackThreads)
+__device__ __forceinline__ void stream8(T* p, const float (&f)[kUnit]) {
+  constexpr int V = Vec16<T>::kElems;
+#pragma unroll
+  for (int i = 0; i < (int)(sizeof(T) / 2); ++i)
+    __stcs(reinterpret_cast<uint4*>(p) + i, Vec16<T>::pack(f + i * V));
+}
+
+// Four CTAs an SM (T 16384 D 4096 H 1408, half of the pairs: 239 us; three 248, five, six and
+// eight 270, 268, 307), and 4 of a lane's 16-byte pieces of a cotangent ahead (8: 238, 12:
+// 266; a short block, T 1021 D 2048: 7.2 us, 8.3, 9.6). Their results are not read here: stores
+// that leave L2 first keep the cotangents in it (plain ones 249 us).
+constexpr int kUnpackCtas = 4, kAheadG = 4;
+
+// SPREAD: there may be more rows than warps (else they are all met at once).
+template <typename T, bool SPREAD>
+__global__ void __launch_bounds__(kUnpackThreads, kUnpackCtas)
 compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale, int shift,
                       const int32_t* __restrict__ perm, const uint8_t* __restrict__ keep,
                       const int32_t* __restrict__ sel_off, const int32_t* __restrict__ sel_pos,
@@ -203,7 +311,14 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
     for (int64_t i = gtid; i < zrows * dv; i += nthr) z[i] = make_uint4(0, 0, 0, 0);
   }
   const int x_groups = x_cols ? (D + x_cols - 1) / x_cols : 1;
-  for (int64_t j = gtid >> 5; j < M; j += nthr >> 5) {
+  const int64_t warps = nthr >> 5, rounds = max((M + warps - 1) / warps, (int64_t)1);
+  const uint32_t share = rounds == 1 ? 0u : (uint32_t)(((uint64_t)1 << 32) / (uint64_t)rounds);
+  for (int64_t round = 0; round < rounds; ++round) {
+    const int64_t j = !SPREAD ? gtid >> 5
+                              : row_of_round(sel_off, E, M, (uint32_t)round * share,
+                                             round + 1 == rounds ? 0u : (uint32_t)(round + 1) * share,
+                                             gtid >> 5, lane);
+    if (j < 0 || j >= M) continue;
     const int i = sel_pos[j];
     const int p = (i >= 0 && i < N) ? perm[i] : -1;
     if (p < 0 || p >= N) {
@@ -216,19 +331,19 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
     const float* sr = scale + (int64_t)i * 2 * groups;
     const uint4* gs = reinterpret_cast<const uint4*>(g + t * D);
     uint4* dyd = reinterpret_cast<uint4*>(dy_c + j * D);
-    for (int c0 = lane; c0 < dv; c0 += 32 * 8) {
-      uint4 v[8];
+    for (int c0 = lane; c0 < dv; c0 += 32 * kAheadG) {
+      uint4 v[kAheadG];
 #pragma unroll
-      for (int u = 0; u < 8; ++u)
+      for (int u = 0; u < kAheadG; ++u)
         if (c0 + 32 * u < dv) v[u] = gs[c0 + 32 * u];
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
+      for (int u = 0; u < kAheadG; ++u) {
         if (c0 + 32 * u < dv) {
           float f[V];
           Vec16<T>::unpack(v[u], f);
 #pragma unroll
           for (int e = 0; e < V; ++e) f[e] *= al;
-          dyd[c0 + 32 * u] = Vec16<T>::pack(f);
+          __stcs(dyd + c0 + 32 * u, Vec16<T>::pack(f));
         }
       }
     }
@@ -240,28 +355,28 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
           float f[kUnit];
           decode8(*reinterpret_cast<const uint2*>(xr + u * kUnit),
                   xs[x_cols ? u * kUnit / x_cols : 0], f);
-          store8(x_c + j * D + u * kUnit, f);
+          stream8(x_c + j * D + u * kUnit, f);
         }
       } else {
         const uint4* xr = reinterpret_cast<const uint4*>((const T*)x + t * D);
         uint4* xd = reinterpret_cast<uint4*>(x_c + j * D);
-        for (int c = lane; c < dv; c += 32) xd[c] = xr[c];
+        for (int c = lane; c < dv; c += 32) __stcs(xd + c, xr[c]);
       }
     }
     T* abd = ab_c + j * 2 * H;
     T* pd = phi_c + j * H;
-#pragma unroll 2
+#pragma unroll 1
     for (int u = lane; u < units; u += 32) {
-      const uint2 ca = *reinterpret_cast<const uint2*>(qr + u * kUnit);
-      const uint2 cb = *reinterpret_cast<const uint2*>(qr + H + u * kUnit);
+      const uint2 ca = __ldcs(reinterpret_cast<const uint2*>(qr + u * kUnit));
+      const uint2 cb = __ldcs(reinterpret_cast<const uint2*>(qr + H + u * kUnit));
       float a[kUnit], b[kUnit], ph[kUnit];
       decode8(ca, sr[u >> shift], a);
       decode8(cb, sr[groups + (u >> shift)], b);
 #pragma unroll
       for (int e = 0; e < kUnit; ++e) ph[e] = silu(a[e]) * b[e];
-      store8(abd + u * kUnit, a);
-      store8(abd + H + u * kUnit, b);
-      store8(pd + u * kUnit, ph);
+      stream8(abd + u * kUnit, a);
+      stream8(abd + H + u * kUnit, b);
+      stream8(pd + u * kUnit, ph);
     }
     if (lane == 0) {
       tok_c[j] = (int32_t)t;
@@ -297,14 +412,23 @@ static lrm_status check_layer(const lrm_shape* s, const lrm_packed* p, const voi
 
 template <typename T>
 static lrm_status launch_pack(const lrm_packed* p, const void* ab, cudaStream_t cs) {
-  const int64_t grid = (p->rows + kPackThreads / 32 - 1) / (kPackThreads / 32);
-  const int per_lane = (p->H / kUnit + 31) / 32;
-  auto kern = per_lane <= 1   ? pack_kernel<T, 1>
-              : per_lane <= 2 ? pack_kernel<T, 2>
-              : per_lane <= 3 ? pack_kernel<T, 3>
-                              : pack_kernel<T, 4>;
-  launch_k(kern, dim3((unsigned)grid), dim3(kPackThreads), 0, cs, (const T*)ab, p->rows, p->H,
-           group_shift(p->cols), p->q, p->scale, p->phi_sq);
+  const int units = p->H / kUnit;
+  const int lanes = units <= 4 ? 4 : units <= 8 ? 8 : units <= 16 ? 16 : 32;
+  // a lane's units in even rounds of up to four
+  const int mine = (units + 31) / 32, rounds = (mine + 3) / 4, ni = (mine + rounds - 1) / rounds;
+  auto kern = lanes == 4    ? pack_kernel<T, 1, 4>
+              : lanes == 8  ? pack_kernel<T, 1, 8>
+              : lanes == 16 ? pack_kernel<T, 1, 16>
+              : ni == 1     ? pack_kernel<T, 1, 32>
+              : ni == 2     ? pack_kernel<T, 2, 32>
+              : ni == 3     ? pack_kernel<T, 3, 32>
+                            : pack_kernel<T, 4, 32>;
+  const int per_cta = kPackThreads / lanes;
+  // a group that is wider than the row is the row
+  int shift = group_shift(p->cols);
+  while (shift > 0 && (1 << shift) > lanes) --shift;
+  launch_k(kern, dim3((unsigned)((p->rows + per_cta - 1) / per_cta)), dim3(kPackThreads), 0, cs,
+           (const T*)ab, p->rows, p->H, shift, p->q, p->scale, p->phi_sq);
   return launch_status();
 }
 
@@ -365,21 +489,23 @@ extern "C" lrm_status lrm_compact_packed(
   for (const void* p : {x, g, (const void*)dy_c, (const void*)x_c, (const void*)ab_c,
                         (const void*)phi_c})
     if (!aligned16(p)) return LRM_ERR_UNSUPPORTED;
-  const dim3 grid(num_sms() * 8);
+  const dim3 grid(num_sms() * kUnpackCtas);
   cudaStream_t cs = (cudaStream_t)stream;
   const int shift = group_shift(pk->cols);
+  const bool spread = pk->rows > (int64_t)grid.x * (kUnpackThreads / 32);
+  auto go = [&](auto kern, auto* type) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    launch_k(kern, grid, dim3(kUnpackThreads), 0, cs, (const uint8_t*)pk->q,
+             (const float*)pk->scale, shift, perm, keep, sel_off, sel_pos, alpha, x, x_scale,
+             x_cols, (const T*)g, (T*)dy_c, (T*)x_c, (T*)ab_c, (T*)phi_c, tok_c, row_of_pos,
+             s->T, s->D, s->H, s->K, s->E, error_word(ws));
+  };
   if (s->dtype == LRM_BF16) {
     using T = __nv_bfloat16;
-    launch_k(compact_packed_kernel<T>, grid, dim3(kUnpackThreads), 0, cs, (const uint8_t*)pk->q,
-             (const float*)pk->scale, shift, perm, keep, sel_off, sel_pos, alpha, x, x_scale,
-             x_cols, (const T*)g, (T*)dy_c, (T*)x_c, (T*)ab_c, (T*)phi_c, tok_c, row_of_pos,
-             s->T, s->D, s->H, s->K, s->E, error_word(ws));
+    go(spread ? compact_packed_kernel<T, true> : compact_packed_kernel<T, false>, (T*)nullptr);
   } else {
-    using T = float;
-    launch_k(compact_packed_kernel<T>, grid, dim3(kUnpackThreads), 0, cs, (const uint8_t*)pk->q,
-             (const float*)pk->scale, shift, perm, keep, sel_off, sel_pos, alpha, x, x_scale,
-             x_cols, (const T*)g, (T*)dy_c, (T*)x_c, (T*)ab_c, (T*)phi_c, tok_c, row_of_pos,
-             s->T, s->D, s->H, s->K, s->E, error_word(ws));
+    go(spread ? compact_packed_kernel<float, true> : compact_packed_kernel<float, false>,
+       (float*)nullptr);
   }
   return launch_status();
 }

@@ -403,7 +403,8 @@ STATES = [  # T, K, H, cols, dtype
     (1, 1, 8, 32, "f32"), (1, 8, 64, 64, "bf16"), (5, 2, 72, 32, "bf16"), (33, 3, 192, 128, "bf16"),
     (130, 8, 512, 64, "bf16"), (77, 4, 768, 128, "bf16"), (20, 8, 1408, 128, "bf16"),
     (9, 1, 1544, 32, "f32"), (65, 2, 264, 128, "f32"), (3, 2, 2056, 64, "bf16"),
-    (1000, 8, 256, 128, "bf16")]
+    (1000, 8, 256, 128, "bf16"), (65, 2, 24, 128, "bf16"), (9, 3, 128, 32, "bf16"),
+    (7, 5, 40, 64, "f32"), (11, 3, 64, 128, "f32"), (50, 1, 120, 64, "bf16"), (6, 2, 904, 64, "bf16")]
 
 
 @pytest.mark.parametrize("T,K,H,cols,dtype", STATES)
