@@ -1242,8 +1242,10 @@ group_route_many_kernel(const T* __restrict__ logits, const RouteArgs a) {
 
 // Gradient: the G lanes of a token write what every expert has (the balance loss), then
 // lane k adds what choice k has on top and writes that element again. kPer: choices a lane.
+// The row's exponentials are the hardware's (off by up to 7e-8 for each unit of a logit),
+// the choices' own are expf's.
 constexpr int kGroupBwdThreads = 256;
-template <typename T, int NI, int G, int kPer>
+template <typename T, int NI, int G, int kPer, bool SOFTMAX>
 __global__ void __launch_bounds__(kGroupBwdThreads)
 group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dlogits) {
   pdl_begin();  // predecessor complete before any global access
@@ -1279,12 +1281,14 @@ group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dl
                    (inv_n / (float)K);
 #pragma unroll
   for (int i = 0; i < NI; ++i) cost[i] *= kb;
+  const bool full = a.vec && E == NI * G;
   for (; first < a.ntok; first += step) {
     const bool real = first + lane / G < a.ntok;
     const int64_t t = real ? first + lane / G : first;
     const T* row = logits + t * a.stride;
     float x[NI];
-    load_row<T, NI, G>(row, gl, E, a.vec, x);
+    if (full) load_row<T, NI, G>(row, gl, NI * G, true, x);
+    else load_row<T, NI, G>(row, gl, E, a.vec, x);
     const bool masked = a.mask && a.mask[t] == 0;
     int idx[kPer];
     float da[kPer], xc[kPer];
@@ -1306,57 +1310,80 @@ group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dl
       }
     }
     read_choices(first + step + lane / G);
-    float top = -CUDART_INF_F;
-    bool some = false;
+    // x becomes the score over exp(m), d what its own derivative makes of it: s (1 - s) over
+    // exp(m), or the softmax's s
+    float d[NI], total = 0.f, cdot = 0.f, m = 0.f, inv = 0.f;
+    bool row_open = true;
+    if constexpr (SOFTMAX) {
+      float top = x[0];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      top = fmaxf(top, x[i]);
-      some |= x[i] != -CUDART_INF_F;
-    }
-    top = group_fmax<G>(top);
-    const uint32_t who = __ballot_sync(0xffffffffu, some);
-    const bool row_open =
-        (G == 32 ? who : who >> (lane & ~(G - 1)) & ((1u << (G & 31)) - 1)) != 0;
-    const bool use = row_open && !masked;
-    // f: the score over exp(m), less: 1 - s of the sigmoid
-    float less[NI], total = 0.f, cdot = 0.f;
-    const float m = a.softmax ? top : top > -CUDART_INF_F ? fminf(top, 0.f) : 0.f;
-    const float c = exp_grad<T>(a.softmax ? 0.f : m);
+      for (int i = 1; i < NI; ++i) top = fmaxf(top, x[i]);
+      top = group_fmax<G>(top);
+      m = top > -CUDART_INF_F ? top : 0.f;  // nothing open: exp(-inf) each
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-      const float xi = x[i];
-      if (a.softmax) {
-        x[i] = row_open ? exp_grad<T>(xi - m) : 0.f;
-        less[i] = 1.f;
-      } else {
-        const float u = exp_grad<T>(-fabsf(xi) - m), z = u * c, r = inverse_grad<T>(1.f + z);
-        x[i] = xi >= 0.f ? r : u * r;
-        less[i] = xi >= 0.f ? z * r : r;
+      for (int i = 0; i < NI; ++i) {
+        total += d[i] = exp_neg(x[i] - m);
+        cdot = fmaf(d[i], cost[i], cdot);
       }
-      total += x[i];
-      cdot = fmaf(x[i], cost[i], cdot);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x[i] * -1.4426950408889634f));
+        e = fminf(e, 1e38f);  // NaN too: seen by the sum below
+        const float s = rcp_fast(1.f + e);
+        total += x[i] != x[i] ? x[i] : s;
+        cdot = fmaf(s, cost[i], cdot);
+        d[i] = s * (e * s);
+      }
     }
     total = group_sum<G>(total);
-    const float inv = total == 0.f ? 0.f : inverse_grad<T>(total);
-    const float cmean = group_sum<G>(cdot) * inv;
+    cdot = group_sum<G>(cdot);
+    const bool lost = !(total >= 1e-30f);
+    if (__any_sync(0xffffffffu, lost)) {
+      // rows of very low logits, of nothing open, with NaN: over exp(m), m the largest logit
+      float top = x[0], sum = 0.f, dot = 0.f;
+#pragma unroll
+      for (int i = 1; i < NI; ++i) top = fmaxf(top, x[i]);
+      top = group_fmax<G>(top);
+      if (!SOFTMAX && lost) m = top > -CUDART_INF_F ? fminf(top, 0.f) : 0.f;
+      const float cm = exp_neg(m);
+      if constexpr (!SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          const float u = exp_neg(-fabsf(x[i]) - m), z = u * cm, r = rcp_fast(1.f + z);
+          const float f = x[i] >= 0.f ? r : u * r;
+          sum += f;
+          dot = fmaf(f, cost[i], dot);
+          if (lost) d[i] = f * (x[i] >= 0.f ? z * r : r);
+        }
+        sum = group_sum<G>(sum);
+        dot = group_sum<G>(dot);
+        if (lost) { total = sum; cdot = dot; }
+      }
+      row_open = total != 0.f;
+    }
+    const bool use = row_open && !masked;
+    inv = row_open ? __frcp_rn(total) : 0.f;
+    const float cmean = cdot * inv;
     // the choices' scores over exp(mc): their ratios are right however low they are
     float most = -CUDART_INF_F;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) most = fmaxf(most, xc[j]);
     most = group_fmax<G>(most);
     float mc = m;  // at most m, so that exp(mc - m) does not overflow
-    if (most > -CUDART_INF_F) mc = a.softmax ? most : fminf(most, 0.f);
+    if (most > -CUDART_INF_F) mc = SOFTMAX ? most : fminf(most, 0.f);
     float sc[kPer], lc[kPer], chosen = 0.f, adot = 0.f;
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const float xj = xc[j];
-      if (a.softmax) {
-        sc[j] = idx[j] >= 0 && xj > -CUDART_INF_F ? exp_grad<T>(xj - mc) : 0.f;
+      if constexpr (SOFTMAX) {
+        sc[j] = idx[j] >= 0 && xj > -CUDART_INF_F ? expf(xj - mc) : 0.f;
         if (xj != xj) sc[j] = xj;
         lc[j] = 1.f;
       } else {
-        const float z = exp_grad<T>(-fabsf(xj)), r = inverse_grad<T>(1.f + z);
-        sc[j] = xj >= 0.f ? r : exp_grad<T>(xj - mc) * r;
+        const float z = expf(-fabsf(xj)), r = __frcp_rn(1.f + z);
+        sc[j] = xj >= 0.f ? r : mc < 0.f ? expf(xj - mc) * r : z * r;
         lc[j] = xj >= 0.f ? z * r : r;
         if (idx[j] < 0) sc[j] = 0.f;
       }
@@ -1365,10 +1392,12 @@ group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dl
     }
     chosen = group_sum<G>(chosen);
     adot = group_sum<G>(adot);
-    const float back = a.softmax ? exp_grad<T>(mc - m) * inv : exp_grad<T>(mc);  // s = sc back
-    const float inv_c = chosen == 0.f ? 0.f : inverse_grad<T>(chosen);
-    const float mean = a.renorm ? adot * inv_c : a.softmax ? adot * back : 0.f;
-    const float common = -cmean - (a.softmax && !a.renorm ? mean : 0.f);
+    const float to_row = mc < m ? expf(mc - m) : 1.f;  // sc to_row inv: the choice's share
+    // s = sc back
+    const float back = SOFTMAX ? to_row * inv : mc < 0.f ? expf(mc) : 1.f;
+    const float inv_c = chosen == 0.f ? 0.f : __frcp_rn(chosen);
+    const float mean = a.renorm ? adot * inv_c : SOFTMAX ? adot * back : 0.f;
+    const float common = -cmean - (SOFTMAX && !a.renorm ? mean : 0.f);
     T* out = dlogits + t * E;
 #pragma unroll
     for (int q = 0; q < NI / S::kVec; ++q) {
@@ -1377,10 +1406,10 @@ group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dl
 #pragma unroll
       for (int i = 0; i < S::kVec; ++i) {
         const int s = q * S::kVec + i;
-        v[i] = (T)(use ? x[s] * inv * (cost[s] + common) * less[s] : 0.f);
+        v[i] = (T)(use ? d[s] * (inv * (cost[s] + common)) : 0.f);
       }
       if (real) {
-        if (a.out_vec && e + S::kVec <= E) {
+        if (full || (a.out_vec && e + S::kVec <= E)) {
           copy_bytes<S::kVec * (int)sizeof(T)>(out + e, v);
         } else {
 #pragma unroll
@@ -1393,8 +1422,7 @@ group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dl
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       if (idx[j] >= 0 && use && real) {
-        // share of the whole row: sc exp(mc - m) / total
-        const float share = sc[j] * exp_grad<T>(mc - m) * inv;
+        const float share = sc[j] * to_row * inv;
         const float base = share * (kb * (float)a.counts[idx[j]] + common);
         const float own = a.renorm ? sc[j] * inv_c * (da[j] - mean) : sc[j] * back * da[j];
         out[idx[j]] = (T)((base + own) * lc[j]);
@@ -1538,8 +1566,10 @@ static lrm_status launch_group_bwd(const void* logits, RouteBwdArgs a, void* dlo
       std::min<int64_t>(((int64_t)a.ntok + kTokens - 1) / kTokens, (int64_t)num_sms() * 8);
   a.vec = a.stride % RowShape<T, NI, G>::kVec == 0;
   a.out_vec = a.E % RowShape<T, NI, G>::kVec == 0;
-  launch_k(group_route_bwd_kernel<T, NI, G, kPer>, dim3((unsigned)blocks), dim3(kGroupBwdThreads),
-           0, cs, (const T*)logits, a, (T*)dlogits);
+  auto kern = a.softmax ? group_route_bwd_kernel<T, NI, G, kPer, true>
+                        : group_route_bwd_kernel<T, NI, G, kPer, false>;
+  launch_k(kern, dim3((unsigned)blocks), dim3(kGroupBwdThreads), 0, cs, (const T*)logits, a,
+           (T*)dlogits);
   return launch_status();
 }
 
