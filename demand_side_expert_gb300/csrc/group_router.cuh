@@ -1245,8 +1245,10 @@ group_route_many_kernel(const T* __restrict__ logits, const RouteArgs a) {
 // The row's exponentials are the hardware's (off by up to 7e-8 for each unit of a logit),
 // the choices' own are expf's.
 constexpr int kGroupBwdThreads = 256;
+// Four CTAs an SM are said outright for rows of 16 experts a lane (T 32768 E 256: 13.4 us, 17.7
+// with the two that the compiler's registers leave room for).
 template <typename T, int NI, int G, int kPer, bool SOFTMAX>
-__global__ void __launch_bounds__(kGroupBwdThreads)
+__global__ void __launch_bounds__(kGroupBwdThreads, NI == 16 && kPer == 1 ? 4 : 0)
 group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dlogits) {
   pdl_begin();  // predecessor complete before any global access
   using S = RowShape<T, NI, G>;
