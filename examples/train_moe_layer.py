@@ -1,6 +1,6 @@
 """Trains one pre-norm MoE block on a fixed random teacher, on one GPU.
 
-    python examples/train_moe_layer.py [--steps 60] [--rate 1/2] [--state f8]
+    python examples/train_moe_layer.py [--steps 60] [--rate 1/2] [--state f8] [--tight]
 
 Every step runs the whole chain of a training step with this package's kernels:
 
@@ -13,6 +13,13 @@ Every step runs the whole chain of a training step with this package's kernels:
   score, select, compact, expert backward                  .step (the retained pairs only)
   d u -> d x, d w                                          AddRMSNorm.backward
   all weights, norm and router among them                  AdamW
+
+With --tight, the block of a model that is short of memory (TightMoeBlock):
+
+  experts of the best groups, with a bias that evens the loads   GroupRouter
+  the saved state in 8 bits, one [a | b] buffer for all layers   PackedState, .forward, .step
+  norm of the experts' output, gate, scaled residual and the
+  norm in front of the next block                                BlockNorm
 """
 
 from __future__ import annotations
@@ -25,8 +32,8 @@ import torch
 
 sys.path.insert(0, os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
 
-from demand_side_expert_gb300 import (AddRMSNorm, AdamW, RecalibratedExpertBackward,  # noqa: E402
-                                      Router)
+from demand_side_expert_gb300 import (AddRMSNorm, AdamW, BlockNorm, GroupRouter,  # noqa: E402
+                                      PackedState, RecalibratedExpertBackward, Router)
 
 
 def init_weights(D: int, H: int, E: int, seed: int, device="cuda") -> dict:
@@ -81,14 +88,76 @@ class MoeBlock:
         return self.norm.dx
 
 
+class TightMoeBlock:
+    """y = RMS norm(h'), h' = scale * h + gate * RMS norm(MoE(RMS norm(h))), h = x + residual:
+    norms on both sides of the experts. What is kept from forward to backward is u, h' and 8-bit
+    rows of [a | b]. Weights beside ``init_weights``'s: "post", "next" and "layer_scale" [D];
+    ``bias`` [E] float32 is moved by the loads, not by a gradient."""
+
+    SCALE = 0.8  # of the residual
+
+    def __init__(self, T, D, H, E, K, weights: dict, groups=4, top_groups=2, balance_coef=0.001,
+                 packed=True):
+        self.w = weights
+        self.norm = AddRMSNorm(T, D, "bf16")
+        self.router = GroupRouter(T, E, K, "bf16", groups=groups, top_groups=top_groups,
+                                  balance_coef=balance_coef)
+        self.experts = ex = RecalibratedExpertBackward(T, D, H, E, K, "bf16")
+        self.state = PackedState(T, K, H, "bf16", cols=64) if packed else None
+        self.after = BlockNorm(T, D, "bf16", gate="column", residual_scale=self.SCALE)
+        self.bias = torch.zeros(E, device="cuda")
+        self.grads = {"norm": self.norm.dw, "router": torch.empty(D, E, device="cuda"),
+                      "gate": ex.dw_gate, "up": ex.dw_up, "down": ex.dw_down,
+                      "post": self.after.dw_post, "next": self.after.dw,
+                      "layer_scale": self.after.dgate}
+
+    def forward(self, x, residual):
+        w, ex, r = self.w, self.experts, self.router
+        self.norm.forward(x, w["norm"], residual=residual)
+        self.logits = self.norm.y @ w["router"]
+        r.route(self.logits, bias=self.bias)
+        ex.forward(r.topk_idx, r.alpha, self.norm.y, w["gate"], w["up"], w["down"],
+                   packed=self.state)
+        self.after.forward(ex.out, self.norm.h, w["next"], w_post=w["post"], gate=w["layer_scale"])
+        return self.after.y.float()
+
+    def even_loads(self, rate=1e-3):
+        self.router.next_bias(self.bias, rate, out=self.bias)
+
+    def backward(self, g, rate=(1, 1)):
+        """g [T, D] float32: the cotangent of forward's result. Leaves the weights'
+        gradients in ``grads`` and returns the one of x (and of the residual)."""
+        w, ex, r, n = self.w, self.experts, self.router, self.after
+        n.backward(g, ex.out, w["next"], w["post"], w["layer_scale"])
+        r.backward(self.logits, ex.gate_grad(n.dblock))
+        u = self.norm.y
+        saved = (ex.ab, ex.phi) if self.state is None else (self.state, None)
+        ex.step(r.topk_idx, r.alpha, u, n.dblock, *saved, w["gate"], w["up"], w["down"],
+                rate=rate, gathered=True)
+        self.grads["router"].copy_(u.t() @ r.dlogits)
+        du = ex.dx + (r.dlogits @ w["router"].t()).float()
+        self.norm.backward(du, w["norm"], dh=n.dres)
+        return self.norm.dx
+
+
+def tight_weights(D: int, H: int, E: int, seed: int, device="cuda") -> dict:
+    w = init_weights(D, H, E, seed, device)
+    for name in ("post", "next"):
+        w[name] = torch.ones(D, dtype=torch.bfloat16, device=device)
+    w["layer_scale"] = torch.full((D,), 0.5, dtype=torch.bfloat16, device=device)
+    return w
+
+
 def train(steps=60, T=2048, D=256, H=128, E=16, K=2, rate=(1, 2), state="f32", lr=2e-3, seed=0,
-          log=None) -> list:
+          log=None, tight=False) -> list:
     """The loss of every step."""
-    teacher = MoeBlock(T, D, H, E, K, init_weights(D, H, E, seed + 1))
-    block = MoeBlock(T, D, H, E, K, init_weights(D, H, E, seed + 2))
+    make, weights = (TightMoeBlock, tight_weights) if tight else (MoeBlock, init_weights)
+    teacher = make(T, D, H, E, K, weights(D, H, E, seed + 1))
+    block = make(T, D, H, E, K, weights(D, H, E, seed + 2))
     names = list(block.w)
     opt = AdamW([block.w[n] for n in names], [block.grads[n] for n in names], lr=lr,
-                betas=(0.9, 0.95), weight_decay=[0.0 if n == "norm" else 0.01 for n in names],
+                betas=(0.9, 0.95),
+                weight_decay=[0.0 if block.w[n].dim() == 1 else 0.01 for n in names],
                 state=state, master=True)
     gen = torch.Generator(device="cuda")
     gen.manual_seed(seed)
@@ -102,6 +171,8 @@ def train(steps=60, T=2048, D=256, H=128, E=16, K=2, rate=(1, 2), state="f32", l
         losses.append(loss.clone())
         block.backward(diff / diff.numel(), rate=rate)
         opt.step()
+        if tight:
+            block.even_loads()
         if log and (i % log == 0 or i == steps - 1):
             print(f"step {i:4d}  loss {loss.item():.5f}  balance {block.router.loss[0].item():.5f}"
                   f"  largest share {block.router.counts.max().item() / (T * K):.3f}")
@@ -115,6 +186,7 @@ if __name__ == "__main__":
     ap.add_argument("--steps", type=int, default=60)
     ap.add_argument("--rate", default="1/2", help="retention rate of the expert backward")
     ap.add_argument("--state", choices=("f32", "f8"), default="f32", help="AdamW's moments")
+    ap.add_argument("--tight", action="store_true", help="the block that saves memory")
     a = ap.parse_args()
     num, den = (int(v) for v in a.rate.split("/"))
-    train(a.steps, rate=(num, den), state=a.state, log=10)
+    train(a.steps, rate=(num, den), state=a.state, log=10, tight=a.tight)
