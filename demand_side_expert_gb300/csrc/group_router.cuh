@@ -1189,7 +1189,8 @@ group_route_many_kernel(const T* __restrict__ logits, const RouteArgs a) {
     } else {
 #pragma unroll
       for (int i = 0; i < kEach; ++i) {
-        w[i] = __frcp_rn(1.f + expf(-xk[i]));
+        const float e = expf(-fabsf(xk[i])), r = __frcp_rn(1.f + e);
+        w[i] = xk[i] >= 0.f ? r : e * r;
         sum += w[i];
       }
     }

@@ -228,10 +228,12 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[kUnit])
 // of the pairs: 239 us; in the rows' own order, at the best number of CTAs, 296).
 constexpr int kUnpackThreads = 256;
 
-// The row of warp `w` in the round whose parts lie between the fractions f0 and f1 (of
-// 2^32; the last round's f1 is 0) of the segments; -1: none.
+// The w-th row of the round whose parts lie between the fractions f0 and f1 (of 2^32; the
+// last round's f1 is 0) of the segments, -1: none; and the round's rows. (Each part is
+// rounded to whole rows, so a round may hold some more than its share.)
 __device__ __forceinline__ int64_t row_of_round(const int32_t* sel_off, int E, int64_t M,
-                                                uint32_t f0, uint32_t f1, int64_t w, int lane) {
+                                                uint32_t f0, uint32_t f1, int64_t w, int lane,
+                                                int64_t& total) {
   const int per = (E + 31) / 32;  // experts a lane, consecutive
   auto part = [&](int e, uint32_t& begin) -> uint32_t {
     if (e >= E) return 0;
@@ -249,6 +251,7 @@ __device__ __forceinline__ int64_t row_of_round(const int32_t* sel_off, int E, i
     const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
+  total = __shfl_sync(0xffffffffu, upto, 31);
   const uint32_t has = __ballot_sync(0xffffffffu, upto > w);
   if (has == 0) return -1;
   const int who = __ffs(has) - 1;
@@ -311,13 +314,22 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
     for (int64_t i = gtid; i < zrows * dv; i += nthr) z[i] = make_uint4(0, 0, 0, 0);
   }
   const int x_groups = x_cols ? (D + x_cols - 1) / x_cols : 1;
-  const int64_t warps = nthr >> 5, rounds = max((M + warps - 1) / warps, (int64_t)1);
+  const int64_t warps = nthr >> 5,
+                rounds = SPREAD ? max((M + warps - 1) / warps, (int64_t)1) : 1;
   const uint32_t share = rounds == 1 ? 0u : (uint32_t)(((uint64_t)1 << 32) / (uint64_t)rounds);
-  for (int64_t round = 0; round < rounds; ++round) {
-    const int64_t j = !SPREAD ? gtid >> 5
-                              : row_of_round(sel_off, E, M, (uint32_t)round * share,
-                                             round + 1 == rounds ? 0u : (uint32_t)(round + 1) * share,
-                                             gtid >> 5, lane);
+  int64_t w = gtid >> 5, total = M;
+  for (int64_t round = 0; round < rounds;) {
+    const int64_t j =
+        !SPREAD ? w
+                : row_of_round(sel_off, E, M, (uint32_t)round * share,
+                               round + 1 == rounds ? 0u : (uint32_t)(round + 1) * share, w, lane,
+                               total);
+    // the warp's next row, of this round or of the next one
+    w += warps;
+    if (w >= total) {
+      w = gtid >> 5;
+      ++round;
+    }
     if (j < 0 || j >= M) continue;
     const int i = sel_pos[j];
     const int p = (i >= 0 && i < N) ? perm[i] : -1;

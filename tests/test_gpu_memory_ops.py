@@ -300,6 +300,43 @@ def test_router_strides_and_mask_types(dev):
         assert torch.equal(getattr(a, name), getattr(b, name)), name
 
 
+@pytest.mark.parametrize("E,groups", [(256, 8), (128, 4), (64, 4), (200, 5)])
+def test_router_strided_rows_of_many_tokens(dev, E, groups):
+    """Odd strides and offsets where tokens share warps: the contiguous rows' bits."""
+    T, K = 17001, 8
+    wide = make_logits(T, E + 9, "f32", E).to(dev)
+    x = wide[:, 4:4 + E]
+    bias = make_bias(E, "steps").to(dev)
+    a, b = (router(T, E, K, "f32", groups=groups, top_groups=2, balance_coef=0.1)
+            for _ in range(2))
+    for r, v in ((a, x), (b, x.contiguous())):
+        r.route(v, bias=bias)
+        r.backward(v, r.alpha)
+    for name in ("topk_idx", "alpha", "counts", "prob_sum", "loss", "dlogits"):
+        assert torch.equal(getattr(a, name), getattr(b, name)), name
+
+
+def test_router_weights_do_not_depend_on_the_block(dev):
+    """The same tokens alone, among a few and among many (three kernels): the same choices,
+    weights to the last bits, also where scores are below float32's normal numbers."""
+    E, K = 256, 8
+    for renorm in (False, True):
+        for kind in ("normal", "low"):
+            x = make_logits(20000, E, "f32", 2, kind=kind).to(dev)
+            bias = make_bias(E, "steps").to(dev)
+            got = []
+            for T in (20000, 5000, 200, 1):
+                r = router(T, E, K, "f32", groups=8, top_groups=4, renorm=renorm)
+                r.route(x[:T], bias=bias, stats=False)
+                got.append(r)
+            for r in got[1:]:
+                n = r.T
+                assert torch.equal(r.topk_idx, got[0].topk_idx[:n])
+                a, b = to64(r.alpha), to64(got[0].alpha[:n])
+                # a dozen roundings, or two steps of the smallest number
+                close(a, b, 32 * U * np.abs(b) + 2 ** -147.0, "alpha")
+
+
 def test_bias_steps_even_the_loads(dev):
     """The step is the formula's, bit for bit, in place as well; many of them even out
     what the experts get."""
@@ -543,6 +580,42 @@ def test_step_from_packed_state(dev, T, D, H, E, K, dtype, rate, x8):
         for a, n in zip(first, ("dw_gate", "dw_up", "dw_down", "dx")):
             assert torch.equal(a, getattr(pipe, n)), n
         assert (pipe.x_c == fill).all()
+
+
+@pytest.mark.parametrize("rounds,more", [(1, 0), (1, 1), (2, -1), (2, 0), (3, 0), (3, 7)])
+def test_packed_rows_of_many_experts(dev, rounds, more):
+    """As many retained rows as the kernel's warps take in whole rounds, a few more or less,
+    from many experts of uneven size: every row comes out, whatever its round."""
+    from demand_side_expert_gb300 import PackedState, RecalibratedExpertBackward
+
+    warps = torch.cuda.get_device_properties(dev).multi_processor_count * 32
+    N, D, H, E = rounds * warps + more, 16, 8, 251
+    gen = torch.Generator().manual_seed(rounds)
+    ids = (torch.rand(N, 1, generator=gen) ** 2 * E).to(torch.int32).clamp_(max=E - 1)
+    pipe = RecalibratedExpertBackward(N, D, H, E, 1, "f32", dev)
+    pipe.dispatch(ids.to(dev))
+    state = PackedState(N, 1, H, "f32", cols=32)
+    state.pack(torch.randn(N, 2 * H, generator=gen).to(dev))
+    alpha = torch.rand(N, 1, generator=gen).to(dev)
+    g, x = torch.randn(N, D, generator=gen).to(dev), torch.randn(N, D, generator=gen).to(dev)
+    pipe.score_pairs(alpha, g, state)
+    for rate in ((1, 1), (2, 3)):
+        pipe.select_rate(*rate)
+        for t in (pipe.dy_c, pipe.x_c, pipe.ab_c, pipe.phi_c):
+            t.fill_(math.nan)
+        pipe.tok_c.fill_(-5)
+        pipe.compact(alpha, x, g, state, None)
+        assert pipe.device_error() == 0
+        M = pipe.retained_rows
+        pos = pipe.sel_pos[:M].long()
+        pair = pipe.perm[pos].long()
+        assert torch.equal(pipe.tok_c[:M].long(), pair)
+        assert torch.equal(pipe.row_of_pos[pos].long(), torch.arange(M, device=dev))
+        assert torch.equal(pipe.x_c[:M], x[pair])
+        assert torch.equal(pipe.dy_c[:M], alpha[pair] * g[pair])
+        wide = state.scale.repeat_interleave(H, 1)
+        assert torch.equal(pipe.ab_c[:M], (state.q.float() * wide)[pos])
+        assert torch.isfinite(pipe.phi_c[:M]).all()
 
 
 def test_forward_packs_its_state(dev):
