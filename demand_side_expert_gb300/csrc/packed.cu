@@ -228,12 +228,11 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[kUnit])
 // of the pairs: 239 us; in the rows' own order, at the best number of CTAs, 296).
 constexpr int kUnpackThreads = 256;
 
-// The w-th row of the round whose parts lie between the fractions f0 and f1 (of 2^32; the
-// last round's f1 is 0) of the segments, -1: none; and the round's rows. (Each part is
-// rounded to whole rows, so a round may hold some more than its share.)
+// The row of warp `w` in the round whose parts lie between the fractions f0 and f1 (of
+// 2^32; the last round's f1 is 0) of the segments; -1: none. Each part is rounded to whole
+// rows, so a round holds up to E more than its share.
 __device__ __forceinline__ int64_t row_of_round(const int32_t* sel_off, int E, int64_t M,
-                                                uint32_t f0, uint32_t f1, int64_t w, int lane,
-                                                int64_t& total) {
+                                                uint32_t f0, uint32_t f1, int64_t w, int lane) {
   const int per = (E + 31) / 32;  // experts a lane, consecutive
   auto part = [&](int e, uint32_t& begin) -> uint32_t {
     if (e >= E) return 0;
@@ -251,7 +250,6 @@ __device__ __forceinline__ int64_t row_of_round(const int32_t* sel_off, int E, i
     const uint32_t v = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += v;
   }
-  total = __shfl_sync(0xffffffffu, upto, 31);
   const uint32_t has = __ballot_sync(0xffffffffu, upto > w);
   if (has == 0) return -1;
   const int who = __ffs(has) - 1;
@@ -281,7 +279,8 @@ __device__ __forceinline__ void stream8(T* p, const float (&f)[kUnit]) {
 // that leave L2 first keep the cotangents in it (plain ones 249 us).
 constexpr int kUnpackCtas = 4, kAheadG = 4;
 
-// SPREAD: there may be more rows than warps (else they are all met at once).
+// SPREAD: there may be more rows than warps (else they are all met at once), and many more
+// warps than experts. A round's rows are then no more than the warps.
 template <typename T, bool SPREAD>
 __global__ void __launch_bounds__(kUnpackThreads, kUnpackCtas)
 compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale, int shift,
@@ -314,22 +313,16 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
     for (int64_t i = gtid; i < zrows * dv; i += nthr) z[i] = make_uint4(0, 0, 0, 0);
   }
   const int x_groups = x_cols ? (D + x_cols - 1) / x_cols : 1;
-  const int64_t warps = nthr >> 5,
-                rounds = SPREAD ? max((M + warps - 1) / warps, (int64_t)1) : 1;
-  const uint32_t share = rounds == 1 ? 0u : (uint32_t)(((uint64_t)1 << 32) / (uint64_t)rounds);
-  int64_t w = gtid >> 5, total = M;
-  for (int64_t round = 0; round < rounds;) {
+  // a fraction is off by up to 8 of 2^32, which is 4 rows of the most that there can be
+  const int64_t warps = nthr >> 5, deal = SPREAD ? warps - E - 8 : warps;
+  const int64_t rounds = (M + deal - 1) / deal;
+  const uint64_t share = rounds ? ((uint64_t)1 << 48) / (uint64_t)rounds : 0;  // 48 bits
+  auto fraction = [&](int64_t r) { return (uint32_t)((uint64_t)r * share >> 16); };
+  for (int64_t round = 0; round < rounds; ++round) {
     const int64_t j =
-        !SPREAD ? w
-                : row_of_round(sel_off, E, M, (uint32_t)round * share,
-                               round + 1 == rounds ? 0u : (uint32_t)(round + 1) * share, w, lane,
-                               total);
-    // the warp's next row, of this round or of the next one
-    w += warps;
-    if (w >= total) {
-      w = gtid >> 5;
-      ++round;
-    }
+        SPREAD ? row_of_round(sel_off, E, M, fraction(round),
+                              round + 1 == rounds ? 0u : fraction(round + 1), gtid >> 5, lane)
+               : round * warps + (gtid >> 5);
     if (j < 0 || j >= M) continue;
     const int i = sel_pos[j];
     const int p = (i >= 0 && i < N) ? perm[i] : -1;
@@ -504,7 +497,8 @@ extern "C" lrm_status lrm_compact_packed(
   const dim3 grid(num_sms() * kUnpackCtas);
   cudaStream_t cs = (cudaStream_t)stream;
   const int shift = group_shift(pk->cols);
-  const bool spread = pk->rows > (int64_t)grid.x * (kUnpackThreads / 32);
+  const int64_t warps = (int64_t)grid.x * (kUnpackThreads / 32);
+  const bool spread = pk->rows > warps && warps > 2 * (int64_t)s->E + 16;
   auto go = [&](auto kern, auto* type) {
     using T = std::remove_pointer_t<decltype(type)>;
     launch_k(kern, grid, dim3(kUnpackThreads), 0, cs, (const uint8_t*)pk->q,
