@@ -11,6 +11,13 @@
 // in the other order. Every key's error has a bound, so the kernel knows which tokens
 // it cannot decide, and does those again in 64 bits. Keys of equal logits and equal
 // biases are equal in any arithmetic and go by their ids.
+//
+// The logits are read once and little is written (T 32768 E 256 float32: 36 MB, 5.3 us of
+// copy bandwidth); what bounds the kernels is the instructions of a token, about half of
+// them minima and maxima (sorting, merging), and at few warps their latency. T 32768 E 256
+// K 8, 4 of 8 groups, with statistics: 32 us, of which 2 to 3 are the statistics' second
+// kernel and about 8 the tokens done again in 64 bits (24.8 with the doubts left as they
+// are); the gradient 13.4 us.
 #pragma once
 
 #include <algorithm>
@@ -591,7 +598,8 @@ group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
 // 32-bit minima and maxima find the choices and equal ones go by their ids. Every lane
 // sorts its keys, the two largest of a group's lanes rank the groups, the others' keys
 // are dropped, and the token's lanes merge their lists of 8 pairwise. Choices that stand
-// further apart than both keys' errors are sure.
+// further apart than both keys' errors are sure. Bound by one token's chain: few warps an
+// SM have work (T 5003 E 128, padded, with statistics: 11 us; T 1000 E 256 6.8).
 constexpr int kTopK = 8;
 constexpr int fast_route_threads(int l) { return l == 32 ? 512 : 768; }
 
@@ -1445,13 +1453,15 @@ static lrm_status launch_route_kernel(void (*kern)(const T*, RouteArgs), const v
   int64_t grid;
   if (stats) {
     // one CTA an SM at most (each leaves a row for the last sums), its warps in even
-    // rounds; tokens that fit one CTA stay in one, without that second launch
+    // rounds; tokens that fit one CTA stay in one, without that second launch. Eight warps
+    // at least: T 1000 E 256 takes 6.8 us, 7.9 with 16 and 6.9 with 4 (T 8192 16.7, 18.8,
+    // 17.1)
     const int64_t ctas = std::min(num_sms(), kRouterMaxCtas);
     const int64_t rounds = (warps + ctas * max_warps - 1) / (ctas * max_warps);
     const int64_t need = (warps + rounds - 1) / rounds;
     nwarp = (int)(need <= max_warps
                       ? need
-                      : std::max<int64_t>(std::min(16, max_warps), (need + ctas - 1) / ctas));
+                      : std::max<int64_t>(std::min(8, max_warps), (need + ctas - 1) / ctas));
     grid = (need + nwarp - 1) / nwarp;
   } else {
     nwarp = (int)std::min<int64_t>(4, warps);  // a warp for each scheduler of an SM
@@ -1535,7 +1545,7 @@ lrm_status pick_group_route(const void* logits, const RouteArgs& a, cudaStream_t
     const int shared_ni = cap == 32 ? 4 : cap == 64 ? 8 : 16;
     if (many && whole_lanes(a, shared_ni)) {
       // From 800 lanes of tokens an SM on the lists are merged across tokens (E 256, 16 lanes a
-      // token, us: T 5003 18.9 against 15.4, T 8192 17.9 | 19.1, T 16384 20.4 | 25.4, T 32768
+      // token, us: T 5003 18.9 against 15.4, T 8192 16.7 | 19.1, T 16384 20.7 | 25.4, T 32768
       // 32.3 | 37.0; E 128, 8 lanes, T 32768 18.2 | 20.8). Lists of few experts a lane gain
       // nothing (E 64 T 32768 19.1 | 18.7).
       const bool most = (int64_t)a.ntok * (cap / 16) >= (int64_t)num_sms() * 800;
