@@ -225,7 +225,8 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[kUnit])
 // therefore go through all experts' segments side by side: in each of `rounds` rounds every
 // segment's next part is dealt out, a row a warp, and the rows of a token, at about the same
 // place of their segments, are met while its cotangent is still in L2 (T 16384 D 4096 H 1408, half
-// of the pairs: 239 us; in the rows' own order, at the best number of CTAs, 296).
+// of the pairs, 1.28 GB: 241 us; in the rows' own order, at the best number of CTAs, 296).
+// Bound by HBM: of the cotangents, what L2 did not keep is read again.
 constexpr int kUnpackThreads = 256;
 
 // The row of warp `w` in the round whose parts lie between the fractions f0 and f1 (of
@@ -273,8 +274,8 @@ __device__ __forceinline__ void stream8(T* p, const float (&f)[kUnit]) {
     __stcs(reinterpret_cast<uint4*>(p) + i, Vec16<T>::pack(f + i * V));
 }
 
-// Four CTAs an SM (T 16384 D 4096 H 1408, half of the pairs: 239 us; three 248, five, six and
-// eight 270, 268, 307), and 4 of a lane's 16-byte pieces of a cotangent ahead (8: 238, 12:
+// Four CTAs an SM (T 16384 D 4096 H 1408, half of the pairs: 241 us; three 248, five, six and
+// eight 270, 268, 307), and 4 of a lane's 16-byte pieces of a cotangent ahead (8: as long, 12:
 // 266; a short block, T 1021 D 2048: 7.2 us, 8.3, 9.6). Their results are not read here: stores
 // that leave L2 first keep the cotangents in it (plain ones 249 us).
 constexpr int kUnpackCtas = 4, kAheadG = 4;
