@@ -166,27 +166,32 @@ pack_kernel(const T* __restrict__ ab, int64_t rows, int H, int shift, uint8_t* _
   if (lane == 0 && real) phi_sq[r] = sq;
 }
 
-// A warp a token: lane k holds slot k's position, ||g_t||^2 is the warp's sum.
+// LANES lanes a token: lane k holds slot k's position, ||g_t||^2 is their sum. HBM-bound for wide
+// rows (T 16384 D 4096: 21.5 us, 0.92 of the copy bandwidth); a token of a narrow row costs a
+// lane the same instructions, so fewer lanes have it (T 29084 bfloat16, us with 8 | 16 | 32: D 80
+// 4.6 | 6.7 | 11.3, D 512 7.2 | 8.2 | 12.3, D 1024 13.3 | 13.3 | 14.9; T 300 D 512 3.6 | 2.8 | 2.6).
 constexpr int kScoreWarps = 4;
 
-template <typename T>
+template <typename T, int LANES>
 __global__ void __launch_bounds__(32 * kScoreWarps)
 score_packed_kernel(const T* __restrict__ g, const float* __restrict__ phi_sq,
                     const float* __restrict__ alpha, const int32_t* __restrict__ inv,
                     float* __restrict__ score, int ntok, int D, int K, int32_t* err) {
   pdl_begin();  // predecessor complete before any global access
   constexpr int V = Vec16<T>::kElems, kAhead = 8;
-  const int lane = threadIdx.x & 31;
-  const int64_t t = (int64_t)blockIdx.x * kScoreWarps + (threadIdx.x >> 5);
-  if (t >= ntok) return;
+  const int lane = threadIdx.x & (LANES - 1);
+  const int64_t t = (int64_t)blockIdx.x * (32 * kScoreWarps / LANES) + threadIdx.x / LANES;
+  if (LANES == 32 && t >= ntok) return;
+  const bool real = LANES == 32 || t < ntok;
   const int64_t N = (int64_t)ntok * K;
   const int chunks = D / V;
   const T* row = g + t * D;
   float s = 0.f;
-  for (int c0 = lane; c0 - lane < chunks; c0 += 32 * kAhead) {
+  for (int c0 = lane; c0 - lane < chunks; c0 += LANES * kAhead) {
     uint4 v[kAhead];
 #pragma unroll
-    for (int i = 0; i < kAhead; ++i) v[i] = load_if(row + (c0 + 32 * i) * V, c0 + 32 * i < chunks);
+    for (int i = 0; i < kAhead; ++i)
+      v[i] = load_if(row + (c0 + LANES * i) * V, real && c0 + LANES * i < chunks);
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
       float f[V];
@@ -195,8 +200,10 @@ score_packed_kernel(const T* __restrict__ g, const float* __restrict__ phi_sq,
       for (int j = 0; j < V; ++j) s = fmaf(f[j], f[j], s);
     }
   }
-  s = warp_sum(s);
-  for (int k = lane; k < K; k += 32) {
+#pragma unroll
+  for (int o = LANES / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (!real) return;
+  for (int k = lane; k < K; k += LANES) {
     const int pos = inv[t * K + k];
     if (pos >= 0 && pos < N) {
       const float a = alpha[t * K + k];
@@ -220,13 +227,14 @@ __device__ __forceinline__ void decode8(uint2 c, float scale, float (&f)[kUnit])
   }
 }
 
-// A warp a retained row; the row count M = sel_off[E] is read on the device. The rows stand by
-// expert, and each expert's by token, so the rows of one token are far apart. The warps
-// therefore go through all experts' segments side by side: in each of `rounds` rounds every
-// segment's next part is dealt out, a row a warp, and the rows of a token, at about the same
-// place of their segments, are met while its cotangent is still in L2 (T 16384 D 4096 H 1408, half
-// of the pairs, 1.28 GB: 241 us; in the rows' own order, at the best number of CTAs, 296).
-// Bound by HBM: of the cotangents, what L2 did not keep is read again.
+// LANES lanes a retained row; the row count M = sel_off[E] is read on the device. The rows stand by
+// expert, and each expert's by token, so the rows of one token are far apart. Where L2 does not
+// hold the cotangents (SPREAD, a warp a row) the warps therefore go through all experts'
+// segments side by side: in each of `rounds` rounds every segment's next part is dealt out,
+// and the rows of a token, at about the same place of their segments, are met while its
+// cotangent is still in L2 (T 16384 D 4096 H 1408, half of the pairs, 1.28 GB: 241 us; in the
+// rows' own order, at the best number of CTAs, 296). Bound by HBM: of the cotangents, what L2
+// did not keep is read again.
 constexpr int kUnpackThreads = 256;
 
 // The row of warp `w` in the round whose parts lie between the fractions f0 and f1 (of
@@ -276,13 +284,13 @@ __device__ __forceinline__ void stream8(T* p, const float (&f)[kUnit]) {
 
 // Four CTAs an SM (T 16384 D 4096 H 1408, half of the pairs: 241 us; three 248, five, six and
 // eight 270, 268, 307), and 4 of a lane's 16-byte pieces of a cotangent ahead (8: as long, 12:
-// 266; a short block, T 1021 D 2048: 7.2 us, 8.3, 9.6). Their results are not read here: stores
+// 266; a short block, T 1021 D 2048: 1.1 and 2.4 us longer). Their results are not read here: stores
 // that leave L2 first keep the cotangents in it (plain ones 249 us).
 constexpr int kUnpackCtas = 4, kAheadG = 4;
 
 // SPREAD: there may be more rows than warps (else they are all met at once), and many more
-// warps than experts. A round's rows are then no more than the warps.
-template <typename T, bool SPREAD>
+// warps than experts. A round's rows are then no more than the warps. Wants a warp a row.
+template <typename T, int LANES, bool SPREAD>
 __global__ void __launch_bounds__(kUnpackThreads, kUnpackCtas)
 compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ scale, int shift,
                       const int32_t* __restrict__ perm, const uint8_t* __restrict__ keep,
@@ -294,6 +302,7 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
                       int32_t* __restrict__ row_of_pos, int ntok, int D, int H, int K, int E,
                       int32_t* err) {
   pdl_begin();  // predecessor complete before any global access
+  static_assert(!SPREAD || LANES == 32, "the warp looks for its row");
   constexpr int V = Vec16<T>::kElems;
   const int64_t N = (int64_t)ntok * K;
   const int64_t gtid = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
@@ -301,7 +310,7 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
   for (int64_t i = gtid; i < N; i += nthr)
     if (!keep[i]) row_of_pos[i] = -1;
 
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & (LANES - 1);
   int64_t M = sel_off[E];
   if (M < 0 || M > N) {  // not of a selection: no row past the buffers is addressed
     if (gtid == 0) flag_error(err, LRM_DEVERR_INDEX);
@@ -315,18 +324,34 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
   }
   const int x_groups = x_cols ? (D + x_cols - 1) / x_cols : 1;
   // a fraction is off by up to 8 of 2^32, which is 4 rows of the most that there can be
-  const int64_t warps = nthr >> 5, deal = SPREAD ? warps - E - 8 : warps;
+  const int64_t teams = nthr / LANES, team = gtid / LANES;
+  const int64_t deal = SPREAD ? teams - E - 8 : teams;
   const int64_t rounds = (M + deal - 1) / deal;
   const uint64_t share = rounds ? ((uint64_t)1 << 48) / (uint64_t)rounds : 0;  // 48 bits
   auto fraction = [&](int64_t r) { return (uint32_t)((uint64_t)r * share >> 16); };
-  for (int64_t round = 0; round < rounds; ++round) {
+  auto row = [&](int64_t round) -> int64_t {
+    if (round >= rounds) return -1;
     const int64_t j =
         SPREAD ? row_of_round(sel_off, E, M, fraction(round),
-                              round + 1 == rounds ? 0u : fraction(round + 1), gtid >> 5, lane)
-               : round * warps + (gtid >> 5);
-    if (j < 0 || j >= M) continue;
-    const int i = sel_pos[j];
-    const int p = (i >= 0 && i < N) ? perm[i] : -1;
+                              round + 1 == rounds ? 0u : fraction(round + 1), team, lane)
+               : round * teams + team;
+    return j < M ? j : -1;
+  };
+  // in the rows' own order the next one's place and pair are looked up before this one's data
+  int64_t j_next = -1;
+  int i_next = -1, p_next = -1;
+  auto look = [&](int64_t round) {
+    j_next = row(round);
+    i_next = j_next >= 0 ? sel_pos[j_next] : -1;
+    p_next = i_next >= 0 && i_next < N ? perm[i_next] : -1;
+  };
+  if (!SPREAD) look(0);
+  for (int64_t round = 0; round < rounds; ++round) {
+    if (SPREAD) look(round);
+    const int64_t j = j_next;
+    const int i = i_next, p = p_next;
+    if (!SPREAD) look(round + 1);
+    if (j < 0) continue;
     if (p < 0 || p >= N) {
       if (lane == 0) flag_error(err, LRM_DEVERR_INDEX);
       continue;
@@ -337,19 +362,19 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
     const float* sr = scale + (int64_t)i * 2 * groups;
     const uint4* gs = reinterpret_cast<const uint4*>(g + t * D);
     uint4* dyd = reinterpret_cast<uint4*>(dy_c + j * D);
-    for (int c0 = lane; c0 < dv; c0 += 32 * kAheadG) {
+    for (int c0 = lane; c0 < dv; c0 += LANES * kAheadG) {
       uint4 v[kAheadG];
 #pragma unroll
       for (int u = 0; u < kAheadG; ++u)
-        if (c0 + 32 * u < dv) v[u] = gs[c0 + 32 * u];
+        if (c0 + LANES * u < dv) v[u] = gs[c0 + LANES * u];
 #pragma unroll
       for (int u = 0; u < kAheadG; ++u) {
-        if (c0 + 32 * u < dv) {
+        if (c0 + LANES * u < dv) {
           float f[V];
           Vec16<T>::unpack(v[u], f);
 #pragma unroll
           for (int e = 0; e < V; ++e) f[e] *= al;
-          __stcs(dyd + c0 + 32 * u, Vec16<T>::pack(f));
+          __stcs(dyd + c0 + LANES * u, Vec16<T>::pack(f));
         }
       }
     }
@@ -357,7 +382,7 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
       if (x_scale) {
         const uint8_t* xr = (const uint8_t*)x + t * D;
         const float* xs = x_scale + t * x_groups;
-        for (int u = lane; u < D / kUnit; u += 32) {
+        for (int u = lane; u < D / kUnit; u += LANES) {
           float f[kUnit];
           decode8(*reinterpret_cast<const uint2*>(xr + u * kUnit),
                   xs[x_cols ? u * kUnit / x_cols : 0], f);
@@ -366,13 +391,13 @@ compact_packed_kernel(const uint8_t* __restrict__ q, const float* __restrict__ s
       } else {
         const uint4* xr = reinterpret_cast<const uint4*>((const T*)x + t * D);
         uint4* xd = reinterpret_cast<uint4*>(x_c + j * D);
-        for (int c = lane; c < dv; c += 32) __stcs(xd + c, xr[c]);
+        for (int c = lane; c < dv; c += LANES) __stcs(xd + c, xr[c]);
       }
     }
     T* abd = ab_c + j * 2 * H;
     T* pd = phi_c + j * H;
 #pragma unroll 1
-    for (int u = lane; u < units; u += 32) {
+    for (int u = lane; u < units; u += LANES) {
       const uint2 ca = __ldcs(reinterpret_cast<const uint2*>(qr + u * kUnit));
       const uint2 cb = __ldcs(reinterpret_cast<const uint2*>(qr + H + u * kUnit));
       float a[kUnit], b[kUnit], ph[kUnit];
@@ -463,14 +488,23 @@ extern "C" lrm_status lrm_score_packed(const lrm_shape* s, const lrm_packed* p, 
   if (!g || !alpha || !inv || !score) return LRM_ERR_INVALID_ARG;
   if (!aligned16(g)) return LRM_ERR_UNSUPPORTED;
   cudaStream_t cs = (cudaStream_t)stream;
-  const dim3 grid((unsigned)(((int64_t)s->T + kScoreWarps - 1) / kScoreWarps));
-  if (s->dtype == LRM_BF16)
-    launch_k(score_packed_kernel<__nv_bfloat16>, grid, dim3(32 * kScoreWarps), 0, cs,
-             (const __nv_bfloat16*)g, (const float*)p->phi_sq, alpha, inv, score, s->T, s->D, s->K,
-             error_word(ws));
-  else
-    launch_k(score_packed_kernel<float>, grid, dim3(32 * kScoreWarps), 0, cs, (const float*)g,
-             (const float*)p->phi_sq, alpha, inv, score, s->T, s->D, s->K, error_word(ws));
+  auto go = [&](auto kern, auto* type, int lanes) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    const int per_cta = 32 * kScoreWarps / lanes;
+    launch_k(kern, dim3((unsigned)(((int64_t)s->T + per_cta - 1) / per_cta)),
+             dim3(32 * kScoreWarps), 0, cs, (const T*)g, (const float*)p->phi_sq, alpha, inv, score,
+             s->T, s->D, s->K, error_word(ws));
+  };
+  auto pick = [&](auto* type) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    // by the width alone: a token's score does not depend on how many others there are
+    const int chunks = s->D / Vec16<T>::kElems;
+    if (chunks <= 32) go(score_packed_kernel<T, 8>, type, 8);
+    else if (chunks <= 128) go(score_packed_kernel<T, 16>, type, 16);
+    else go(score_packed_kernel<T, 32>, type, 32);
+  };
+  if (s->dtype == LRM_BF16) pick((__nv_bfloat16*)nullptr);
+  else pick((float*)nullptr);
   return launch_status();
 }
 
@@ -499,7 +533,18 @@ extern "C" lrm_status lrm_compact_packed(
   cudaStream_t cs = (cudaStream_t)stream;
   const int shift = group_shift(pk->cols);
   const int64_t warps = (int64_t)grid.x * (kUnpackThreads / 32);
-  const bool spread = pk->rows > warps && warps > 2 * (int64_t)s->E + 16;
+  // Cotangents that L2 holds are read from it in any order, and narrow rows pass faster in their
+  // own, each one's place known before its turn (bfloat16, half of 8 a token, us spread | in
+  // order: T 16384 D 512 H 256 53 | 40, D 1024 H 512 82 | 79, D 2048 H 768 131 | 146; T 8192
+  // D 2048 H 704 66 | 67; T 32768 D 1024 H 512 160 | 169, 4 a token H 256 72 | 63).
+  const int64_t row_bytes = (int64_t)s->D * (s->dtype == LRM_BF16 ? 2 : 4);
+  const bool spread = pk->rows > warps && warps > 2 * (int64_t)s->E + 16 && row_bytes >= 4096 &&
+                      row_bytes * s->T >= 32 << 20;
+  // Few lanes for a narrow row (T 29084 D 80 H 48 float32, us with 8 | 16 | 32 lanes: 30 | 35 |
+  // 54; T 7260 D 320 H 128 bfloat16 15 | 16 | 23; T 16384 D 512 H 256 42 | 40 | 41), as long as
+  // the rows are more than the teams (T 969 of 4, D 168 H 208: 5.3 | 4.6 | 4.1).
+  int lanes = row_bytes <= 512 && s->H <= 64 ? 8 : row_bytes <= 1024 && s->H <= 256 ? 16 : 32;
+  while (lanes < 32 && pk->rows <= warps * 16 / lanes) lanes *= 2;
   auto go = [&](auto kern, auto* type) {
     using T = std::remove_pointer_t<decltype(type)>;
     launch_k(kern, grid, dim3(kUnpackThreads), 0, cs, (const uint8_t*)pk->q,
@@ -507,12 +552,14 @@ extern "C" lrm_status lrm_compact_packed(
              x_cols, (const T*)g, (T*)dy_c, (T*)x_c, (T*)ab_c, (T*)phi_c, tok_c, row_of_pos,
              s->T, s->D, s->H, s->K, s->E, error_word(ws));
   };
-  if (s->dtype == LRM_BF16) {
-    using T = __nv_bfloat16;
-    go(spread ? compact_packed_kernel<T, true> : compact_packed_kernel<T, false>, (T*)nullptr);
-  } else {
-    go(spread ? compact_packed_kernel<float, true> : compact_packed_kernel<float, false>,
-       (float*)nullptr);
-  }
+  auto pick = [&](auto* type) {
+    using T = std::remove_pointer_t<decltype(type)>;
+    if (spread) go(compact_packed_kernel<T, 32, true>, type);
+    else if (lanes == 8) go(compact_packed_kernel<T, 8, false>, type);
+    else if (lanes == 16) go(compact_packed_kernel<T, 16, false>, type);
+    else go(compact_packed_kernel<T, 32, false>, type);
+  };
+  if (s->dtype == LRM_BF16) pick((__nv_bfloat16*)nullptr);
+  else pick((float*)nullptr);
   return launch_status();
 }

@@ -618,6 +618,64 @@ def test_packed_rows_of_many_experts(dev, rounds, more):
         assert torch.isfinite(pipe.phi_c[:M]).all()
 
 
+def _every_row_comes_out(dev, T, K, D, H, E, dtype, seed):
+    """compact of random pairs of uneven experts: each retained row is its pair's, bit for bit
+    (dy is one rounded product, a and b another)."""
+    from demand_side_expert_gb300 import PackedState, RecalibratedExpertBackward
+
+    tdtype = torch.float32 if dtype == "f32" else torch.bfloat16
+    gen = torch.Generator().manual_seed(seed)
+    ids = (torch.rand(T, E, generator=gen) ** torch.arange(1, E + 1)).topk(K, dim=1)[1]
+    pipe = RecalibratedExpertBackward(T, D, H, E, K, dtype, dev)
+    pipe.dispatch(ids.to(torch.int32).to(dev))
+    state = PackedState(T, K, H, dtype, cols=32)
+    state.pack(torch.randn(T * K, 2 * H, generator=gen).to(tdtype).to(dev))
+    alpha = torch.rand(T, K, generator=gen).to(dev)
+    g = torch.randn(T, D, generator=gen).to(tdtype).to(dev)
+    x = torch.randn(T, D, generator=gen).to(tdtype).to(dev)
+    pipe.score_pairs(alpha, g, state)
+    for rate in ((1, 1), (2, 3)):
+        pipe.select_rate(*rate)
+        for t in (pipe.dy_c, pipe.x_c, pipe.ab_c, pipe.phi_c):
+            t.fill_(math.nan)
+        pipe.tok_c.fill_(-5)
+        pipe.compact(alpha, x, g, state, None)
+        assert pipe.device_error() == 0
+        M = pipe.retained_rows
+        pos = pipe.sel_pos[:M].long()
+        pair = pipe.perm[pos].long()
+        tok = pair // K
+        assert torch.equal(pipe.tok_c[:M].long(), tok)
+        assert torch.equal(pipe.row_of_pos[pos].long(), torch.arange(M, device=dev))
+        assert int((pipe.row_of_pos[:T * K] >= 0).sum()) == M
+        assert torch.equal(pipe.x_c[:M], x[tok])
+        dy = alpha.view(-1)[pair][:, None] * g[tok].float()
+        assert torch.equal(pipe.dy_c[:M], dy.to(tdtype))
+        wide = state.scale.view(T * K, 2, -1).repeat_interleave(32, 2)[:, :, :H].reshape(T * K, -1)
+        assert torch.equal(pipe.ab_c[:M], (state.q.float() * wide)[pos].to(tdtype))
+        assert torch.isfinite(pipe.phi_c[:M].float()).all()
+
+
+@pytest.mark.parametrize("rounds,more", [(2, -1), (2, 0), (2, 1), (3, 0), (3, 7)])
+def test_packed_rows_of_wide_tokens(dev, rounds, more):
+    """The rows that are met by segments (32 MB of cotangents at least), as many as the warps take
+    in whole rounds, a few more or less."""
+    warps = torch.cuda.get_device_properties(dev).multi_processor_count * 32
+    _every_row_comes_out(dev, rounds * warps + more, 1, 1024, 8, 251, "f32", rounds)
+    _every_row_comes_out(dev, rounds * (warps - 60 - 8) + more, 1, 2048, 8, 60, "bf16", rounds)
+
+
+@pytest.mark.parametrize("T,K,D,H,E,dtype", [
+    (1, 1, 8, 8, 1, "bf16"), (5, 3, 24, 40, 7, "f32"),
+    (20000, 2, 80, 48, 28, "f32"), (20001, 2, 256, 64, 28, "bf16"),  # eight lanes a row
+    (7261, 4, 320, 136, 130, "bf16"), (10001, 2, 256, 256, 9, "f32"),  # sixteen
+    (3001, 4, 80, 48, 28, "bf16"), (1200, 4, 80, 48, 28, "f32"),  # more lanes for fewer rows
+    (8001, 4, 1032, 264, 17, "bf16"), (3001, 4, 264, 520, 64, "f32"),  # a warp, several rounds
+])
+def test_packed_rows_of_every_width(dev, T, K, D, H, E, dtype):
+    _every_row_comes_out(dev, T, K, D, H, E, dtype, T)
+
+
 def test_forward_packs_its_state(dev):
     """forward(packed=...) leaves what pack makes of the saved [a | b]; the backward from it
     is near the one from the 16-bit state (e4m3 has 2^-4 of a value, random ones add in
