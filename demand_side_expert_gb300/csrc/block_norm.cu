@@ -659,7 +659,12 @@ static lrm_status pick_block_bwd(const lrm_block* b, const BlockGrad& g, cudaStr
   // Two chunks a thread wherever 512 threads hold the row so (T 32768, float32 gradients, two
   // | four: D 512 56 us | 58, D 1024 103 | 112, D 4096 T 16384 207 | 224; with one, D 2048 takes
   // 398 instead of 222).
-  if (b->D <= kBlockThreads * 2 * lane_columns<O, G>()) return launch_block_bwd<T, O, G, 2>(a, cs);
+  // A bfloat16 layer's float32 block with bfloat16 gradients has the fewest bytes a chunk, and
+  // four there put more rows into a turn (us two | four: T 32768 D 768 67 | 68, D 1024 87 | 76,
+  // D 1536 134 | 115, T 16384 D 2048 89 | 77, D 3200 154 | 159, T 8192 D 4096 91 | 80).
+  constexpr bool kLight = sizeof(T) == 2 && sizeof(O) == 4 && sizeof(G) == 2;
+  const int two = kLight ? 1023 : kBlockThreads * 2 * lane_columns<O, G>();
+  if (b->D <= two) return launch_block_bwd<T, O, G, 2>(a, cs);
   return launch_block_bwd<T, O, G, 4>(a, cs);
 }
 
