@@ -75,11 +75,12 @@ extern "C" lrm_status lrm_group_route(const lrm_group_router* r, const void* log
   if (((reinterpret_cast<uintptr_t>(bias) | reinterpret_cast<uintptr_t>(loss)) & 3) != 0)
     return LRM_ERR_UNSUPPORTED;
   if (r->T == 0 && !counts) return LRM_OK;
+  // all groups kept are one group of all experts
+  const int groups = r->top_groups == r->groups ? 1 : r->groups;
   RouteArgs a{bias, mask, topk_idx, alpha, counts, prob_sum, loss,
               reinterpret_cast<float2*>((char*)ws + kWsHeaderBytes), r->stride, r->T, r->E, r->K,
-              0, r->score_fn == LRM_SOFTMAX, r->top_groups == r->groups ? 1 : r->groups,
-              r->E / r->groups, r->top_groups, r->group_top, r->renorm, r->scale,
-              r->balance_coef};
+              0, r->score_fn == LRM_SOFTMAX, groups, r->E / groups, r->top_groups,
+              r->group_top, r->renorm, r->scale, r->balance_coef};
   cudaStream_t cs = (cudaStream_t)stream;
   return r->dtype == LRM_BF16 ? group_route_bf16(logits, a, cs)
                               : group_route_f32(logits, a, cs);

@@ -56,6 +56,21 @@ def choose(logits, K, fn="sigmoid", bias=None, groups=1, top_groups=1, group_top
     return out
 
 
+def choose_rows(logits, K, fn="sigmoid", bias=None, groups=1, top_groups=1, group_top=2):
+    """What ``choose`` gives, for all tokens at once by stable sorts."""
+    x = np.asarray(logits, dtype=np.float64)
+    T, E = x.shape
+    s, _ = scores(x, fn)
+    v = s if bias is None else s + np.asarray(bias, dtype=np.float64)
+    opened = x > -np.inf
+    best = -np.sort(np.where(opened, -v, np.inf).reshape(T, groups, E // groups))[..., :group_top]
+    score = np.where(best[..., 0] > -np.inf, np.where(best > -np.inf, best, 0.0).sum(-1), -np.inf)
+    rank = np.argsort(np.argsort(-score, axis=1, kind="stable"), axis=1)
+    dropped = np.repeat(rank >= top_groups, E // groups, axis=1)
+    key = np.where(opened, -(x if bias is None else v), np.inf)
+    return np.lexsort((key, dropped), axis=1)[:, :K].astype(np.int32)
+
+
 def group_route(logits, K, fn="sigmoid", bias=None, groups=1, top_groups=1, group_top=2,
                 renorm=True, scale=1.0, balance_coef=0.0, mask=None, idx=None):
     x = np.asarray(logits, dtype=np.float64)
