@@ -70,3 +70,103 @@ def test_router_keeps_all_groups(dev, E, groups, dtype, fn):  # noqa: F811
     """top_groups is groups, of fewer experts than a lane holds: one group of all."""
     x, mask = routed_rows(E, dtype, "equal", 0.1)
     check_routed(dev, x, 8, fn, make_bias(E, "steps"), groups, groups, 2, True, mask)
+
+
+# E, K, groups, top, group_top, dtype, fn, bias, kind, renorm, off. Not a bias on sigmoids of
+# 1 but for 64 bits' last place, where the larger of two is a matter of the formula's rounding.
+MERGED = [
+    (256, 8, 8, 4, 2, "f32", "sigmoid", "steps", "normal", True, 0.0),
+    (256, 8, 8, 4, 2, "bf16", "softmax", None, "equal", False, 0.1),
+    (256, 5, 8, 4, 1, "f32", "softmax", "zero", "near", True, 0.0),
+    (256, 8, 16, 5, 2, "bf16", "sigmoid", None, "equal", True, 0.0),
+    (256, 1, 4, 1, 2, "f32", "sigmoid", None, "low", True, 0.0),
+    (256, 8, 8, 3, 2, "f32", "sigmoid", None, "high", False, 0.0),
+    (256, 7, 2, 1, 1, "f32", "softmax", None, "one", True, 0.0),
+    (256, 8, 1, 1, 2, "bf16", "softmax", "steps", "low", False, 0.0),
+    (200, 8, 1, 1, 2, "bf16", "sigmoid", "steps", "normal", True, 0.9),
+    (200, 3, 1, 1, 1, "f32", "softmax", None, "near", False, 0.0),
+    (192, 6, 12, 5, 2, "f32", "sigmoid", "zero", "equal", False, 0.2),
+    (192, 8, 3, 2, 2, "bf16", "softmax", "random", "low", True, 0.0),
+    (240, 8, 15, 7, 1, "f32", "sigmoid", "steps", "near", True, 0.0),
+    (128, 8, 8, 3, 2, "f32", "sigmoid", None, "low", False, 0.1),
+    (128, 8, 4, 2, 1, "bf16", "softmax", None, "normal", False, 0.1),
+    (128, 4, 2, 1, 2, "f32", "softmax", "steps", "equal", True, 0.0),
+    (128, 8, 8, 4, 1, "f32", "sigmoid", "random", "near", True, 0.9),
+    (100, 5, 1, 1, 2, "bf16", "sigmoid", None, "equal", True, 0.0),
+    (100, 8, 1, 1, 1, "f32", "softmax", "zero", "low", False, 0.0),
+    (96, 2, 6, 3, 1, "bf16", "sigmoid", "steps", "normal", False, 0.9),
+    (96, 8, 3, 2, 2, "f32", "softmax", None, "one", True, 0.0),
+    (80, 1, 5, 2, 2, "f32", "sigmoid", "random", "normal", True, 0.0),
+]
+
+
+@pytest.mark.parametrize("E,K,groups,top,gt,dtype,fn,bias,kind,renorm,off", MERGED)
+def test_router_merges_lists_across_tokens(dev, E, K, groups, top, gt, dtype, fn,  # noqa: F811
+                                           bias, kind, renorm, off):
+    x, mask = routed_rows(E, dtype, kind, off)
+    check_routed(dev, x, K, fn, make_bias(E, bias, E), groups, top, gt, renorm, mask)
+
+
+FORMS = [  # tokens a SM (0: 6 in all), E, K, groups, top
+    (0, 16, 3, 4, 2), (0, 256, 8, 8, 4),  # a warp a token, lists of 8
+    (25, 32, 3, 4, 2), (25, 64, 8, 4, 2), (25, 256, 8, 8, 4),  # tokens that share a warp
+    (50, 256, 8, 8, 4), (50, 200, 3, 1, 1), (100, 128, 8, 4, 2),  # and merge their lists
+    (0, 64, 12, 4, 2), (3, 320, 6, 8, 3), (3, 200, 8, 25, 5),  # a warp a token, one maximum each
+]
+
+
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("bias", [None, "steps"])
+@pytest.mark.parametrize("per_sm,E,K,groups,top", FORMS)
+def test_router_nan_and_inf_in_every_form(dev, per_sm, E, K, groups, top, bias, fn):  # noqa: F811
+    """NaN and infinities reach the outputs of their own tokens, and of masked ones nothing;
+    every row's ids are valid, distinct and of the kept groups."""
+    T = per_sm * sms() + 6
+    clean = make_logits(T, E, "f32", E)
+    hit = torch.arange(T) % 5 == 1  # a lane group's neighbours are clean
+    nan_rows, all_nan = torch.nonzero(hit)[:, 0], torch.nonzero(torch.arange(T) % 5 == 4)[:, 0]
+    dirty = clean.clone()
+    dirty[nan_rows, 1] = math.nan
+    dirty[all_nan] = math.nan
+    out = torch.zeros(T, dtype=torch.bool)
+    out[nan_rows] = out[all_nan] = True
+    mask = (~out).to(dev)
+    b = None if bias is None else make_bias(E, bias).to(dev)
+    da = torch.ones(T, K, device=dev)
+    da[out.to(dev)] = math.nan
+    size = E // groups
+
+    def routed(x, m, **kw):
+        r = router(T, E, K, "f32", score=fn, groups=groups, top_groups=top, balance_coef=1.0, **kw)
+        r.route(x.to(dev), bias=b, mask=m)
+        ids = r.topk_idx.cpu().long()
+        assert ids.min() >= 0 and ids.max() < E
+        assert (ids.sort(1)[0].diff(dim=1) > 0).all()
+        kept = (ids // size).sort(1)[0]
+        assert ((kept.diff(dim=1) > 0).sum(1) < top).all()
+        return r
+
+    got = [routed(x, mask) for x in (clean, dirty)]
+    for r, x in zip(got, (clean, dirty)):
+        r.backward(x.to(dev), da, mask=mask)
+        assert torch.isfinite(r.dlogits).all() and (r.dlogits[out.to(dev)] == 0).all()
+    for name in ("alpha", "counts", "prob_sum", "loss", "dlogits"):
+        assert torch.equal(getattr(got[0], name), getattr(got[1], name)), name
+    assert torch.equal(got[0].topk_idx[mask], got[1].topk_idx[mask])
+    r = routed(dirty, None)
+    alone = routed(clean, None)
+    assert torch.isnan(r.prob_sum).all() and torch.isnan(r.loss).all()
+    assert torch.equal(r.alpha[mask], alone.alpha[mask])
+    assert torch.equal(r.topk_idx[mask], alone.topk_idx[mask])
+    if fn == "softmax":
+        assert torch.isnan(r.alpha[out.to(dev)]).all()
+    else:  # NaN comes last: numbers are there to choose, and a row of NaN alone has none
+        assert torch.isfinite(r.alpha[nan_rows.to(dev)]).all()
+        assert (r.topk_idx[nan_rows.to(dev)] != 1).all()
+        assert torch.isnan(r.alpha[all_nan.to(dev)]).all()
+        x = clean.clone()
+        x[nan_rows, E - 1] = math.inf  # a score of 1, and without a bias the largest key
+        r = routed(x, None, renorm=False)
+        assert torch.isfinite(r.prob_sum).all() and torch.isfinite(r.alpha).all()
+        ids = mo.choose(to64(x[:12]), K, fn, None if b is None else to64(b), groups, top, 2)
+        assert np.array_equal(r.topk_idx[:12].cpu().numpy(), ids[:T])
