@@ -10,8 +10,8 @@ import pytest
 import torch
 
 from oracle import memory_oracle as mo
-from test_gpu_memory_ops import (TINY, U, close, dev, make_bias, make_logits,  # noqa: F401
-                                 router, score_tol, to64)
+from test_gpu_memory_ops import (BF16, DT, TINY, U, close, dev, make_bias,  # noqa: F401
+                                 make_logits, router, score_tol, to64)
 
 pytestmark = pytest.mark.gpu
 
@@ -170,3 +170,88 @@ def test_router_nan_and_inf_in_every_form(dev, per_sm, E, K, groups, top, bias, 
         assert torch.isfinite(r.prob_sum).all() and torch.isfinite(r.alpha).all()
         ids = mo.choose(to64(x[:12]), K, fn, None if b is None else to64(b), groups, top, 2)
         assert np.array_equal(r.topk_idx[:12].cpu().numpy(), ids[:T])
+
+
+# -- rows rebuilt from 8 bits ---------------------------------------------------
+def compacted(dev, T, K, D, H, E, dtype, x_cols, seed):
+    """compact of random pairs of uneven experts, all and two thirds of them: each retained row
+    is its pair's. dy, a, b and the rows of an 8-bit x are one rounded product each, bit for bit;
+    phi is within the formula's own roundings."""
+    from demand_side_expert_gb300 import PackedState, RecalibratedExpertBackward
+
+    tdtype, N = DT[dtype], T * K
+    gen = torch.Generator(device=dev).manual_seed(seed)
+
+    def randn(*shape):
+        return torch.randn(*shape, generator=gen, device=dev)
+
+    ids = torch.rand(T, E, generator=gen, device=dev)
+    ids = (ids ** torch.arange(1, E + 1, device=dev)).topk(K, dim=1)[1].to(torch.int32)
+    pipe = RecalibratedExpertBackward(T, D, H, E, K, dtype, dev)
+    pipe.dispatch(ids)
+    state = PackedState(T, K, H, dtype, cols=32)
+    state.pack(randn(N, 2 * H).to(tdtype))
+    alpha, g, x = torch.rand(T, K, generator=gen, device=dev), randn(T, D).to(tdtype), randn(T, D)
+    if x_cols is None:
+        x = x_rows = x.to(tdtype)
+    else:
+        groups = -(-D // x_cols) if x_cols else 1
+        scale = torch.rand(T, groups, generator=gen, device=dev) + 0.5
+        q = x.to(torch.float8_e4m3fn)
+        x_rows = (q.float() * scale.repeat_interleave(x_cols or D, 1)[:, :D]).to(tdtype)
+        x = (q, scale)
+    wide = state.scale.view(N, 2, -1).repeat_interleave(32, 2)[:, :, :H].reshape(N, 2 * H)
+    ab = state.q.float() * wide
+    a, b = ab[:, :H].double(), ab[:, H:].double()
+    phi = a / (1 + torch.exp(-a)) * b
+    half = BF16 if dtype == "bf16" else 0.0
+    lim = (half + (2 * a.abs() + 12) * U) * phi.abs() + TINY
+    pipe.score_pairs(alpha, g, state)
+    for rate in ((1, 1), (2, 3)):
+        pipe.select_rate(*rate)
+        for t in (pipe.dy_c, pipe.x_c, pipe.ab_c, pipe.phi_c):
+            t.fill_(math.nan)
+        pipe.tok_c.fill_(-5)
+        pipe.compact(alpha, x, g, state, None)
+        assert pipe.device_error() == 0
+        M = pipe.retained_rows
+        assert M == N or rate != (1, 1)
+        pos = pipe.sel_pos[:M].long()
+        pair = pipe.perm[pos].long()
+        tok = pair // K
+        assert torch.equal(pipe.tok_c[:M].long(), tok)
+        assert torch.equal(pipe.row_of_pos[pos].long(), torch.arange(M, device=dev))
+        assert int((pipe.row_of_pos[:N] >= 0).sum()) == M
+        assert torch.equal(pipe.x_c[:M], x_rows[tok])
+        assert torch.equal(pipe.dy_c[:M], (alpha.view(-1)[pair][:, None] * g[tok].float()).to(tdtype))
+        assert torch.equal(pipe.ab_c[:M], ab[pos].to(tdtype))
+        assert ((pipe.phi_c[:M].double() - phi[pos]).abs() <= lim[pos]).all()
+
+
+@pytest.mark.parametrize("more", [-1, 0, 1, 7])
+@pytest.mark.parametrize("rounds", [2, 3])
+@pytest.mark.parametrize("lanes,D,H,dtype", [(8, 16, 8, "f32"), (8, 256, 64, "bf16"),
+                                             (16, 256, 72, "f32"), (16, 24, 256, "bf16"),
+                                             (32, 264, 8, "f32"), (32, 64, 264, "bf16")])
+def test_packed_rows_in_whole_rounds(dev, lanes, D, H, dtype, rounds, more):  # noqa: F811
+    """As many rows as the teams of lanes take in whole rounds, a few more or less."""
+    teams = sms() * 4 * (256 // lanes)
+    compacted(dev, rounds * teams + more, 1, D, H, 61, dtype, None, rounds)
+
+
+@pytest.mark.parametrize("more", [-1, 0, 1])
+@pytest.mark.parametrize("K,E,x_cols", [(4, 60, None), (8, 60, 128), (4, 28, 0), (2, 121, 32)])
+def test_packed_rows_met_by_segments(dev, K, E, x_cols, more):  # noqa: F811
+    """32 MB of cotangents whose tokens' rows are shared by K pairs: about as many rows as are
+    dealt out in whole rounds, x in the layer's type or in 8 bits."""
+    deal = sms() * 32 - E - 8
+    tokens = -(-8192 * K // deal) * deal // K + more  # 32 MB of rows of 4096 bytes at least
+    compacted(dev, tokens, K, 2048, 40, E, "bf16", x_cols, K)
+    compacted(dev, -(-2048 * K // deal) * deal // K + more, K, 4096, 8, E, "f32", x_cols, K)
+
+
+@pytest.mark.parametrize("T,K,D,H,E,dtype,x_cols", [
+    (20001, 2, 64, 48, 28, "bf16", 0), (10001, 2, 256, 256, 9, "f32", 64),
+    (3001, 4, 264, 520, 64, "f32", 256), (33, 3, 1032, 264, 17, "bf16", 128)])
+def test_packed_rows_beside_8_bit_rows(dev, T, K, D, H, E, dtype, x_cols):  # noqa: F811
+    compacted(dev, T, K, D, H, E, dtype, x_cols, T)
