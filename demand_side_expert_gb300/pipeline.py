@@ -17,6 +17,7 @@ and passes pointers.
 from __future__ import annotations
 
 import ctypes
+import math
 
 import torch
 
@@ -135,6 +136,19 @@ def _x_groups(D: int, groups: int) -> int:
     raise ValueError(f"x: {groups} scales for {D} columns")
 
 
+def _weight_gradient(name: str) -> property:
+    """A float32 output of the backward pass that the caller may give memory for."""
+    attr = "_" + name
+
+    def give(self, t):
+        if t is None:
+            raise ValueError(f"{name}: the backward pass writes it")
+        shape = (self.E, self.H, self.D) if name == "dw_down" else (self.E, self.D, self.H)
+        setattr(self, attr, self._own(t, name, shape, torch.float32))
+
+    return property(lambda self: getattr(self, attr), give)
+
+
 class RecalibratedExpertBackward:
     """Buffers + call sequence for one (T, D, H, E, K, dtype) layer shape."""
 
@@ -167,11 +181,14 @@ class RecalibratedExpertBackward:
         self.ab_c, self.phi_c = empty(rows, 2 * H, dtype=dt), empty(rows, H, dtype=dt)
         self.tok_c, self.row_of_pos = empty(rows, dtype=i32), empty(rows, dtype=i32)
         self.dab_c, self.dx_c = empty(rows, 2 * H, dtype=dt), empty(rows, D, dtype=f32)
-        self.dw_gate, self.dw_up = empty(E, D, H, dtype=f32), empty(E, D, H, dtype=f32)
-        self.dw_down = empty(E, H, D, dtype=f32)
+        self._dw_gate, self._dw_up = empty(E, D, H, dtype=f32), empty(E, D, H, dtype=f32)
+        self._dw_down = empty(E, H, D, dtype=f32)
         self.dx = empty(max(T, 1), D, dtype=f32)
-        self._y = None
+        self._y = self._out = None
         lrm.lrm_clear_device_error(self.ws, self.ws_bytes)
+
+    dw_gate, dw_up = _weight_gradient("dw_gate"), _weight_gradient("dw_up")
+    dw_down = _weight_gradient("dw_down")
 
     # -- forward side -------------------------------------------------------
     def dispatch(self, topk_idx, stream=None):
@@ -186,7 +203,10 @@ class RecalibratedExpertBackward:
             self.x_disp = torch.empty(rows, self.D, dtype=dt, device=dev)
             self.ab = torch.empty(rows, 2 * self.H, dtype=dt, device=dev)
             self.phi = torch.empty(rows, self.H, dtype=dt, device=dev)
-            self.out = torch.empty(max(self.T, 1), self.D, dtype=torch.float32, device=dev)
+        if self._out is None:
+            _after_current(stream)
+            self._out = torch.empty(max(self.T, 1), self.D, dtype=torch.float32,
+                                    device=self.device)
 
     def _expert_outputs(self, stream):
         if self._y is None:
@@ -203,14 +223,41 @@ class RecalibratedExpertBackward:
 
     @y.setter
     def y(self, rows):
-        self._y = rows
+        self._y = self._own(rows, "y", (self.N, self.D), self.tdtype)
+
+    @property
+    def out(self) -> torch.Tensor:
+        """The layer output [T, D], float32. Allocated by the first forward call."""
+        if self._out is None:
+            raise AttributeError("out: there was no forward call")
+        return self._out
+
+    @out.setter
+    def out(self, rows):
+        self._out = self._own(rows, "out", (self.T, self.D), torch.float32)
+
+    def _own(self, t, name: str, shape: tuple, dtype: torch.dtype):
+        """Memory of the caller's for an output of this shape (None: none)."""
+        if t is not None and (t.dtype is not dtype or t.device != self.ws.device or
+                              not t.is_contiguous() or t.numel() < math.prod(shape)):
+            raise ValueError(f"{name}: a contiguous {dtype} tensor {shape} on {self.ws.device} is "
+                             f"needed, got {t.dtype} {tuple(t.shape)} strides {t.stride()} on "
+                             f"{t.device}")
+        return t
 
     def forward(self, topk_idx, alpha, x, w_gate, w_up, w_down, stream=None,
                 packed: PackedState | None = None):
         """Forward expert pass: dispatch, gather, gate/up + SwiGLU, down,
         combine. Leaves the saved state in ``ab`` / ``phi`` (dispatch order)
         and the layer output in ``out`` (float32 [T, D]). ``packed`` gets the
-        state in 8 bits: ``ab`` and ``phi`` may then serve the next layer."""
+        state in 8 bits: ``ab`` and ``phi`` may then serve the next layer.
+
+        One object can so serve several layers of its shape, forward one after
+        the other and back again. What stays a layer's own until its backward
+        pass, beside x, the choices and ``packed``: ``y`` where ``gate_grad`` is
+        to be called, ``out`` where something reads it, and ``dw_gate``,
+        ``dw_up``, ``dw_down``. Assign the layer's own rows to these before the
+        call that writes or reads them; ``gate_grad`` says what else it needs."""
         if packed is not None:
             self._check_packed(packed)
         self._forward_buffers(stream)
@@ -252,7 +299,9 @@ class RecalibratedExpertBackward:
     def gate_grad(self, g, stream=None) -> torch.Tensor:
         """Gradient of the routing weights [T, K] (float32) from the cotangent g
         [T, D] of the layer output, in the layer's type, and the rows ``y`` of the
-        last forward."""
+        last forward, in the order of the last dispatch. Where other layers have
+        used the object since: assign this layer's rows to ``y``, and call it after
+        its ``step``, or ``dispatch``, with its choices."""
         if self._y is None:
             raise RuntimeError("gate_grad needs the expert outputs of a forward call")
         device = self.ws.device

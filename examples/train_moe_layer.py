@@ -17,9 +17,12 @@ Every step runs the whole chain of a training step with this package's kernels:
 With --tight, the block of a model that is short of memory (TightMoeBlock):
 
   experts of the best groups, with a bias that evens the loads   GroupRouter
-  the saved state in 8 bits, one [a | b] buffer for all layers   PackedState, .forward, .step
+  the saved state in 8 bits                                      PackedState, .forward, .step
   norm of the experts' output, gate, scaled residual and the
   norm in front of the next block                                BlockNorm
+
+and the experts' buffers, [a | b] and phi among them, are one set for all blocks (here for the
+teacher and the trained one).
 """
 
 from __future__ import annotations
@@ -90,24 +93,35 @@ class MoeBlock:
 
 class TightMoeBlock:
     """y = RMS norm(h'), h' = scale * h + gate * RMS norm(MoE(RMS norm(h))), h = x + residual:
-    norms on both sides of the experts. What is kept from forward to backward is u, h' and 8-bit
-    rows of [a | b]. Weights beside ``init_weights``'s: "post", "next" and "layer_scale" [D];
-    ``bias`` [E] float32 is moved by the loads, not by a gradient."""
+    norms on both sides of the experts. Weights beside ``init_weights``'s: "post", "next" and
+    "layer_scale" [D]; ``bias`` [E] float32 is moved by the loads, not by a gradient.
+
+    ``experts``: another block's, whose buffers then serve both, one after the other. What a
+    block keeps of its own from forward to backward: h, u, h' [T, D], the logits, choices and
+    weights, 8-bit rows of [a | b], the experts' output before and behind the combination (``y``
+    [T*K, D], which the routing weights' gradient reads, and ``out`` [T, D] float32), and its
+    weights' gradients."""
 
     SCALE = 0.8  # of the residual
 
     def __init__(self, T, D, H, E, K, weights: dict, groups=4, top_groups=2, balance_coef=0.001,
-                 packed=True):
+                 packed=True, experts=None):
+        if experts is not None and not packed:
+            raise ValueError("experts: the state in 16 bits stands in their buffers, of one block")
         self.w = weights
         self.norm = AddRMSNorm(T, D, "bf16")
         self.router = GroupRouter(T, E, K, "bf16", groups=groups, top_groups=top_groups,
                                   balance_coef=balance_coef)
-        self.experts = ex = RecalibratedExpertBackward(T, D, H, E, K, "bf16")
+        self.experts = experts or RecalibratedExpertBackward(T, D, H, E, K, "bf16")
+        self.y = torch.empty(T * K, D, dtype=torch.bfloat16, device="cuda")
+        self.out = torch.empty(T, D, device="cuda")
         self.state = PackedState(T, K, H, "bf16", cols=64) if packed else None
         self.after = BlockNorm(T, D, "bf16", gate="column", residual_scale=self.SCALE)
         self.bias = torch.zeros(E, device="cuda")
         self.grads = {"norm": self.norm.dw, "router": torch.empty(D, E, device="cuda"),
-                      "gate": ex.dw_gate, "up": ex.dw_up, "down": ex.dw_down,
+                      "gate": torch.empty(E, D, H, device="cuda"),
+                      "up": torch.empty(E, D, H, device="cuda"),
+                      "down": torch.empty(E, H, D, device="cuda"),
                       "post": self.after.dw_post, "next": self.after.dw,
                       "layer_scale": self.after.dgate}
 
@@ -116,9 +130,10 @@ class TightMoeBlock:
         self.norm.forward(x, w["norm"], residual=residual)
         self.logits = self.norm.y @ w["router"]
         r.route(self.logits, bias=self.bias)
+        ex.y, ex.out = self.y, self.out
         ex.forward(r.topk_idx, r.alpha, self.norm.y, w["gate"], w["up"], w["down"],
                    packed=self.state)
-        self.after.forward(ex.out, self.norm.h, w["next"], w_post=w["post"], gate=w["layer_scale"])
+        self.after.forward(self.out, self.norm.h, w["next"], w_post=w["post"], gate=w["layer_scale"])
         return self.after.y.float()
 
     def even_loads(self, rate=1e-3):
@@ -128,12 +143,15 @@ class TightMoeBlock:
         """g [T, D] float32: the cotangent of forward's result. Leaves the weights'
         gradients in ``grads`` and returns the one of x (and of the residual)."""
         w, ex, r, n = self.w, self.experts, self.router, self.after
-        n.backward(g, ex.out, w["next"], w["post"], w["layer_scale"])
-        r.backward(self.logits, ex.gate_grad(n.dblock))
+        n.backward(g, self.out, w["next"], w["post"], w["layer_scale"])
         u = self.norm.y
         saved = (ex.ab, ex.phi) if self.state is None else (self.state, None)
+        ex.y, ex.dw_gate, ex.dw_up, ex.dw_down = (self.y, self.grads["gate"], self.grads["up"],
+                                                  self.grads["down"])
         ex.step(r.topk_idx, r.alpha, u, n.dblock, *saved, w["gate"], w["up"], w["down"],
                 rate=rate, gathered=True)
+        # after the step, whose dispatch is of this block's choices
+        r.backward(self.logits, ex.gate_grad(n.dblock))
         self.grads["router"].copy_(u.t() @ r.dlogits)
         du = ex.dx + (r.dlogits @ w["router"].t()).float()
         self.norm.backward(du, w["norm"], dh=n.dres)
@@ -153,7 +171,8 @@ def train(steps=60, T=2048, D=256, H=128, E=16, K=2, rate=(1, 2), state="f32", l
     """The loss of every step."""
     make, weights = (TightMoeBlock, tight_weights) if tight else (MoeBlock, init_weights)
     teacher = make(T, D, H, E, K, weights(D, H, E, seed + 1))
-    block = make(T, D, H, E, K, weights(D, H, E, seed + 2))
+    shared = {"experts": teacher.experts} if tight else {}
+    block = make(T, D, H, E, K, weights(D, H, E, seed + 2), **shared)
     names = list(block.w)
     opt = AdamW([block.w[n] for n in names], [block.grads[n] for n in names], lr=lr,
                 betas=(0.9, 0.95),
