@@ -51,19 +51,30 @@ class LrmError(RuntimeError):
         super().__init__(f"{fn} returned {status_string(status)}")
 
 
-class lrm_shape(ctypes.Structure):
+class _Descriptor(ctypes.Structure):
+    """A host struct. A number that its 32 bits do not hold is refused (ctypes would keep
+    the low ones)."""
+
+    def __init__(self, *args):
+        super().__init__(*args)
+        for (name, kind), v in zip(self._fields_, args):
+            if kind is ctypes.c_int32 and getattr(self, name) != v:
+                raise ValueError(f"{type(self).__name__}.{name}: {v} is past 32 bits")
+
+
+class lrm_shape(_Descriptor):
     _fields_ = [("T", ctypes.c_int32), ("D", ctypes.c_int32), ("H", ctypes.c_int32),
                 ("E", ctypes.c_int32), ("K", ctypes.c_int32), ("dtype", ctypes.c_int32)]
 
 
-class lrm_router(ctypes.Structure):
+class lrm_router(_Descriptor):
     _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("stride", ctypes.c_int64),
                 ("renorm", ctypes.c_int32), ("balance_coef", ctypes.c_float),
                 ("z_coef", ctypes.c_float)]
 
 
-class lrm_norm(ctypes.Structure):
+class lrm_norm(_Descriptor):
     _fields_ = [("T", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("grad_dtype", ctypes.c_int32), ("q_cols", ctypes.c_int32),
                 ("eps", ctypes.c_float), ("x_stride", ctypes.c_int64),
@@ -85,7 +96,7 @@ class lrm_adamw(ctypes.Structure):
                 ("grad_scale", ctypes.c_void_p)]
 
 
-class lrm_group_router(ctypes.Structure):
+class lrm_group_router(_Descriptor):
     _fields_ = [("T", ctypes.c_int32), ("E", ctypes.c_int32), ("K", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("stride", ctypes.c_int64),
                 ("score_fn", ctypes.c_int32), ("groups", ctypes.c_int32),
@@ -98,13 +109,13 @@ class lrm_bias(ctypes.Structure):
     _fields_ = [("E", ctypes.c_int32), ("rate", ctypes.c_float)]
 
 
-class lrm_packed(ctypes.Structure):
+class lrm_packed(_Descriptor):
     _fields_ = [("q", ctypes.c_void_p), ("scale", ctypes.c_void_p), ("phi_sq", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("H", ctypes.c_int32), ("cols", ctypes.c_int32),
                 ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
-class lrm_block(ctypes.Structure):
+class lrm_block(_Descriptor):
     _fields_ = [("T", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_int32),
                 ("block_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32),
                 ("gate", ctypes.c_int32), ("q_cols", ctypes.c_int32), ("eps", ctypes.c_float),

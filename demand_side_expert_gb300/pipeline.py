@@ -97,9 +97,10 @@ class PackedState:
         self.N, self.H, self.cols = T * K, H, cols
         self.dtype_code = dtype_code(dtype)
         self.tdtype = _TORCH_DTYPE[self.dtype_code]
-        if T < 0 or K <= 0 or H <= 0 or H % 8 or cols not in (32, 64, 128) or self.N >= 1 << 31:
+        if T < 0 or K <= 0 or H <= 0 or H % 8 or cols not in (32, 64, 128) or \
+                max(self.N, H) >= 1 << 31:
             raise ValueError(f"unsupported state T={T} K={K} H={H} cols={cols}: H a multiple of "
-                             "8, cols one of 32, 64, 128 and T*K < 2^31 are needed")
+                             "8, cols one of 32, 64, 128, T*K and H below 2^31 are needed")
         self.device = dev = _device(device)
         with torch.inference_mode(False):  # inference tensors do not count their writes
             self._q = torch.empty(self.N, 2 * H, dtype=torch.uint8, device=dev).view(
