@@ -663,9 +663,10 @@ static lrm_status pick_block_bwd(const lrm_block* b, const BlockGrad& g, cudaStr
   // four there put more rows into a turn (us two | four: T 32768 D 768 67 | 68, D 1024 87 | 76,
   // D 1536 134 | 115, T 16384 D 2048 89 | 77, D 3200 154 | 159, T 8192 D 4096 91 | 80).
   constexpr bool kLight = sizeof(T) == 2 && sizeof(O) == 4 && sizeof(G) == 2;
-  const int two = kLight ? 1023 : kBlockThreads * 2 * lane_columns<O, G>();
-  if (b->D <= two) return launch_block_bwd<T, O, G, 2>(a, cs);
-  return launch_block_bwd<T, O, G, 4>(a, cs);
+  constexpr int two = kLight ? 1023 : kBlockThreads * 2 * lane_columns<O, G>();
+  if constexpr (two < kBlockMaxD)
+    if (b->D > two) return launch_block_bwd<T, O, G, 4>(a, cs);
+  return launch_block_bwd<T, O, G, 2>(a, cs);
 }
 
 template <typename... P>
