@@ -573,6 +573,15 @@ static lrm_status launch_block(const lrm_block* b, const BlockFwd& a, cudaStream
 template <typename T, typename O>
 static lrm_status pick_block(const lrm_block* b, const BlockFwd& a, cudaStream_t cs) {
   const int D = b->D;
+  // Few elements an SM: as many threads a row as there are units, for a short row's latency
+  // (bfloat16 rows, float32 block, us so | several units a thread: D 1024 T 608 2.9 | 4.5, T 2432
+  // 7.2 | 9.0, T 58368 91 | 93; D 2048 T 304 3.0 | 3.5, T 1216 7.7 | 6.9, T 29184 95 | 90; D 4096
+  // T 152 3.4 | 3.8, T 608 8.5 | 7.2, T 14592 105 | 92; D 8192 T 304 7.6 | 9.9, T 7296 99 | 98).
+  // Rows of 8192 columns that are all float32 would gain by it at any T (T 7296 174 | 198, 0.81
+  // and 0.71 of the copy bandwidth; D 6144 182 | 173).
+  // Narrow rows have a unit a thread up to 256 columns; of the copy bandwidth, 0.17 to 0.34 GB in
+  // all, and with two units a thread: D 32 0.91 | 0.80, D 64 0.96 | 0.97, D 128 0.96 | 0.94,
+  // D 256 0.95 | 0.95. D 512 has two units, 0.94; one on 64 threads 0.72.
   const bool few = (int64_t)b->T * D <= (int64_t)num_sms() * 16384;
   if (D <= 32) return launch_block<T, O, 4, 1>(b, a, cs);
   if (D <= 64) return launch_block<T, O, 8, 1>(b, a, cs);
@@ -661,7 +670,10 @@ static lrm_status pick_block_bwd(const lrm_block* b, const BlockGrad& g, cudaStr
   // 398 instead of 222).
   // A bfloat16 layer's float32 block with bfloat16 gradients has the fewest bytes a chunk, and
   // four there put more rows into a turn (us two | four: T 32768 D 768 67 | 68, D 1024 87 | 76,
-  // D 1536 134 | 115, T 16384 D 2048 89 | 77, D 3200 154 | 159, T 8192 D 4096 91 | 80).
+  // D 1536 134 | 115, T 16384 D 2048 89 | 77, D 3200 154 | 159, T 8192 D 4096 91 | 80; widths
+  // like 3200 are not told apart).
+  // Where everything is float32 four chunks of a row of D 8192 with dh fill the ring, so one row
+  // is in flight: T 8192 252 us, 0.94 of the copy bandwidth (D 7168 0.93).
   constexpr bool kLight = sizeof(T) == 2 && sizeof(O) == 4 && sizeof(G) == 2;
   constexpr int two = kLight ? 1023 : kBlockThreads * 2 * lane_columns<O, G>();
   if constexpr (two < kBlockMaxD)

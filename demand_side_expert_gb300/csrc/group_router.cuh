@@ -17,7 +17,9 @@
 // them minima and maxima (sorting, merging), and at few warps their latency. T 32768 E 256
 // K 8, 4 of 8 groups, with statistics: 32 us, of which 2 to 3 are the statistics' second
 // kernel and about 8 the tokens done again in 64 bits (24.8 with the doubts left as they
-// are); the gradient 13.4 us.
+// are); the gradient 15.4 us, of bfloat16 15.7: half the bytes and the same instructions.
+// Times in this file are of four inputs in turn with sigmoid scores and a bias in float32,
+// where nothing else is said.
 #pragma once
 
 #include <algorithm>
@@ -599,7 +601,8 @@ group_route_kernel(const T* __restrict__ logits, const RouteArgs a) {
 // sorts its keys, the two largest of a group's lanes rank the groups, the others' keys
 // are dropped, and the token's lanes merge their lists of 8 pairwise. Choices that stand
 // further apart than both keys' errors are sure. Bound by one token's chain: few warps an
-// SM have work (T 5003 E 128, padded, with statistics: 11 us; T 1000 E 256 6.8).
+// SM have work (T 5003 E 128, softmax, padded, with statistics: 12 us; T 1000 E 256 9.9). The
+// 768 threads leave 80 registers, and 16 experts a lane with statistics spill 20 to 84 bytes.
 constexpr int kTopK = 8;
 constexpr int fast_route_threads(int l) { return l == 32 ? 512 : 768; }
 
@@ -875,8 +878,8 @@ group_route_fast_kernel(const T* __restrict__ logits, const RouteArgs a) {
 // weights, doubts) is then done for all of the round's tokens at once. What a merge leaves
 // out is remembered by its largest key: the first one behind the choices.
 constexpr int kRound = 4;
-// 512 threads: 32768 tokens, E 256, statistics, take 34.1 us, 640 and 768 (which spill) 35.1
-// and 39.4.
+// 512 threads: 32768 tokens, E 256, statistics, take 32.1 us, 640 and 768 (which spill) 33.2
+// and 35.7.
 constexpr int kRoundThreads = 512;
 
 // a := the 8 largest of two descending lists, descending; `out`: the largest left out.
@@ -1254,8 +1257,9 @@ group_route_many_kernel(const T* __restrict__ logits, const RouteArgs a) {
 // The row's exponentials are the hardware's (off by up to 7e-8 for each unit of a logit),
 // the choices' own are expf's.
 constexpr int kGroupBwdThreads = 256;
-// Four CTAs an SM are said outright for rows of 16 experts a lane (T 32768 E 256: 13.4 us, 17.7
-// with the two that the compiler's registers leave room for).
+// Four CTAs an SM are said outright for rows of 16 experts a lane (T 32768 E 256: 15.4 us, 21.3
+// with the two that the compiler's registers leave room for, though 64 registers spill 16 to
+// 44 bytes). A token's choices are distinct: two lanes with one expert would write one element.
 template <typename T, int NI, int G, int kPer, bool SOFTMAX>
 __global__ void __launch_bounds__(kGroupBwdThreads, NI == 16 && kPer == 1 ? 4 : 0)
 group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dlogits) {
@@ -1454,8 +1458,8 @@ static lrm_status launch_route_kernel(void (*kern)(const T*, RouteArgs), const v
   if (stats) {
     // one CTA an SM at most (each leaves a row for the last sums), its warps in even
     // rounds; tokens that fit one CTA stay in one, without that second launch. Eight warps
-    // at least: T 1000 E 256 takes 6.8 us, 7.9 with 16 and 6.9 with 4 (T 8192 16.7, 18.8,
-    // 17.1)
+    // at least: T 1000 E 256 takes 10.1 us, 11.3 with 16 and 10.1 with 4 (T 8192 17.2, 19.8,
+    // 17.5)
     const int64_t ctas = std::min(num_sms(), kRouterMaxCtas);
     const int64_t rounds = (warps + ctas * max_warps - 1) / (ctas * max_warps);
     const int64_t need = (warps + rounds - 1) / rounds;
@@ -1541,13 +1545,17 @@ template <typename T>
 lrm_status pick_group_route(const void* logits, const RouteArgs& a, cudaStream_t cs) {
   if (a.E <= 256 && a.K <= kTopK) {
     const int cap = a.E <= 32 ? 32 : a.E <= 64 ? 64 : a.E <= 128 ? 128 : 256;
+    // From 20 tokens an SM on they share warps (T 3040, with statistics, us shared | a warp a
+    // token: E 32 7.9 | 10.8, E 64 10.9 | 13.2, E 128 10.4 | 12.3, E 256 12.8 | 13.3, softmax of
+    // bfloat16 E 128 21.0 | 19.6, E 256 26.5 | 27.6; T 1520 E 32 7.7 | 8.4, E 128 10.4 | 10.2,
+    // softmax of bfloat16 17.9 | 15.6, E 256 10.9 | 10.6).
     const bool many = (int64_t)a.ntok > (int64_t)num_sms() * 20;
     const int shared_ni = cap == 32 ? 4 : cap == 64 ? 8 : 16;
     if (many && whole_lanes(a, shared_ni)) {
-      // From 800 lanes of tokens an SM on the lists are merged across tokens (E 256, 16 lanes a
-      // token, us: T 5003 18.9 against 15.4, T 8192 16.7 | 19.1, T 16384 20.7 | 25.4, T 32768
-      // 32.3 | 37.0; E 128, 8 lanes, T 32768 18.2 | 20.8). Lists of few experts a lane gain
-      // nothing (E 64 T 32768 19.1 | 18.7).
+      // From 800 lanes of tokens an SM on the lists are merged across tokens (us merged | not:
+      // E 256, 16 lanes a token, T 5003 14.2 | 13.6, T 7600 15.4 | 17.5, T 16384 19.7 | 24.1,
+      // T 32768 32.5 | 38.1; E 128, 8 lanes, T 8192 14.9 | 12.7, T 15200 16.7 | 17.4, T 32768
+      // 19.9 | 23.0). Lists of few experts a lane gain nothing (E 64 T 32768 19.1 | 18.7).
       const bool most = (int64_t)a.ntok * (cap / 16) >= (int64_t)num_sms() * 800;
       if (cap == 32) return launch_fast_route<T, 4, 8>(logits, a, cs);
       if (cap == 64) return launch_fast_route<T, 8, 8>(logits, a, cs);

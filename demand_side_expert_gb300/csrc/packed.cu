@@ -15,7 +15,8 @@ constexpr float kLog2e = 1.4426950408889634f;
 
 // a sigmoid(a) = a / (1 + 2^(-a log2 e)) on the hardware's power of two and reciprocal:
 // the product's rounding puts it off by up to 9e-8 |a| of itself for a below 0, where
-// SiLU falls as |a| e^a, and by 3e-7 elsewhere. -inf gives NaN, as the formula does.
+// SiLU falls as |a| e^a, and by 3e-7 elsewhere. From -87.3 down, where |SiLU| is below
+// 1.1e-36, the reciprocal is below 2^-126 and the result 0. -inf gives NaN, as the formula does.
 __device__ __forceinline__ float silu(float a) {
   float e, r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(-a * kLog2e));
@@ -284,7 +285,8 @@ __device__ __forceinline__ void stream8(T* p, const float (&f)[kUnit]) {
 
 // Four CTAs an SM (T 16384 D 4096 H 1408, half of the pairs: 241 us; three 248, five, six and
 // eight 270, 268, 307), and 4 of a lane's 16-byte pieces of a cotangent ahead (8: as long, 12:
-// 266; a short block, T 1021 D 2048: 1.1 and 2.4 us longer). Their results are not read here: stores
+// 266; a short block, T 1021 D 2048: 1.1 and 2.4 us longer), for which its 64 registers spill 24 to
+// 80 bytes. Their results are not read here: stores
 // that leave L2 first keep the cotangents in it (plain ones 249 us).
 constexpr int kUnpackCtas = 4, kAheadG = 4;
 
@@ -536,7 +538,8 @@ extern "C" lrm_status lrm_compact_packed(
   // Cotangents that L2 holds are read from it in any order, and narrow rows pass faster in their
   // own, each one's place known before its turn (bfloat16, half of 8 a token, us spread | in
   // order: T 16384 D 512 H 256 53 | 40, D 1024 H 512 82 | 79, D 2048 H 768 131 | 146; T 8192
-  // D 2048 H 704 66 | 67; T 32768 D 1024 H 512 160 | 169, 4 a token H 256 72 | 63).
+  // D 2048 H 704 66 | 67; T 32768 D 1024 H 512 160 | 169, 4 a token H 256 72 | 63). The line at
+  // 4096 bytes a row leaves the one that loses by 6% on the wrong side of it.
   const int64_t row_bytes = (int64_t)s->D * (s->dtype == LRM_BF16 ? 2 : 4);
   const bool spread = pk->rows > warps && warps > 2 * (int64_t)s->E + 16 && row_bytes >= 4096 &&
                       row_bytes * s->T >= 32 << 20;

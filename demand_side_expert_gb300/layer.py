@@ -381,9 +381,10 @@ class GroupRouter:
         """The logits' gradient, from the choices and counts of the last ``route`` (with
         statistics) on the same logits and mask. ``dalpha`` [T, K] float32
         (``RecalibratedExpertBackward.gate_grad``), ``dloss`` [1] float32: what the
-        balance loss weighs in the total (1 by default). Choices and counts that the
-        caller wrote into ``topk_idx`` and ``counts`` serve as well; without either the
-        call is refused (counts are not needed where the loss's coefficient is 0)."""
+        balance loss weighs in the total (1 by default). Choices (a token's distinct) and
+        counts that the caller wrote into ``topk_idx`` and ``counts`` serve as well; without
+        either the call is refused (counts are not needed where the loss's coefficient is
+        0)."""
         mask = self._inputs(logits, mask)
         if not self._routed and self._topk_idx._version == self._idx_at:
             raise ValueError("no choices to take the gradient of: call route before")

@@ -683,7 +683,8 @@ lrm_status lrm_group_route(const lrm_group_router* router, const void* logits,
  *   logits, mask as lrm_group_route (read); topk_idx [T,K], counts [E] from it (read).
  *   dalpha [T,K] float (read) or NULL (0); dloss [1] float (read) or NULL (1).
  *   dlogits [T,E] dtype, contiguous (written).
- * Ids outside [0,E) are skipped and flag LRM_DEVERR_EXPERT_ID.
+ * Ids outside [0,E) are skipped and flag LRM_DEVERR_EXPERT_ID. A token's ids have to be
+ * distinct, as lrm_group_route's are.
  */
 lrm_status lrm_group_route_bwd(const lrm_group_router* router, const void* logits,
                                const uint8_t* mask, const int32_t* topk_idx,
