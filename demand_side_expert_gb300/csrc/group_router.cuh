@@ -1208,16 +1208,17 @@ group_route_many_kernel(const T* __restrict__ logits, const RouteArgs a) {
     float factor = a.scale;
     if (a.renorm) {
       sum = over_token(sum, plus);
-      if (!SOFTMAX && __any_sync(0xffffffffu, sum < 1e-25f)) {
-        // scores below 32 bits: over the largest of them
+      if (!SOFTMAX && __any_sync(0xffffffffu, sum < 1e-6f)) {
+        // one of the scores may be below 32 bits' normal numbers and a weight all the same: over
+        // exp(m), m the largest logit
         float m = xk[0], low_sum = 0.f;
 #pragma unroll
         for (int i = 1; i < kEach; ++i) m = fmaxf(m, xk[i]);
         m = over_token(m, larger);
-        const bool lost = sum < 1e-25f;
+        const bool lost = sum < 1e-6f;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
-          const float f = m > -CUDART_INF_F ? expf(xk[i] - m) : 0.f;
+          const float f = m > -CUDART_INF_F ? expf(xk[i] - m) / (1.f + expf(xk[i])) : 0.f;
           low_sum += f;
           w[i] = lost ? f : w[i];
         }

@@ -255,3 +255,25 @@ def test_packed_rows_met_by_segments(dev, K, E, x_cols, more):  # noqa: F811
     (3001, 4, 264, 520, 64, "f32", 256), (33, 3, 1032, 264, 17, "bf16", 128)])
 def test_packed_rows_beside_8_bit_rows(dev, T, K, D, H, E, dtype, x_cols):  # noqa: F811
     compacted(dev, T, K, D, H, E, dtype, x_cols, T)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("per_sm,E,K", [(0, 64, 8), (25, 128, 8), (50, 256, 8), (100, 128, 3),
+                                        (0, 600, 20)])
+def test_router_weights_of_low_rows(dev, per_sm, E, K, dtype):  # noqa: F811
+    """One choice of a score of 1e-9 to 1e-26, the others 40 to 45 below it: each weight keeps
+    its own accuracy."""
+    T = per_sm * sms() + 100
+    gen = torch.Generator().manual_seed(E)
+    top = -21 - 39 * torch.rand(T, 1, generator=gen)
+    x = top - 40 - 5 * torch.rand(T, E, generator=gen)
+    x.scatter_(1, torch.randint(0, E, (T, 1), generator=gen), top)
+    x = x.to(DT[dtype])
+    r = router(T, E, K, dtype, score="sigmoid", renorm=True)
+    r.route(x.to(dev), stats=False)
+    x64 = to64(x)
+    ids = mo.choose_rows(x64, K)
+    ref = mo.group_route(x64, K, idx=ids)
+    assert np.array_equal(r.topk_idx.cpu().numpy(), ids)
+    lim = (2 * score_tol(x64) + K * U) * ref["alpha"]
+    close(to64(r.alpha), ref["alpha"], lim + TINY, "alpha")
