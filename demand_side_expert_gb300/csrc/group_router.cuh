@@ -68,6 +68,11 @@ __device__ __forceinline__ float rcp_fast(float x) {
   return y;
 }
 
+// Rows whose sigmoids add up to less have all of them taken over exp(m), m the largest logit: a
+// score below 2^-126 is 0 in the fast form, which is then less than 1.2e-29 of the sum. (Less
+// than an eighth of a unit of the keys' grid, so that the keys are the same either way.)
+constexpr float kLowRow = 1e-9f;
+
 // Keeps the larger two of (a, b) and (c, d), a >= b, c >= d.
 template <typename F>
 __device__ __forceinline__ void merge_two(F& a, F& b, F c, F d) {
@@ -679,8 +684,8 @@ group_route_fast_kernel(const T* __restrict__ logits, const RouteArgs a) {
 #pragma unroll
       for (int i = 0; i < NI; ++i) total += s[i] = score_of(x[i]);
       total = group_sum<L>(total);
-      // scores below 32 bits (and rows of none): over exp(m), m the largest logit
-      const bool lost = !(total >= 1e-30f);
+      // low rows (and rows of none): over exp(m), m the largest logit
+      const bool lost = !(total >= kLowRow);
       if (__any_sync(0xffffffffu, lost)) {
         float m = x[0], sum = 0.f;
 #pragma unroll
@@ -807,7 +812,7 @@ group_route_fast_kernel(const T* __restrict__ logits, const RouteArgs a) {
         for (int i = 0; i < NI; ++i) {
           const float bi = a.bias && e0 + i < E ? a.bias[e0 + i] : 0.f;
           const float o = L == 32 ? off[L == 32 ? i : 0] : sm_off[L == 32 ? 0 : e0 + i];
-          // (scores below 32 bits are 0 in units either way)
+          // (low rows' scores are 0 units either way)
           const float unit = fmaf(score_of(x[i]), SOFTMAX ? size : grid.size, o);
           const uint32_t k = (__float_as_uint(unit) << 8) + (255 - e0) - i;
           near |= more && in && x[i] > -CUDART_INF_F && k >= reach && k < last && e0 + i != il &&
@@ -987,8 +992,8 @@ group_route_many_kernel(const T* __restrict__ logits, const RouteArgs a) {
           total += s[i] = rcp_fast(1.f + e);
         }
         total = group_sum<L>(total);
-        // scores below 32 bits (and rows of none): over exp(m), m the largest logit
-        const bool lost = !(total >= 1e-30f);
+        // low rows (and rows of none): over exp(m), m the largest logit
+        const bool lost = !(total >= kLowRow);
         if (__any_sync(0xffffffffu, lost)) {
           float m = x[0], sum = 0.f;
 #pragma unroll
@@ -1355,7 +1360,7 @@ group_route_bwd_kernel(const T* __restrict__ logits, const RouteBwdArgs a, T* dl
     }
     total = group_sum<G>(total);
     cdot = group_sum<G>(cdot);
-    const bool lost = !(total >= 1e-30f);
+    const bool lost = !(total >= kLowRow);
     if (__any_sync(0xffffffffu, lost)) {
       // rows of very low logits, of nothing open, with NaN: over exp(m), m the largest logit
       float top = x[0], sum = 0.f, dot = 0.f;

@@ -257,6 +257,37 @@ def test_packed_rows_beside_8_bit_rows(dev, T, K, D, H, E, dtype, x_cols):  # no
     compacted(dev, T, K, D, H, E, dtype, x_cols, T)
 
 
+@pytest.mark.parametrize("fn", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("per_sm,E,K", [(0, 16, 2), (0, 64, 8), (25, 64, 4), (25, 128, 8),
+                                        (25, 256, 8), (50, 256, 8), (100, 128, 2), (0, 600, 20)])
+def test_router_shares_of_low_rows(dev, per_sm, E, K, dtype, fn):  # noqa: F811
+    """Rows whose largest logit is -21 to -69 and whose others are up to 60 below: every share
+    keeps its own accuracy, in the statistics and in the gradient, however small its score."""
+    T = per_sm * sms() + 100
+    gen = torch.Generator().manual_seed(E)
+    top = -21 - 48 * torch.rand(T, 1, generator=gen)
+    below = 60 * torch.rand(1, E, generator=gen) + 0.5 * torch.rand(T, E, generator=gen)
+    x = (top - below).to(DT[dtype])
+    r = router(T, E, K, dtype, score=fn, balance_coef=1.0)
+    r.route(x.to(dev))
+    x64 = to64(x)
+    kw = dict(fn=fn, balance_coef=1.0)
+    ref = mo.group_route(x64, K, idx=mo.choose_rows(x64, K, fn), **kw)
+    assert np.array_equal(r.topk_idx.cpu().numpy(), ref["topk_idx"])
+    tol = score_tol(x64)
+    close(to64(r.prob_sum), ref["prob_sum"], (tol + (T + 8) * U) * ref["prob_sum"] + TINY,
+          "prob_sum")
+    r.backward(x.to(dev))
+    assert r.device_error() == 0
+    some = np.r_[:60, T - 60:T] if T > 120 else np.arange(T)
+    want = mo.group_route_bwd(x64[some], ref["topk_idx"][some], ref["counts"], None, **kw)
+    cost = E * ref["counts"] / (float(T) * T * K)
+    mag = ref["share"][some] * (cost + ref["share"][some] @ cost[:, None])
+    lim = (4 * tol + (E + 24) * U) * mag + (BF16 * np.abs(want) if dtype == "bf16" else 0)
+    close(to64(r.dlogits)[some], want, lim + TINY, "dlogits")
+
+
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("per_sm,E,K", [(0, 64, 8), (25, 128, 8), (50, 256, 8), (100, 128, 3),
                                         (0, 600, 20)])
