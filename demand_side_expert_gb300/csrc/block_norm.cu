@@ -573,10 +573,11 @@ static lrm_status launch_block(const lrm_block* b, const BlockFwd& a, cudaStream
 template <typename T, typename O>
 static lrm_status pick_block(const lrm_block* b, const BlockFwd& a, cudaStream_t cs) {
   const int D = b->D;
-  // Few elements an SM: as many threads a row as there are units, for a short row's latency
-  // (bfloat16 rows, float32 block, us so | several units a thread: D 1024 T 608 2.9 | 4.5, T 2432
-  // 7.2 | 9.0, past the edge T 4864 11.2 | 15.7, T 19456 33.0 | 36.7, T 58368 91 | 93; D 2048 T 304 3.0 | 3.5, T 1216 7.7 | 6.9, T 29184 95 | 90; D 4096
-  // T 152 3.4 | 3.8, T 608 8.5 | 7.2, T 14592 105 | 92; D 8192 T 304 7.6 | 9.9, T 7296 99 | 98).
+  // Few elements an SM: as many threads a row as it has units (512 at most), for the latency of
+  // one row (bfloat16 rows, float32 block, us so | several units a thread: D 1024 T 608 2.9 | 4.5,
+  // T 2432 7.2 | 9.0, past the edge T 4864 11.2 | 15.7, T 19456 33.0 | 36.7, T 58368 91 | 93;
+  // D 2048 T 304 3.0 | 3.5, T 1216 7.7 | 6.9, T 29184 95 | 90; D 4096 T 152 3.4 | 3.8, T 608
+  // 8.5 | 7.2, T 14592 105 | 92; D 8192 T 304 7.6 | 9.9, T 7296 99 | 98).
   // Rows of 8192 columns that are all float32 would gain by it at any T (T 7296 174 | 198, 0.81
   // and 0.71 of the copy bandwidth; D 6144 182 | 173).
   // Narrow rows have a unit a thread up to 256 columns; of the copy bandwidth, 0.17 to 0.34 GB in
